@@ -373,6 +373,142 @@ mok_status mok_selftest_bounded_wait(void* workspace, size_t ws_bytes, void* str
  * Asynchronous on `stream`; the caller owns `dst`. */
 mok_status mok_fill_zero(void* dst, size_t bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators around the layer in a pre-norm block: the residual addition with
+ * its RMS norm, the router's balance losses, and the dense product with bias,
+ * activation and residual.  They have no counterpart on the pages: additions
+ * of this library, under the conventions above (pointers 16-byte aligned
+ * unless said otherwise, arguments checked before anything is enqueued,
+ * results bitwise the same from call to call).  Row strides are in elements;
+ * 0 stands for contiguous rows. */
+
+/* Element types of their tensors. */
+typedef enum mok_elem { MOK_ELEM_BF16 = 0, MOK_ELEM_F32 = 1 } mok_elem;
+
+typedef struct mok_rmsnorm_desc {
+  int64_t rows, d;       /* 0 <= rows < 2^31, 1 <= d <= 16384 */
+  int64_t ld_x;          /* row stride of x (forward), dy (backward) */
+  int64_t ld_res;        /* of residual (forward), ds (backward) */
+  int64_t ld_s;          /* of s */
+  int64_t ld_y;          /* of y (forward), dx (backward) */
+  float eps;             /* added to the mean square; >= 0 */
+  int32_t x_elem;        /* mok_elem of x (forward), dy (backward) */
+  int32_t s_elem;        /* mok_elem of the residual stream: residual, s, ds, dx */
+  int32_t weight_elem;   /* mok_elem of weight */
+  int32_t accumulate;    /* backward: add into dweight */
+  uint32_t reserved;     /* 0 */
+} mok_rmsnorm_desc;
+
+/* s = x + residual,  y = weight * s / sqrt(mean(s^2) + eps) per row.
+ * x [rows,d]; residual [rows,d] or NULL: then s = x (x_elem must be s_elem)
+ * and the pointer s may be NULL.  s: the sum in fp32, rounded once to s_elem;
+ * the norm reads s as it is stored, so that the backward, which gets the
+ * stored s, differentiates the very function that ran.  s may equal residual
+ * or x (same strides).  Statistics in fp32.
+ * Outputs, each optional but one of y, values, codes needed:
+ *   y       bf16 [rows,d] (stride ld_y): the norm rounded once
+ *   values  bf16 [rows,d] contiguous: the values of its MXFP8 form
+ *   codes, scales  uint8 [rows,d] E4M3 codes and [rows,d/32] E8M0 bytes, both
+ *           or neither: the MXFP8 form by mok_mx_quantize's rule (along rows),
+ *           of the fp32 norm; what mok_gemm_mxfp8 takes
+ * d a multiple of 32 for values and codes.  Any pointer aligned to its
+ * element and any row stride >= d is taken; 16-byte aligned rows with d a
+ * multiple of 8 run at full width. */
+mok_status mok_add_rmsnorm_forward(const mok_rmsnorm_desc* desc, const void* x,
+                                   const void* residual, const void* weight, void* s, void* y,
+                                   void* values, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Backward, from the gradient dy [rows,d] of y and ds [rows,d] (s_elem; NULL:
+ * none) that reaches s by other ways:
+ *   n = s rstd,  g = dy weight,  dx = rstd (g - n mean(g n)) + ds
+ *   dweight [d] fp32 (+)= sum over rows of dy n, in a fixed order
+ * dx [rows,d] (s_elem) is the gradient of x and of residual alike; it may
+ * equal ds.  dweight NULL: not computed.  workspace: see the size query. */
+mok_status mok_add_rmsnorm_backward(const mok_rmsnorm_desc* desc, const void* dy, const void* s,
+                                    const void* weight, const void* ds, void* dx,
+                                    float* dweight, void* workspace, size_t ws_bytes,
+                                    void* stream);
+mok_status mok_add_rmsnorm_workspace_size(const mok_rmsnorm_desc* desc, size_t* bytes);
+
+typedef struct mok_balance_desc {
+  int64_t T;             /* 0 <= T, T*k < 2^30 */
+  int64_t ld_logits;     /* row stride of logits and dlogits */
+  int32_t E, k;          /* 1 <= E <= 512, 1 <= k <= min(E, 8) */
+  float balance_coef, z_coef;
+} mok_balance_desc;
+
+/* The router's auxiliary losses over the N tokens whose mask byte is not 0
+ * (mask uint8 [T] or NULL: all), from fp32 logits [T,E] and the chosen experts
+ * topk_idx int32 [T,k]:
+ *   P_t = softmax(l_t),  c_e = slots of those tokens on expert e
+ *   prob_e = sum_t P_te / N,  f_e = c_e / (N k)
+ *   loss[0] = balance_coef E sum_e f_e prob_e
+ *   loss[1] = z_coef sum_t lse_t^2 / N
+ * Outputs: loss fp32 [2], counts int32 [E], prob fp32 [E], lse fp32 [T] (of
+ * every token), n_valid int32 [1] (= N).  N = 0 gives zero losses.  A logit of
+ * -inf has no probability; a token without a finite logit has lse -inf and
+ * adds to counts and N only.  A NaN or +inf logit is taken as -inf and, in a
+ * token of the mask, sets MOK_ERR_DEVICE_NONFINITE; an index outside [0, E) is
+ * skipped and sets MOK_ERR_DEVICE_INDEX.  Pointers aligned to their elements.
+ * status: device int32 or NULL.  It is sticky: only ever set, by the first
+ * error, and never cleared here; zero it once before its first use. */
+mok_status mok_router_balance_forward(const mok_balance_desc* desc, const float* logits,
+                                      const int32_t* topk_idx, const uint8_t* mask, float* loss,
+                                      int32_t* counts, float* prob, float* lse, int32_t* n_valid,
+                                      void* workspace, size_t ws_bytes, int32_t* status,
+                                      void* stream);
+mok_status mok_router_balance_workspace_size(const mok_balance_desc* desc, size_t* bytes);
+
+/* Gradient of dloss[0] loss[0] + dloss[1] loss[1] (dloss fp32 [2] on the
+ * device) with respect to the logits, the counts held constant, from the
+ * forward's lse, counts and n_valid:
+ *   dlogits_te = P_te (dloss0 balance_coef E (f_e - sum_j f_j P_tj) +
+ *                      dloss1 2 z_coef lse_t) / N,  0 for a masked token
+ * dlogits fp32 [T,E] (stride ld_logits), overwritten; may equal logits. */
+mok_status mok_router_balance_backward(const mok_balance_desc* desc, const float* dloss,
+                                       const float* logits, const float* lse,
+                                       const int32_t* counts, const int32_t* n_valid,
+                                       const uint8_t* mask, float* dlogits, void* stream);
+
+typedef enum mok_act {
+  MOK_ACT_NONE = 0,
+  MOK_ACT_RELU = 1,
+  MOK_ACT_SILU = 2, /* z sigmoid(z) */
+  MOK_ACT_GELU = 3  /* tanh form: z sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)) */
+} mok_act;
+
+typedef struct mok_linear_desc {
+  int64_t M, N, K;       /* 0 <= M, 1 <= N, 8 <= K, K % 8 == 0, each <= 2^24 */
+  int64_t ld_x;          /* row stride of x (a multiple of 8) */
+  int32_t act;           /* mok_act */
+  int32_t y_elem;        /* forward: mok_elem of y, z, residual; backward: of dy, z */
+  int32_t dx_elem;       /* backward: mok_elem of dx */
+  int32_t accumulate;    /* backward: add into dx (fp32 only), dw and dbias */
+} mok_linear_desc;
+
+/* z = x w^T + bias,  y = act(z) + residual, accumulated in fp32 on the tensor
+ * cores and rounded once to y_elem.  x bf16 [M,K] (stride ld_x), w bf16 [N,K],
+ * bias fp32 [N] or NULL, residual [M,N] or NULL (may equal y), y [M,N];
+ * z [M,N] or NULL: the pre-activation, for the backward.  x, w 16-byte
+ * aligned, the others to their elements.  status: as in
+ * mok_router_balance_forward; a bounded wait that gave up sets
+ * MOK_ERR_DEVICE_TIMEOUT. */
+mok_status mok_linear_forward(const mok_linear_desc* desc, const void* x, const void* w,
+                              const float* bias, const void* residual, void* y, void* z,
+                              int32_t* status, void* stream);
+
+/* Backward from dy [M,N] (y_elem):  dz = dy act'(z);
+ *   dx [M,K] (dx_elem) = dz w,  dw fp32 [N,K] = dz^T x,  dbias fp32 [N] =
+ * the column sums of dz, each optional (NULL).  (The gradient of residual is
+ * dy itself.)  z: the forward's, needed unless act is MOK_ACT_NONE.  dz enters
+ * the products as a bf16 hi + lo pair (about 16 significant bits) unless it is
+ * bf16 already (act NONE and dy bf16); fp32 accumulation, fixed order.
+ * x, w, dx, dw 16-byte aligned.  workspace: see the size query. */
+mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, const void* x,
+                               const void* w, const void* z, void* dx, float* dw, float* dbias,
+                               void* workspace, size_t ws_bytes, int32_t* status, void* stream);
+mok_status mok_linear_workspace_size(const mok_linear_desc* desc, size_t* bytes);
+
 /* Waits for `stream`, then reads the device status word at the start of
  * `buf` (the `saved` buffer of forward/backward, or the workspace of the
  * other entry points) into *code (a mok_status; MOK_OK = no device error). */

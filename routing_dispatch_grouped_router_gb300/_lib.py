@@ -30,6 +30,24 @@ class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", c_int32), ("total_ms", ctypes.c_double)]
 
 
+class RmsnormDesc(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("d", c_int64), ("ld_x", c_int64), ("ld_res", c_int64),
+                ("ld_s", c_int64), ("ld_y", c_int64), ("eps", ctypes.c_float),
+                ("x_elem", c_int32), ("s_elem", c_int32), ("weight_elem", c_int32),
+                ("accumulate", c_int32), ("reserved", ctypes.c_uint32)]
+
+
+class BalanceDesc(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("ld_logits", c_int64), ("E", c_int32), ("k", c_int32),
+                ("balance_coef", ctypes.c_float), ("z_coef", ctypes.c_float)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("N", c_int64), ("K", c_int64), ("ld_x", c_int64),
+                ("act", c_int32), ("y_elem", c_int32), ("dx_elem", c_int32),
+                ("accumulate", c_int32)]
+
+
 # name -> (restype, argtypes)
 _SIGS = {
     "mok_moe_workspace_size": (c_int32, [ctypes.POINTER(MoeDesc), ctypes.POINTER(c_size_t),
@@ -62,6 +80,21 @@ _SIGS = {
     "mok_gemm_nvfp4": (c_int32, [c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                  c_void_p]),
+    "mok_add_rmsnorm_forward": (c_int32, [ctypes.POINTER(RmsnormDesc)] + [c_void_p] * 9),
+    "mok_add_rmsnorm_backward": (c_int32, [ctypes.POINTER(RmsnormDesc)] + [c_void_p] * 7
+                                 + [c_size_t, c_void_p]),
+    "mok_add_rmsnorm_workspace_size": (c_int32, [ctypes.POINTER(RmsnormDesc),
+                                                 ctypes.POINTER(c_size_t)]),
+    "mok_router_balance_forward": (c_int32, [ctypes.POINTER(BalanceDesc)] + [c_void_p] * 9
+                                   + [c_size_t, c_void_p, c_void_p]),
+    "mok_router_balance_workspace_size": (c_int32, [ctypes.POINTER(BalanceDesc),
+                                                    ctypes.POINTER(c_size_t)]),
+    "mok_router_balance_backward": (c_int32, [ctypes.POINTER(BalanceDesc)] + [c_void_p] * 8),
+    "mok_linear_forward": (c_int32, [ctypes.POINTER(LinearDesc)] + [c_void_p] * 8),
+    "mok_linear_backward": (c_int32, [ctypes.POINTER(LinearDesc)] + [c_void_p] * 8
+                            + [c_size_t, c_void_p, c_void_p]),
+    "mok_linear_workspace_size": (c_int32, [ctypes.POINTER(LinearDesc),
+                                            ctypes.POINTER(c_size_t)]),
     "mok_selftest_bounded_wait": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_fill_zero": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_get_device_status": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(c_int32)]),

@@ -38,6 +38,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "act.cuh"
 #include "mok_internal.h"
 #include "mx.cuh"
 #include "ptx.cuh"
@@ -53,7 +54,12 @@ enum Epi : int {
   EPI_F32_T = 4,  // KGROUP: fp32 C^T through TMA (the tile is stored transposed)
   EPI_BF16_TMA = 5,  // KGROUP: C rounded to bf16, through TMA
   EPI_BF16_T = 6,    // KGROUP: C^T rounded to bf16, through TMA
+  // DENSE, through TMA: act(C + bias) + residual, and C + bias to its own map
+  // (the dense product with its epilogue, and plain C for its gradients)
+  EPI_LIN_F32 = 7,
+  EPI_LIN_BF16 = 8,
 };
+constexpr bool linear_epi(int epi) { return epi == EPI_LIN_F32 || epi == EPI_LIN_BF16; }
 // Split operands: a bf16 "hi" tile plus a bf16 "lo" tile (value - hi) whose
 // products are accumulated into the same fp32 accumulator, giving the GEMM
 // an operand with ~16 significant bits.
@@ -121,6 +127,12 @@ struct GemmArgs {
   // tile GEMMs read, for output rows nothing reads) get no epilogue: no
   // operand loads, no stores, whole 32-row quarters.
   const int* coff;
+  // EPI_LIN_*: bias fp32 [N] or NULL; residual [M, N] (C's type, row stride
+  // N) or NULL; activation; z stored through the h map
+  const float* bias;
+  const void* res;
+  int act;
+  int store_z;
   int* status;
 };
 
@@ -131,6 +143,7 @@ struct GemmArgs {
 struct OutMaps {
   CUtensorMap dgu_hi, dgu_lo, p_hi, p_lo;
   CUtensorMap sfa, sfb;
+  // (EPI_LIN_*: z, in 32 x 32 blocks as C's)
   // SwiGLU forward with bf16 h: h [rows, I], 32 x 32 blocks of 64-byte rows
   // (64-byte swizzle); a zeroed map (no h, or h as MXFP8 codes) is unused
   CUtensorMap h;
@@ -309,6 +322,8 @@ struct SegWalk {
 template <int SCHED>
 __device__ __forceinline__ int total_pairs(const GemmArgs& a) {
   if (SCHED == SCHED_MGROUP) return __ldg(a.mtile_prefix + 2 * a.E + 1) * a.n_tiles;
+  if (SCHED == SCHED_DENSE)
+    return (a.m_tiles + 1) / 2 * a.n_tiles * (a.k_splits > 1 ? a.k_splits : 1);
   return a.E * (a.m_tiles / 2) * a.n_tiles;
 }
 
@@ -338,6 +353,21 @@ __device__ __forceinline__ Tile decode_pair(const GemmArgs& a, int t, int rank, 
     tl.k_row0 = 0;
     tl.num_kb = a.num_kb;
     tl.kb0 = 0;
+  } else if (SCHED == SCHED_DENSE) {
+    // as decode_tile's; an odd last row tile leaves the pair's second CTA
+    // without rows (its loads are zero-filled)
+    const int mp = (a.m_tiles + 1) / 2;
+    const int mn = mp * a.n_tiles;
+    const int split = t / mn;
+    const int tt = t - split * mn;
+    tl.e = split;
+    tl.n_tile = tt / mp;
+    tl.m_tile = 2 * (tt - tl.n_tile * mp) + rank;
+    tl.row0 = tl.m_tile * 128;
+    tl.k_row0 = 0;
+    tl.num_kb = a.num_kb;
+    tl.kb0 = split * a.num_kb;
+    *valid = tl.m_tile < a.m_tiles;
   } else {
     const int mp = a.m_tiles / 2;
     const int tpe = mp * a.n_tiles;
@@ -657,6 +687,66 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& tl,
         stage_and_store_f32<DBUF>(stage_buf, nst, tmC, v, lane, col0 + c, y, a.accumulate != 0,
                                   a.evict_first != 0);
       }
+    }
+  } else if constexpr (linear_epi(EPI)) {
+    // split s of a split-K product writes its partial at rows s * m_rows
+    const int y = tl.e * a.m_rows + tl.row0 + q * 32;
+    if (tl.row0 + q * 32 >= a.m_valid) return;  // (a partial block is clipped)
+    const int col0 = tl.n_tile * BN + half * HALF_COLS;
+    const long long row = tl.row0 + row_in_tile;
+#pragma unroll 1
+    for (int c = 0; c < HALF_COLS; c += 32) {
+      const int x = col0 + c;
+      if (x >= a.n_valid) break;
+      float v[32];
+      tmem_ld32(taddr + half * HALF_COLS + c, v);
+      if (a.bias) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (x + 4 * j < a.n_valid) {
+            const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + x) + j);
+            v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
+          }
+        }
+      }
+      if (a.store_z) {
+        if (EPI == EPI_LIN_F32) stage_and_store_f32<DBUF>(stage_buf, nst, tmH, v, lane, x, y);
+        else stage_and_store_bf16_rows32(stage_buf, tmH, v, lane, x, y);
+      }
+      if (a.act != MOK_ACT_NONE) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], a.act);
+      }
+      if (a.res && row < a.m_valid) {
+        if (EPI == EPI_LIN_F32) {
+          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.res) +
+                                                            row * a.n_valid + x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (x + 4 * j < a.n_valid) {
+              const float4 b = p[j];
+              v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
+            }
+          }
+        } else {
+          const uint4* p = reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(a.res) + row * a.n_valid + x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (x + 8 * j < a.n_valid) {
+              const uint4 b = p[j];
+              v[8 * j] += bf16lo(b.x); v[8 * j + 1] += bf16hi(b.x);
+              v[8 * j + 2] += bf16lo(b.y); v[8 * j + 3] += bf16hi(b.y);
+              v[8 * j + 4] += bf16lo(b.z); v[8 * j + 5] += bf16hi(b.z);
+              v[8 * j + 6] += bf16lo(b.w); v[8 * j + 7] += bf16hi(b.w);
+            }
+          }
+        }
+      }
+      if (EPI == EPI_LIN_F32)
+        stage_and_store_f32<DBUF>(stage_buf, nst, tmC, v, lane, x, y, a.accumulate != 0);
+      else
+        stage_and_store_bf16_rows32(stage_buf, tmC, v, lane, x, y);
     }
   } else if (EPI == EPI_F32_T || EPI == EPI_BF16_T) {
     // C^T through TMA: accumulator rows are output columns; C viewed as
@@ -1065,7 +1155,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (EPI == EPI_SWIGLU_BWD && PAIR),
                 "DB: double-buffered staging of the fp32 weight gradients, or the SwiGLU "
                 "backward's stores from registers");
-  static_assert(!PAIR || (SCHED != SCHED_DENSE && SPLIT != SPLIT_B && BN == 256), "pair");
+  static_assert(!PAIR || ((SCHED != SCHED_DENSE || linear_epi(EPI)) && SPLIT != SPLIT_B && BN == 256),
+                "pair");
+  static_assert(!linear_epi(EPI) || SCHED == SCHED_DENSE, "the dense product");
   static_assert(SPLIT != SPLIT_MX ||
                     (!A_MN && !B_MN && BN == (PAIR ? 256 : 128) && SCHED == SCHED_MGROUP),
                 "MXFP8 operands: K-major, 128-wide tiles (256 on CTA pairs)");
@@ -1091,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* gu_bar = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF + 256);
   constexpr bool kTmaStore = (EPI == EPI_F32 && SCHED != SCHED_DENSE) || EPI == EPI_SWIGLU_FWD ||
                              EPI == EPI_F32_T || EPI == EPI_SWIGLU_BWD || EPI == EPI_BF16_TMA ||
-                             EPI == EPI_BF16_T;
+                             EPI == EPI_BF16_T || linear_epi(EPI);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1263,6 +1355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // A tile: 128 rows (M) x 64 (K)  (+ its lo tile with SPLIT_A)
           if (!A_MN) {
             load(sA, &tmA, (tl.kb0 + kb) * KX, tl.row0);
+            if (SPLIT == SPLIT_A) load(sA + C::A_BYTES, &tmL, (tl.kb0 + kb) * KX, tl.row0);
           } else {
             const int ky = SCHED == SCHED_KGROUP ? kgy : tl.k_row0 + (tl.kb0 + kb) * 64;
 #pragma unroll
@@ -2274,6 +2367,116 @@ cudaError_t launch_router_logits(const Dims& D, const void* x, const void* w_rou
   if (bn == 256)
     return launch<256, false, false, SCHED_DENSE, EPI_F32>("router_logits", ta, tb, ta, a, mt, st);
   return launch<128, false, false, SCHED_DENSE, EPI_F32>("router_logits", ta, tb, ta, a, mt, st);
+}
+
+// ---------------------------------------------------- the dense product --
+
+// A DENSE launch of the dense product's GEMMs: CTA pairs when C has more than
+// one row tile (a pair's second CTA would have no rows otherwise).
+template <bool A_MN, bool B_MN, int EPI, int SPLIT>
+static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const CUtensorMap& tb,
+                                const CUtensorMap& tc, GemmArgs& a, cudaStream_t st,
+                                const CUtensorMap* tl, const OutMaps* om) {
+  const int splits = a.k_splits > 1 ? a.k_splits : 1;
+  if (a.m_tiles > 1)
+    return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true>(
+        name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
+  return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT>(
+      name, ta, tb, tc, a, a.m_tiles * a.n_tiles * splits, st, tl, om);
+}
+
+// 32 x 32 blocks of C or z, fp32 or bf16
+static bool make_lin_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+                         bool f32) {
+  return f32 ? make_out_map(m, base, cols, rows) : make_out_map_bf16_t(m, base, cols, rows);
+}
+
+cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
+                            const void* w, const float* bias, const void* res, int act, void* y,
+                            void* z, bool f32, int* status, cudaStream_t st) {
+  CUtensorMap ta, tb, tc;
+  const int b_rows = M > 128 ? 128 : 256;  // rows of w one CTA stages
+  if (!make_map(&ta, x, K, M, ld_x, 128) || !make_map(&tb, w, K, N, K, b_rows) ||
+      !make_lin_map(&tc, y, N, M, f32))
+    return cudaErrorInvalidValue;
+  OutMaps om;
+  memset(&om, 0, sizeof(om));
+  if (z && !make_lin_map(&om.h, z, N, M, f32)) return cudaErrorInvalidValue;
+  GemmArgs a = blank_args(status);
+  a.E = 1;
+  a.m_tiles = (int)((M + 127) / 128);
+  a.n_tiles = (int)((N + 255) / 256);
+  a.num_kb = (int)((K + 63) / 64);
+  a.m_valid = (int)M;
+  a.n_valid = (int)N;
+  a.bias = bias;
+  a.res = res;
+  a.act = act;
+  a.store_z = z ? 1 : 0;
+  if (f32)
+    return dense_linear<false, false, EPI_LIN_F32, SPLIT_NONE>("linear", ta, tb, tc, a, st,
+                                                               nullptr, &om);
+  return dense_linear<false, false, EPI_LIN_BF16, SPLIT_NONE>("linear", ta, tb, tc, a, st,
+                                                              nullptr, &om);
+}
+
+cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
+                           const void* dz_lo, const void* w, void* dx, bool f32, bool accumulate,
+                           int* status, cudaStream_t st) {
+  // dx [M, K] = (dz_hi + dz_lo) [M, N] w [N, K]: the reduction runs over N
+  CUtensorMap ta, tl, tb, tc;
+  if (!make_map(&ta, dz_hi, N, M, ld_dz, 128) || !make_map(&tb, w, K, N, K, 64) ||
+      !make_lin_map(&tc, dx, K, M, f32))
+    return cudaErrorInvalidValue;
+  if (dz_lo && !make_map(&tl, dz_lo, N, M, ld_dz, 128)) return cudaErrorInvalidValue;
+  GemmArgs a = blank_args(status);
+  a.E = 1;
+  a.m_tiles = (int)((M + 127) / 128);
+  a.n_tiles = (int)((K + 255) / 256);
+  a.num_kb = (int)((N + 63) / 64);
+  a.m_valid = (int)M;
+  a.n_valid = (int)K;
+  a.accumulate = accumulate ? 1 : 0;
+  if (f32) {
+    if (dz_lo)
+      return dense_linear<false, true, EPI_LIN_F32, SPLIT_A>("linear_dx", ta, tb, tc, a, st, &tl,
+                                                             nullptr);
+    return dense_linear<false, true, EPI_LIN_F32, SPLIT_NONE>("linear_dx", ta, tb, tc, a, st,
+                                                              nullptr, nullptr);
+  }
+  if (dz_lo)
+    return dense_linear<false, true, EPI_LIN_BF16, SPLIT_A>("linear_dx", ta, tb, tc, a, st, &tl,
+                                                            nullptr);
+  return dense_linear<false, true, EPI_LIN_BF16, SPLIT_NONE>("linear_dx", ta, tb, tc, a, st,
+                                                             nullptr, nullptr);
+}
+
+cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
+                           const void* dz_lo, const void* x, int64_t ld_x, float* dw,
+                           bool accumulate, int splits, int* status, cudaStream_t st) {
+  // dw [N, K] = (dz_hi + dz_lo)^T [N x M] x [M, K]: the reduction runs over
+  // the tokens, `splits` partial products at rows s * (N padded to 128) of dw
+  CUtensorMap ta, tl, tb, tc;
+  const int64_t n_pad = (N + 127) / 128 * 128;
+  if (!make_map(&ta, dz_hi, N, M, ld_dz, 64) || !make_map(&tb, x, K, M, ld_x, 64) ||
+      !make_out_map(&tc, dw, K, splits > 1 ? splits * n_pad : N))
+    return cudaErrorInvalidValue;
+  if (dz_lo && !make_map(&tl, dz_lo, N, M, ld_dz, 64)) return cudaErrorInvalidValue;
+  GemmArgs a = blank_args(status);
+  a.E = 1;
+  a.m_tiles = (int)(n_pad / 128);
+  a.n_tiles = (int)((K + 255) / 256);
+  a.k_splits = splits;
+  a.num_kb = (int)(((M + 63) / 64 + splits - 1) / splits);
+  a.m_rows = (int)n_pad;
+  a.m_valid = (int)(splits > 1 ? n_pad : N);
+  a.n_valid = (int)K;
+  a.accumulate = accumulate ? 1 : 0;
+  if (dz_lo)
+    return dense_linear<true, true, EPI_LIN_F32, SPLIT_A>("linear_dw", ta, tb, tc, a, st, &tl,
+                                                          nullptr);
+  return dense_linear<true, true, EPI_LIN_F32, SPLIT_NONE>("linear_dw", ta, tb, tc, a, st,
+                                                           nullptr, nullptr);
 }
 
 cudaError_t gemm_dense_bf16(int64_t M, int64_t N, int64_t K, const void* A, bool a_mn,

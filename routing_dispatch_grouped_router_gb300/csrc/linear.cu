@@ -1,0 +1,519 @@
+// Dense product with bias, activation and residual in its epilogue:
+//   z = x w^T + bias,  y = act(z) + residual
+// on tcgen05, for few tokens and for shapes the persistent engine does not
+// take.
+//
+// The tokens are the narrow operand here: a tile is 128 rows of w (the MMA's
+// M) by BN tokens (its N), so one token costs 16 MMA columns and the ring in
+// shared memory is spent on the weights, whose bytes bound the call.  When the
+// tiles do not fill the GPU, a cluster of up to 8 CTAs splits K: each leaves
+// its fp32 partial in its own shared memory and takes a share of the tokens,
+// which it sums over the cluster in rank order, so the result does not depend
+// on timing.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "act.cuh"
+#include "mok_internal.h"
+#include "ptx.cuh"
+
+namespace mok {
+
+namespace {
+
+constexpr int kLinThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+
+template <int BN>
+struct LinCfg {
+  static constexpr int A_BYTES = 128 * 64 * 2;
+  static constexpr int B_BYTES = BN * 64 * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  // two CTAs per SM up to 64 tokens
+  static constexpr int ROOM = BN <= 64 ? 108 * 1024 : 220 * 1024;
+  static constexpr int STAGES = ROOM / STAGE_BYTES;
+  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
+  static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+  static_assert(BN * 128 * 4 <= BAR_OFF, "the partial sums fit the operand ring");
+  static_assert(SMEM_BYTES <= 232448 && STAGES >= 4 && (2 * STAGES + 2) * 8 + 8 <= 256, "smem");
+};
+
+struct LinArgs {
+  const float* bias;
+  const void* res;
+  void *y, *z;
+  int M, N, nkb, act;
+  int* status;
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// One output element (token m, feature n) from its sum.
+template <bool F32>
+__device__ __forceinline__ void finish(const LinArgs& a, long long m, int n, float v, float bias) {
+  const long long o = m * a.N + n;
+  v += bias;
+  if (F32) {
+    if (a.z) static_cast<float*>(a.z)[o] = v;
+    v = act_value(v, a.act);
+    if (a.res) v += static_cast<const float*>(a.res)[o];
+    static_cast<float*>(a.y)[o] = v;
+  } else {
+    if (a.z) static_cast<__nv_bfloat16*>(a.z)[o] = __float2bfloat16_rn(v);
+    v = act_value(v, a.act);
+    if (a.res) v += __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[o]);
+    static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
+  }
+}
+
+// grid (K splits = the cluster, feature tiles, token tiles)
+template <int BN, bool F32>
+__global__ void __launch_bounds__(kLinThreads)
+    linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                  const LinArgs args) {
+  using C = LinCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* done = empty + C::STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ks = gridDim.x, split = blockIdx.x;
+  const int n0 = blockIdx.y * 128, m0 = blockIdx.z * BN;
+  const int kb0 = static_cast<int>(static_cast<long long>(args.nkb) * split / ks);
+  const int kb1 = static_cast<int>(static_cast<long long>(args.nkb) * (split + 1) / ks);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  volatile int* vabort = abort_flag;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, vabort)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sW = smem + stage * C::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+        tma_load_2d(sW, &tmW, &full[stage], kb * 64, n0);
+        tma_load_2d(sW + C::A_BYTES, &tmX, &full[stage], kb * 64, m0);
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        *vabort = 1;
+        set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
+        // copies already issued land before the CTA can exit: the last fill
+        // of each stage
+        const int zero = 0;
+        for (int s = 0; s < C::STAGES && s < issued; ++s) {
+          const int fills = (issued - 1 - s) / C::STAGES;
+          mbar_wait(&full[s], static_cast<uint32_t>(fills & 1), &zero);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, BN, false, false);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full[stage], phase, vabort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t a_base = smem_addr(smem + stage * C::STAGE_BYTES);
+        const uint32_t b_base = a_base + C::A_BYTES;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_bf16(tmem, smem_desc_sw128(a_base + j * 32, 16, 1024),
+                   smem_desc_sw128(b_base + j * 32, 16, 1024), idesc,
+                   (kb > kb0 || j > 0) ? 1u : 0u);
+        mma_commit(&empty[stage]);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        *vabort = 1;
+        set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
+      }
+      mma_commit(done);
+      const int zero = 0;
+      if (!ok) mbar_wait(done, 0, &zero);
+    }
+  }
+  // every thread waits for the last MMA: the epilogue reads TMEM, and with a
+  // split the partial sums go over the operand ring
+  __syncwarp();
+  const bool good = __all_sync(0xffffffffu, mbar_wait(done, 0, vabort));
+  if (!good) {
+    *vabort = 1;
+    set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
+  }
+  tc_fence_after_sync();
+
+  const int q = warp & 3;  // TMEM lane quarter of an epilogue warp
+  const int f = q * 32 + lane;
+  const int n = n0 + f;
+  if (ks == 1) {
+    if (warp >= 2 && good) {
+      const float bias = args.bias && n < args.N ? args.bias[n] : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 16) {
+        if (m0 + c >= args.M) break;
+        uint32_t r[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (m0 + c + j < args.M && n < args.N)
+            finish<F32>(args, m0 + c + j, n, __uint_as_float(r[j]), bias);
+      }
+    }
+  } else {
+    float* part = reinterpret_cast<float*>(smem);  // [BN tokens][128 features]
+    __syncthreads();  // every warp has seen the last MMA
+    if (warp >= 2) {
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 16) {
+        if (m0 + c >= args.M) break;
+        uint32_t r[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + f] = __uint_as_float(r[j]);
+      }
+    }
+    cluster_sync();
+    if (warp >= 2 && good && n < args.N) {
+      const float bias = args.bias ? args.bias[n] : 0.f;
+      const uint32_t mine = smem_addr(part) + f * 4;
+#pragma unroll 1
+      for (int m = split; m < BN && m0 + m < args.M; m += ks) {
+        float v = 0.f;
+        for (int r = 0; r < ks; ++r)
+          v += ld_cluster_f32(mapa_shared(mine + static_cast<uint32_t>(m) * 512u, r));
+        finish<F32>(args, m0 + m, n, v, bias);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its partial sums
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int BN, bool F32>
+cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, const LinArgs& a,
+                       cudaStream_t st) {
+  using C = LinCfg<BN>;
+  CUtensorMap tw, tx;
+  const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!make_tensor_map_2d(&tw, bf, 2, w, D.K, D.N, D.K, 64, 128, sw) ||
+      !make_tensor_map_2d(&tx, bf, 2, x, D.K, D.M, D.ld_x, 64, BN, sw))
+    return cudaErrorInvalidValue;
+  auto kern = linear_kernel<BN, F32>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t nt = (D.N + 127) / 128, mt = (D.M + BN - 1) / BN;
+  if (nt > 65535 || mt > 65535) return cudaErrorInvalidConfiguration;
+  // K splits: as many as the CTAs that fit at once leave room for, at least
+  // four 64-value blocks each
+  const int64_t slots = static_cast<int64_t>(num_sms_current_device()) * (BN <= 64 ? 2 : 1);
+  int64_t ks = slots / (nt * mt);
+  if (ks > 8) ks = 8;
+  if (ks > a.nkb / 4) ks = a.nkb / 4;
+  if (ks < 1) ks = 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ks), static_cast<unsigned>(nt),
+                     static_cast<unsigned>(mt));
+  cfg.blockDim = dim3(kLinThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ProfScope prof("linear", st);
+  e = cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
+  count_launch();
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w,
+                          const float* bias, const void* res, void* y, void* z, int* status,
+                          cudaStream_t st) {
+  if (D.M == 0) return cudaSuccess;
+  LinArgs a;
+  a.bias = bias; a.res = res; a.y = y; a.z = z;
+  a.M = static_cast<int>(D.M);
+  a.N = static_cast<int>(D.N);
+  a.nkb = static_cast<int>((D.K + 63) / 64);
+  a.act = D.act;
+  a.status = status;
+  const bool f32 = D.y_elem == MOK_ELEM_F32;
+  if (D.M <= 16) return f32 ? run_linear<16, true>(D, x, w, a, st) : run_linear<16, false>(D, x, w, a, st);
+  if (D.M <= 64) return f32 ? run_linear<64, true>(D, x, w, a, st) : run_linear<64, false>(D, x, w, a, st);
+  return f32 ? run_linear<128, true>(D, x, w, a, st) : run_linear<128, false>(D, x, w, a, st);
+}
+
+// ----------------------------------------------------------------- backward --
+
+namespace {
+
+struct DzArgs {
+  const void *dy, *z;
+  __nv_bfloat16 *hi, *lo;  // [M, n_pad], zero past N (NULL: not stored)
+  float* part;             // [ceil(M / kDzRows), N] column sums (NULL: none)
+  long long M;
+  int N, n_pad, act;
+};
+
+constexpr int kDzRows = 64;  // rows of a block: 8 for each of its 8 warps
+
+// dz = dy act'(z) as a bf16 hi + lo pair, and its column sums over the block's
+// rows.  A block takes 256 columns, a lane 8 of them.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
+  __shared__ float s_sum[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + lane * 8;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+  for (int i = 0; i < kDzRows / 8; ++i) {
+    const long long r = static_cast<long long>(blockIdx.y) * kDzRows + i * 8 + warp;
+    if (r >= a.M || c >= a.n_pad) break;
+    float v[8], zz[8];
+    auto load = [&](const void* base, float (&o)[8]) {
+      if (VEC) {
+        if (c >= a.N) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = 0.f;
+        } else if (F32) {
+          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + r * a.N + c);
+          const float4 x = __ldg(p), y = __ldg(p + 1);
+          o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+          o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
+        } else {
+          const uint4 x = ld_global_nc_v4(static_cast<const __nv_bfloat16*>(base) + r * a.N + c);
+          o[0] = bf16lo(x.x); o[1] = bf16hi(x.x); o[2] = bf16lo(x.y); o[3] = bf16hi(x.y);
+          o[4] = bf16lo(x.z); o[5] = bf16hi(x.z); o[6] = bf16lo(x.w); o[7] = bf16hi(x.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j] = 0.f;
+          if (c + j < a.N)
+            o[j] = F32 ? static_cast<const float*>(base)[r * a.N + c + j]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[r * a.N + c + j]);
+        }
+      }
+    };
+    load(a.dy, v);
+    if (a.act != MOK_ACT_NONE) {
+      load(a.z, zz);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < a.N) v[j] *= act_slope(zz[j], a.act);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    if (a.hi) {
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float h0 = bf16_round(v[2 * j]), h1 = bf16_round(v[2 * j + 1]);
+        h[j] = pack_bf16x2(h0, h1);
+        l[j] = pack_bf16x2(v[2 * j] - h0, v[2 * j + 1] - h1);
+      }
+      st_global_v4(a.hi + r * a.n_pad + c, make_uint4(h[0], h[1], h[2], h[3]));
+      if (a.lo) st_global_v4(a.lo + r * a.n_pad + c, make_uint4(l[0], l[1], l[2], l[3]));
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s_sum[warp][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col < a.N) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += s_sum[w][threadIdx.x];
+    a.part[static_cast<long long>(blockIdx.y) * a.N + col] = t;
+  }
+}
+
+// dw[i] (+)= sum over s < n of part[s * stride4 + i], float4s, in order
+__global__ void __launch_bounds__(256) split_sum_kernel(const float4* __restrict__ part, int n,
+                                                        long long stride4, long long n4,
+                                                        float4* dw, int accumulate) {
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n4; i += gridDim.x * 256LL) {
+    float4 v = __ldg(part + i);
+    for (int s = 1; s < n; ++s) {
+      const float4 p = __ldg(part + s * stride4 + i);
+      v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+    }
+    if (accumulate) {
+      const float4 p = dw[i];
+      v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+    }
+    dw[i] = v;
+  }
+}
+
+// K splits of the weight gradient (over the tokens): as many as its tiles
+// leave SMs for, at least eight 64-token blocks each.
+int dw_splits(const mok_linear_desc& D) {
+  const int64_t mt = (D.N + 127) / 128, nt = (D.K + 255) / 256;
+  const int64_t tiles = mt > 1 ? (mt + 1) / 2 * nt : nt;
+  const int64_t slots = mt > 1 ? 76 : 152;  // whatever the device: the sums do not depend on it
+  const int64_t nkb = (D.M + 63) / 64;
+  int64_t ks = slots / tiles;
+  if (ks > nkb / 8) ks = nkb / 8;
+  if (ks < 1) return 1;
+  const int64_t kb = (nkb + ks - 1) / ks;
+  return static_cast<int>((nkb + kb - 1) / kb);  // no empty split
+}
+
+}  // namespace
+
+void linear_layout(const mok_linear_desc& D, LinearWs* W) {
+  auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  W->n_pad = (D.N + 63) / 64 * 64;
+  W->bias_rows = (D.M + kDzRows - 1) / kDzRows;
+  W->dw_splits = dw_splits(D);
+  const size_t dz = static_cast<size_t>(D.M) * W->n_pad * 2;
+  W->dz_hi = 0;
+  W->dz_lo = al(dz);
+  W->part_bias = W->dz_lo + al(dz);
+  W->part_dw = W->part_bias + al(static_cast<size_t>(W->bias_rows) * D.N * 4);
+  const size_t rows = static_cast<size_t>((D.N + 127) / 128 * 128);
+  W->total = W->part_dw + (W->dw_splits > 1 ? al(W->dw_splits * rows * D.K * 4) : 0);
+}
+
+cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const void* x,
+                              const void* w, const void* z, void* dx, float* dw, float* dbias,
+                              void* ws, int* status, cudaStream_t st) {
+  LinearWs W;
+  linear_layout(D, &W);
+  char* b = static_cast<char*>(ws);
+  const bool f32 = D.y_elem == MOK_ELEM_F32;
+  const bool vec = D.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+  // a bf16 dy without an activation is dz already
+  const bool direct = !f32 && D.act == MOK_ACT_NONE && vec;
+  const bool split = f32 || D.act != MOK_ACT_NONE;
+  const bool products = D.M > 0 && (dx || dw);
+  float* part_bias = reinterpret_cast<float*>(b + W.part_bias);
+  if (D.M > 0 && ((products && !direct) || dbias)) {
+    DzArgs a;
+    a.dy = dy;
+    a.z = z;
+    a.hi = products && !direct ? reinterpret_cast<__nv_bfloat16*>(b + W.dz_hi) : nullptr;
+    a.lo = products && split ? reinterpret_cast<__nv_bfloat16*>(b + W.dz_lo) : nullptr;
+    a.part = dbias ? part_bias : nullptr;
+    a.M = D.M;
+    a.N = static_cast<int>(D.N);
+    a.n_pad = static_cast<int>(W.n_pad);
+    a.act = D.act;
+    const dim3 grid(static_cast<unsigned>((W.n_pad + 255) / 256),
+                    static_cast<unsigned>(W.bias_rows));
+    if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
+    ProfScope prof("linear_dz", st);
+    if (f32) {
+      if (vec) linear_dz_kernel<true, true><<<grid, 256, 0, st>>>(a);
+      else linear_dz_kernel<true, false><<<grid, 256, 0, st>>>(a);
+    } else {
+      if (vec) linear_dz_kernel<false, true><<<grid, 256, 0, st>>>(a);
+      else linear_dz_kernel<false, false><<<grid, 256, 0, st>>>(a);
+    }
+    count_launch();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (dbias) {
+    const cudaError_t e = launch_column_sum(part_bias, W.bias_rows, D.N, dbias, D.accumulate != 0, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (D.M == 0) {
+    if (dw && !D.accumulate) return cudaMemsetAsync(dw, 0, static_cast<size_t>(D.N) * D.K * 4, st);
+    return cudaSuccess;
+  }
+  const void* hi = direct ? dy : b + W.dz_hi;
+  const void* lo = split ? b + W.dz_lo : nullptr;
+  const int64_t ld = direct ? D.N : W.n_pad;
+  if (dx) {
+    const cudaError_t e = gemm_linear_dx(D.M, D.N, D.K, ld, hi, lo, w, dx,
+                                         D.dx_elem == MOK_ELEM_F32, D.accumulate != 0, status, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (dw) {
+    float* part = reinterpret_cast<float*>(b + W.part_dw);
+    const bool sum = W.dw_splits > 1;
+    cudaError_t e = gemm_linear_dw(D.M, D.N, D.K, ld, hi, lo, x, D.ld_x, sum ? part : dw,
+                                   !sum && D.accumulate != 0, W.dw_splits, status, st);
+    if (e != cudaSuccess || !sum) return e;
+    const long long n4 = D.N * D.K / 4;
+    const long long stride4 = (D.N + 127) / 128 * 128 * D.K / 4;
+    long long blocks = (n4 + 255) / 256;
+    const long long cap = 8LL * num_sms_current_device();
+    if (blocks > cap) blocks = cap;
+    ProfScope prof("linear_dw_sum", st);
+    split_sum_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
+        reinterpret_cast<const float4*>(part), W.dw_splits, stride4, n4,
+        reinterpret_cast<float4*>(dw), D.accumulate ? 1 : 0);
+    count_launch();
+    return cudaGetLastError();
+  }
+  return cudaSuccess;
+}
+
+}  // namespace mok

@@ -261,6 +261,61 @@ cudaError_t gemm_dense_mxfp8(int64_t M, int64_t N, int64_t K, const uint8_t* A,
 cudaError_t gemm_dense_bf16(int64_t M, int64_t N, int64_t K, const void* A, bool a_mn,
                             const void* B, bool b_mn, void* C, int* status, cudaStream_t st);
 
+// ------------------------------------------- operators around the layer --
+
+// Residual addition with RMS norm (norm.cu); the descriptors' strides filled in.
+cudaError_t launch_add_rmsnorm(const mok_rmsnorm_desc& D, const void* x, const void* res,
+                               const void* w, void* s, void* y, void* values, uint8_t* codes,
+                               uint8_t* scales, cudaStream_t st);
+int64_t norm_bwd_blocks(const mok_rmsnorm_desc& D);  // partial weight gradients [.., d]
+cudaError_t launch_add_rmsnorm_bwd(const mok_rmsnorm_desc& D, const void* dy, const void* s,
+                                   const void* w, const void* ds, void* dx, float* dweight,
+                                   float* part, cudaStream_t st);
+// out[c] (+)= sum over g < n of part[g, c], c < d, in a fixed order
+cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* out,
+                              bool accumulate, cudaStream_t st);
+
+// The router's auxiliary losses (balance.cu).
+struct BalanceWs {
+  size_t arrivals, part_prob, part_cnt, part_z, part_n, total;
+};
+int64_t balance_blocks(const mok_balance_desc& D);
+void balance_layout(const mok_balance_desc& D, BalanceWs* W);
+cudaError_t launch_balance_fwd(const mok_balance_desc& D, const float* logits,
+                               const int32_t* idx, const uint8_t* mask, float* loss,
+                               int32_t* counts, float* prob, float* lse, int32_t* n_valid,
+                               void* ws, int* status, cudaStream_t st);
+cudaError_t launch_balance_bwd(const mok_balance_desc& D, const float* dloss,
+                               const float* logits, const float* lse, const int32_t* counts,
+                               const int32_t* n_valid, const uint8_t* mask, float* dlogits,
+                               cudaStream_t st);
+
+// The dense product (linear.cu) and its GEMMs on the persistent engine (gemm.cu).
+struct LinearWs {
+  size_t dz_hi, dz_lo, part_bias, part_dw, total;
+  int64_t n_pad;      // row length of dz_hi, dz_lo
+  int64_t bias_rows;  // partial bias gradients
+  int dw_splits;      // partial weight gradients (1: none)
+};
+void linear_layout(const mok_linear_desc& D, LinearWs* W);
+cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w,
+                          const float* bias, const void* res, void* y, void* z, int* status,
+                          cudaStream_t st);
+cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const void* x,
+                              const void* w, const void* z, void* dx, float* dw, float* dbias,
+                              void* ws, int* status, cudaStream_t st);
+// y, res, z, bias 16-byte aligned, N a multiple of 8
+cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
+                            const void* w, const float* bias, const void* res, int act, void* y,
+                            void* z, bool f32, int* status, cudaStream_t st);
+// dz as a bf16 tensor with row stride ld_dz (a multiple of 8); dz_lo may be null
+cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
+                           const void* dz_lo, const void* w, void* dx, bool f32, bool accumulate,
+                           int* status, cudaStream_t st);
+cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
+                           const void* dz_lo, const void* x, int64_t ld_x, float* dw,
+                           bool accumulate, int splits, int* status, cudaStream_t st);
+
 // MXFP8 fake quantisation (mx.cu): rows = blocks along each row, cols =
 // blocks of 32 rows; codes/scales may be null.
 // tiled: scales in the tiled layout of mx_tiled_off (rows, cols multiples of

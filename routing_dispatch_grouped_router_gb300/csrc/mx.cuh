@@ -38,6 +38,15 @@ __device__ __forceinline__ float exp2i(int n) {
   return n >= -126 ? __int_as_float((n + 127) << 23) : __int_as_float(1 << (n + 149));
 }
 
+// Shared exponent of a block whose largest magnitude is amax.
+__device__ __forceinline__ int mx_shared_exp(float amax) {
+  if (!(amax > 0.f)) return -127;
+  int e;
+  frexpf(amax, &e);  // amax = m * 2^e with 0.5 <= m < 1
+  const int shared = e - 1 - 8;
+  return shared < -127 ? -127 : (shared > 127 ? 127 : shared);
+}
+
 // In-place MXFP8 fake quantisation of one 32-value block.  shared lies in
 // [-127, 119] for finite input (floor(log2 of the largest finite fp32) - 8 =
 // 119), so both scale factors are fp32 powers of two.

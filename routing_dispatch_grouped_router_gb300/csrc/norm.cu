@@ -1,0 +1,515 @@
+// Residual addition with RMS norm, forward (bf16 and MXFP8 out) and backward.
+//
+//   s = x + r (rounded once to the stream's type),  y = w s rstd,
+//   rstd = 1 / sqrt(mean(s^2) + eps)
+//   backward: n = s rstd, g = dy w:  dx = rstd (g - n mean(g n)) + ds,
+//   dw = sum over rows of dy n
+//
+// Bound by HBM bytes: a row is read once, kept in registers across the row
+// reductions and written once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "mok_internal.h"
+#include "mx.cuh"
+#include "ptx.cuh"
+
+namespace mok {
+
+namespace {
+
+// Eight elements of a row held by one thread.  The rows' vectors v = 0 ..
+// ceil(d/8)-1 go round the threads of the row.  VEC: vector v is elements
+// 8v .. 8v+7 (one or two 16-byte accesses; 16-byte aligned rows, d a multiple
+// of 8).  Otherwise element j of vector v is 256 (v / 32) + 32 j + v % 32, so
+// that a warp's element accesses are consecutive whatever the alignment.
+template <bool VEC>
+__device__ __forceinline__ int elem_of(int v, int j) {
+  return VEC ? 8 * v + j : 256 * (v >> 5) + 32 * j + (v & 31);
+}
+
+// A vector as it lies in memory (aligned bf16 stays packed), so that all of a
+// row's loads can be in flight before the first is used.  Plain loads: the
+// outputs may be the same memory as inputs.
+template <bool F32, bool VEC>
+struct Raw8 {
+  float f[8];
+  __device__ __forceinline__ void load(const void* row, int v, int d) {
+    if (VEC) {
+      const float4* p = reinterpret_cast<const float4*>(row) + 2 * v;
+      const float4 a = p[0], b = p[1];
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = elem_of<false>(v, j);
+        f[j] = 0.f;
+        if (i < d)
+          f[j] = F32 ? static_cast<const float*>(row)[i]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.f;
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = f[j];
+  }
+};
+template <>
+struct Raw8<false, true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* row, int v, int) {
+    u = reinterpret_cast<const uint4*>(row)[v];
+  }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    o[0] = bf16lo(u.x); o[1] = bf16hi(u.x); o[2] = bf16lo(u.y); o[3] = bf16hi(u.y);
+    o[4] = bf16lo(u.z); o[5] = bf16hi(u.z); o[6] = bf16lo(u.w); o[7] = bf16hi(u.w);
+  }
+};
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load8(const void* row, int v, int d, float (&o)[8]) {
+  Raw8<F32, VEC> r;
+  r.load(row, v, d);
+  r.get(o);
+}
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store8(void* row, int v, int d, const float (&o)[8]) {
+  if (VEC) {
+    if (F32) {
+      float4* p = reinterpret_cast<float4*>(row) + 2 * v;
+      p[0] = make_float4(o[0], o[1], o[2], o[3]);
+      p[1] = make_float4(o[4], o[5], o[6], o[7]);
+    } else {
+      reinterpret_cast<uint4*>(row)[v] =
+          make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                     pack_bf16x2(o[6], o[7]));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = elem_of<false>(v, j);
+      if (i < d) {
+        if (F32) static_cast<float*>(row)[i] = o[j];
+        else static_cast<__nv_bfloat16*>(row)[i] = __float2bfloat16_rn(o[j]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Row `r` of an array with row stride ld, F32 or bf16 elements.
+template <bool F32>
+__device__ __forceinline__ const void* row_at(const void* base, long long r, long long ld) {
+  return static_cast<const char*>(base) + r * ld * (F32 ? 4 : 2);
+}
+template <bool F32>
+__device__ __forceinline__ void* row_at(void* base, long long r, long long ld) {
+  return static_cast<char*>(base) + r * ld * (F32 ? 4 : 2);
+}
+
+}  // namespace
+
+struct NormFwd {
+  const void *x, *r, *w;
+  void *s, *y, *values;
+  uint8_t *codes, *scales;
+  long long rows, ld_x, ld_r, ld_s, ld_y;
+  int d, nvec, w_f32;
+  float inv_d, eps;
+};
+
+// MXFP8 of the vector's elements: the block's 32 columns are 4 threads'
+// vectors (VEC) or one element of each lane of the warp.
+template <bool VEC>
+__device__ __forceinline__ void mx_store(const NormFwd& a, long long r, int v, bool in,
+                                         const float (&n)[8]) {
+  if (VEC) {
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(n[j]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    if (!in) return;
+    const int shared = mx_shared_exp(amax);
+    const float down = exp2i(-shared), up = exp2i(shared);
+    uint32_t w[2];
+    float q[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint16_t p01 = cvt_e4m3x2(n[4 * h + 1] * down, n[4 * h] * down);
+      const uint16_t p23 = cvt_e4m3x2(n[4 * h + 3] * down, n[4 * h + 2] * down);
+      w[h] = static_cast<uint32_t>(p01) | (static_cast<uint32_t>(p23) << 16);
+      e4m3x2_to_f32(p01, &q[4 * h + 1], &q[4 * h]);
+      e4m3x2_to_f32(p23, &q[4 * h + 3], &q[4 * h + 2]);
+    }
+    if (a.codes) {
+      *reinterpret_cast<uint2*>(a.codes + r * a.d + 8 * v) = make_uint2(w[0], w[1]);
+      if ((v & 3) == 0)
+        a.scales[r * (a.d >> 5) + (v >> 2)] = static_cast<uint8_t>(shared + 127);
+    }
+    if (a.values) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] *= up;
+      store8<false, true>(static_cast<__nv_bfloat16*>(a.values) + r * a.d, v, a.d, q);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float amax = fabsf(n[j]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int i = elem_of<false>(v, j);
+      if (!in || i >= a.d) continue;
+      const int shared = mx_shared_exp(amax);
+      const uint16_t p = cvt_e4m3x2(0.f, n[j] * exp2i(-shared));
+      if (a.codes) {
+        a.codes[r * a.d + i] = static_cast<uint8_t>(p & 0xFFu);
+        if ((i & 31) == 0) a.scales[r * (a.d >> 5) + (i >> 5)] = static_cast<uint8_t>(shared + 127);
+      }
+      if (a.values) {
+        float hi, lo;
+        e4m3x2_to_f32(p, &hi, &lo);
+        static_cast<__nv_bfloat16*>(a.values)[r * a.d + i] = __float2bfloat16_rn(lo * exp2i(shared));
+      }
+    }
+  }
+}
+
+// One row per threadIdx.y; blockDim.x threads of whole warps hold it, NV
+// vectors each.
+template <bool XF32, bool SF32, bool VEC, int NV, bool MX>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormFwd a) {
+  __shared__ float red[32];
+  const int t = threadIdx.x, tpr = blockDim.x;
+  const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool row_in = r < a.rows;
+  Raw8<XF32, VEC> x[NV];
+  Raw8<SF32, VEC> res[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vi = t + i * tpr;
+    x[i].zero();
+    res[i].zero();
+    if (row_in && vi < a.nvec) {
+      x[i].load(row_at<XF32>(a.x, r, a.ld_x), vi, a.d);
+      if (a.r) res[i].load(row_at<SF32>(a.r, r, a.ld_r), vi, a.d);
+    }
+  }
+  float v[NV][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vi = t + i * tpr;
+    x[i].get(v[i]);
+    if (a.r) {
+      float b[8];
+      res[i].get(b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] += b[j];
+        if (!SF32) v[i][j] = bf16_round(v[i][j]);
+      }
+    }
+    if (a.s && row_in && vi < a.nvec)
+      store8<SF32, VEC>(row_at<SF32>(a.s, r, a.ld_s), vi, a.d, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+  }
+  sum = warp_sum(sum);
+  if (tpr > 32) {  // one row per block
+    if ((t & 31) == 0) red[t >> 5] = sum;
+    __syncthreads();
+    sum = (t & 31) < (tpr >> 5) ? red[t & 31] : 0.f;
+    sum = warp_sum(sum);
+  }
+  const float rstd = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vi = t + i * tpr;
+    const bool in = row_in && vi < a.nvec;
+    if (!MX && !in) continue;
+    float w[8];
+    if (in) {
+      if (a.w_f32) load8<true, VEC>(a.w, vi, a.d, w);
+      else load8<false, VEC>(a.w, vi, a.d, w);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = in ? v[i][j] * rstd * w[j] : 0.f;
+    if (in && a.y) store8<false, VEC>(row_at<false>(a.y, r, a.ld_y), vi, a.d, v[i]);
+    if (MX) mx_store<VEC>(a, r, vi, in, v[i]);
+  }
+}
+
+namespace {
+
+// Threads of a row (a multiple of 32) and vectors per thread (1, 2 or 4; at
+// most 1024 threads of one vector, 512 of more).  Few rows: one vector per
+// thread where that fits, so that a row's loads are all in flight at once.
+// Many rows: up to max_nv, so that several rows share an SM.
+void norm_shape(long long rows, int nvec, int max_nv, int* tpr, int* nv) {
+  int n = rows >= 4LL * num_sms_current_device() ? max_nv : 1;
+  if (nvec > 1024) n = 4;
+  while (n > 1 && nvec <= 32 * (n / 2)) n /= 2;
+  const int th = (nvec + n - 1) / n;
+  *tpr = (th + 31) / 32 * 32;
+  *nv = n;
+}
+
+bool vec_rows(const void* p, long long ld, int esz) {
+  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * esz % 16 == 0);
+}
+
+template <bool XF32, bool SF32, bool VEC, bool MX>
+cudaError_t fwd_launch(const NormFwd& a, cudaStream_t st) {
+  int tpr, nv;
+  norm_shape(a.rows, a.nvec, 4, &tpr, &nv);
+  const int rpb = tpr == 32 ? 4 : 1;
+  const dim3 block(tpr, rpb);
+  const unsigned grid = static_cast<unsigned>((a.rows + rpb - 1) / rpb);
+  ProfScope prof("add_rmsnorm", st);
+  if (nv == 1) add_rmsnorm_kernel<XF32, SF32, VEC, 1, MX><<<grid, block, 0, st>>>(a);
+  else if (nv == 2) add_rmsnorm_kernel<XF32, SF32, VEC, 2, MX><<<grid, block, 0, st>>>(a);
+  else add_rmsnorm_kernel<XF32, SF32, VEC, 4, MX><<<grid, block, 0, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <bool XF32, bool SF32>
+cudaError_t fwd_pick(const NormFwd& a, bool vec, bool mx, cudaStream_t st) {
+  if (vec) return mx ? fwd_launch<XF32, SF32, true, true>(a, st)
+                     : fwd_launch<XF32, SF32, true, false>(a, st);
+  return mx ? fwd_launch<XF32, SF32, false, true>(a, st)
+            : fwd_launch<XF32, SF32, false, false>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const mok_rmsnorm_desc& D, const void* x, const void* res,
+                               const void* w, void* s, void* y, void* values, uint8_t* codes,
+                               uint8_t* scales, cudaStream_t st) {
+  if (D.rows == 0) return cudaSuccess;
+  const bool xf = D.x_elem == MOK_ELEM_F32, sf = D.s_elem == MOK_ELEM_F32;
+  NormFwd a;
+  a.x = x; a.r = res; a.w = w; a.s = s; a.y = y; a.values = values;
+  a.codes = codes; a.scales = scales;
+  a.rows = D.rows;
+  a.ld_x = D.ld_x; a.ld_r = D.ld_res; a.ld_s = D.ld_s; a.ld_y = D.ld_y;
+  a.d = static_cast<int>(D.d);
+  a.nvec = (a.d + 7) / 8;
+  a.w_f32 = D.weight_elem == MOK_ELEM_F32;
+  a.inv_d = 1.0f / static_cast<float>(a.d);
+  a.eps = D.eps;
+  const int xe = xf ? 4 : 2, se = sf ? 4 : 2;
+  const bool vec = a.d % 8 == 0 && vec_rows(x, a.ld_x, xe) && vec_rows(res, a.ld_r, se) &&
+                   vec_rows(s, a.ld_s, se) && vec_rows(y, a.ld_y, 2) && vec_rows(w, 0, 4) &&
+                   vec_rows(values, a.d, 2) && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
+  if (!vec) a.nvec = (a.d + 255) / 256 * 32;  // whole groups of 256 elements
+  const bool mx = values || codes;
+  if (xf) return sf ? fwd_pick<true, true>(a, vec, mx, st) : fwd_pick<true, false>(a, vec, mx, st);
+  return sf ? fwd_pick<false, true>(a, vec, mx, st) : fwd_pick<false, false>(a, vec, mx, st);
+}
+
+// ----------------------------------------------------------------- backward --
+
+struct NormBwd {
+  const void *dy, *s, *w, *ds;
+  void* dx;
+  float* part;  // [gridDim.x, d] partial weight gradients (NULL: not computed)
+  long long rows, ld_dy, ld_s, ld_ds, ld_dx;
+  int d, nvec, w_f32;
+  float inv_d, eps;
+};
+
+// Block b takes rows b, b + gridDim.x, ..; its threads keep the weight
+// gradient of their columns in registers over those rows.
+template <bool DYF32, bool SF32, bool VEC, int NV>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_bwd_kernel(NormBwd a) {
+  __shared__ float red[2][2][32];  // [row parity][sum][warp]
+  const int t = threadIdx.x, tpr = blockDim.x, nw = tpr >> 5;
+  float dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  int par = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, par ^= 1) {
+    Raw8<SF32, VEC> rs[NV], rd[NV];
+    Raw8<DYF32, VEC> ry[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vi = t + i * tpr;
+      rs[i].zero();
+      ry[i].zero();
+      rd[i].zero();
+      if (vi < a.nvec) {
+        rs[i].load(row_at<SF32>(a.s, r, a.ld_s), vi, a.d);
+        ry[i].load(row_at<DYF32>(a.dy, r, a.ld_dy), vi, a.d);
+        if (a.ds) rd[i].load(row_at<SF32>(a.ds, r, a.ld_ds), vi, a.d);
+      }
+    }
+    float ss = 0.f, gs = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vi = t + i * tpr;
+      if (vi < a.nvec) {
+        float w[8], s[8], dy[8];
+        if (a.w_f32) load8<true, VEC>(a.w, vi, a.d, w);
+        else load8<false, VEC>(a.w, vi, a.d, w);
+        rs[i].get(s);
+        ry[i].get(dy);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ss = fmaf(s[j], s[j], ss);
+          gs = fmaf(dy[j] * w[j], s[j], gs);
+        }
+      }
+    }
+    ss = warp_sum(ss);
+    gs = warp_sum(gs);
+    if (nw > 1) {
+      if ((t & 31) == 0) {
+        red[par][0][t >> 5] = ss;
+        red[par][1][t >> 5] = gs;
+      }
+      __syncthreads();  // (the other parity's buffer may still be read)
+      const bool in = (t & 31) < nw;
+      ss = warp_sum(in ? red[par][0][t & 31] : 0.f);
+      gs = warp_sum(in ? red[par][1][t & 31] : 0.f);
+    }
+    const float rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+    const float c = gs * rstd * rstd * a.inv_d;  // rstd mean(g n) = c; n c = s rstd c
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vi = t + i * tpr;
+      if (vi >= a.nvec) continue;
+      float w[8], s[8], dy[8], o[8];
+      if (a.w_f32) load8<true, VEC>(a.w, vi, a.d, w);
+      else load8<false, VEC>(a.w, vi, a.d, w);
+      rs[i].get(s);
+      ry[i].get(dy);
+      rd[i].get(o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[j] = rstd * (dy[j] * w[j] - s[j] * c) + o[j];
+        dw[i][j] = fmaf(dy[j], s[j] * rstd, dw[i][j]);
+      }
+      store8<SF32, VEC>(row_at<SF32>(a.dx, r, a.ld_dx), vi, a.d, o);
+    }
+  }
+  if (!a.part) return;
+  float* p = a.part + static_cast<long long>(blockIdx.x) * a.d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vi = t + i * tpr;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = elem_of<VEC>(vi, j);
+      if (vi < a.nvec && e < a.d) p[e] = dw[i][j];
+    }
+  }
+}
+
+// out[c] (+)= sum over g < n of part[g, c]: 32 columns per block, 8 threads of
+// each column take every eighth partial, then their sums in order.
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part,
+                                                         long long n, int d, float* out,
+                                                         int accumulate) {
+  __shared__ float s[8][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float acc = 0.f;
+  if (c < d) {
+#pragma unroll 8
+    for (long long g = threadIdx.y; g < n; g += 8) acc += part[g * d + c];
+  }
+  s[threadIdx.y][threadIdx.x] = acc;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < d) {
+    float v = accumulate ? out[c] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v += s[j][threadIdx.x];
+    out[c] = v;
+  }
+}
+
+cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* out,
+                              bool accumulate, cudaStream_t st) {
+  ProfScope prof("column_sum", st);
+  column_sum_kernel<<<static_cast<unsigned>((d + 31) / 32), dim3(32, 8), 0, st>>>(
+      part, n, static_cast<int>(d), out, accumulate ? 1 : 0);
+  count_launch();
+  return cudaGetLastError();
+}
+
+namespace {
+
+template <bool DYF32, bool SF32, bool VEC>
+cudaError_t bwd_launch(const NormBwd& a, int64_t grid, cudaStream_t st) {
+  int tpr, nv;
+  norm_shape(a.rows, a.nvec, 2, &tpr, &nv);
+  ProfScope prof("add_rmsnorm_bwd", st);
+  const unsigned g = static_cast<unsigned>(grid);
+  if (nv == 1) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 1><<<g, tpr, 0, st>>>(a);
+  else if (nv == 2) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 2><<<g, tpr, 0, st>>>(a);
+  else add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 4><<<g, tpr, 0, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_bwd_blocks(const mok_rmsnorm_desc& D) {
+  const int64_t most = 4 * 152;  // whatever the device, so that the sums do not depend on it
+  return D.rows < most ? D.rows : most;
+}
+
+cudaError_t launch_add_rmsnorm_bwd(const mok_rmsnorm_desc& D, const void* dy, const void* s,
+                                   const void* w, const void* ds, void* dx, float* dweight,
+                                   float* part, cudaStream_t st) {
+  const bool yf = D.x_elem == MOK_ELEM_F32, sf = D.s_elem == MOK_ELEM_F32;
+  const int64_t grid = norm_bwd_blocks(D);
+  cudaError_t e = cudaSuccess;
+  if (grid > 0) {
+    NormBwd a;
+    a.dy = dy; a.s = s; a.w = w; a.ds = ds; a.dx = dx;
+    a.part = dweight ? part : nullptr;
+    a.rows = D.rows;
+    a.ld_dy = D.ld_x; a.ld_s = D.ld_s; a.ld_ds = D.ld_res; a.ld_dx = D.ld_y;
+    a.d = static_cast<int>(D.d);
+    a.nvec = (a.d + 7) / 8;
+    a.w_f32 = D.weight_elem == MOK_ELEM_F32;
+    a.inv_d = 1.0f / static_cast<float>(a.d);
+    a.eps = D.eps;
+    const int ye = yf ? 4 : 2, se = sf ? 4 : 2;
+    const bool vec = a.d % 8 == 0 && vec_rows(dy, a.ld_dy, ye) && vec_rows(s, a.ld_s, se) &&
+                     vec_rows(ds, a.ld_ds, se) && vec_rows(dx, a.ld_dx, se) && vec_rows(w, 0, 4);
+    if (!vec) a.nvec = (a.d + 255) / 256 * 32;
+    if (yf) {
+      if (sf) e = vec ? bwd_launch<true, true, true>(a, grid, st)
+                      : bwd_launch<true, true, false>(a, grid, st);
+      else e = vec ? bwd_launch<true, false, true>(a, grid, st)
+                   : bwd_launch<true, false, false>(a, grid, st);
+    } else {
+      if (sf) e = vec ? bwd_launch<false, true, true>(a, grid, st)
+                      : bwd_launch<false, true, false>(a, grid, st);
+      else e = vec ? bwd_launch<false, false, true>(a, grid, st)
+                   : bwd_launch<false, false, false>(a, grid, st);
+    }
+  }
+  if (e != cudaSuccess || !dweight) return e;
+  return launch_column_sum(part, grid, D.d, dweight, D.accumulate != 0, st);
+}
+
+}  // namespace mok
