@@ -501,8 +501,9 @@ mok_status mok_linear_forward(const mok_linear_desc* desc, const void* x, const 
  *   dx [M,K] (dx_elem) = dz w,  dw fp32 [N,K] = dz^T x,  dbias fp32 [N] =
  * the column sums of dz, each optional (NULL).  (The gradient of residual is
  * dy itself.)  z: the forward's, needed unless act is MOK_ACT_NONE.  dz enters
- * the products as a bf16 hi + lo pair (about 16 significant bits) unless it is
- * bf16 already (act NONE and dy bf16); fp32 accumulation, fixed order.
+ * the products as the sum of bf16 parts, three (all 24 bits) for an fp32
+ * result and two for a bf16 dx, unless it is bf16 itself (act NONE and dy
+ * bf16); fp32 accumulation, fixed order.
  * x, w, dx, dw 16-byte aligned.  workspace: see the size query. */
 mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, const void* x,
                                const void* w, const void* z, void* dx, float* dw, float* dbias,

@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(BalArgs a, int
     }
     s_nall = nn;
     a.n_valid[0] = nn;
-    a.loss[1] = nn > 0 ? a.z_coef * zz / static_cast<float>(nn) : 0.f;
+    // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
+    a.loss[1] = nn > 0 && a.z_coef != 0.f ? a.z_coef * zz / static_cast<float>(nn) : 0.f;
   }
   __syncthreads();
   const float inv_n = s_nall > 0 ? 1.0f / static_cast<float>(s_nall) : 0.f;

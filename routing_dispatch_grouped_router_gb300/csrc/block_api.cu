@@ -68,9 +68,9 @@ mok_status mok_add_rmsnorm_forward(const mok_rmsnorm_desc* desc, const void* x,
   mok_rmsnorm_desc D;
   mok_status st = norm_desc(desc, &D);
   if (st != MOK_OK) return st;
-  if (!weight || (!y && !values && !codes) || (codes == nullptr) != (scales == nullptr))
+  if (!weight || (codes == nullptr) != (scales == nullptr)) return MOK_ERR_INVALID_ARG;
+  if (D.rows > 0 && (!x || (residual && !s) || (!y && !values && !codes)))
     return MOK_ERR_INVALID_ARG;
-  if (D.rows > 0 && (!x || (residual && !s))) return MOK_ERR_INVALID_ARG;
   if (!residual && D.x_elem != D.s_elem) return MOK_ERR_UNSUPPORTED;
   if ((values || codes) && D.d % 32) return MOK_ERR_UNSUPPORTED;
   const size_t se = elem_size(D.s_elem);

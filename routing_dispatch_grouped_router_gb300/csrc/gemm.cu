@@ -71,7 +71,15 @@ constexpr bool linear_epi(int epi) { return epi == EPI_LIN_F32 || epi == EPI_LIN
 // 16 K values, multiplied by tcgen05.mma.kind::mxf4nvf4.block_scale
 // (scale_vec::4X); the tensor scales of A and B multiply the accumulator in
 // the epilogue.
-enum Split : int { SPLIT_NONE = 0, SPLIT_A = 1, SPLIT_B = 2, SPLIT_MX = 3, SPLIT_NV = 4 };
+// SPLIT_A3: A as three bf16 parts (all 24 bits of an fp32 operand).
+enum Split : int {
+  SPLIT_NONE = 0,
+  SPLIT_A = 1,
+  SPLIT_B = 2,
+  SPLIT_MX = 3,
+  SPLIT_NV = 4,
+  SPLIT_A3 = 5
+};
 constexpr bool block_scaled(int split) { return split == SPLIT_MX || split == SPLIT_NV; }
 
 struct GemmArgs {
@@ -142,6 +150,7 @@ struct GemmArgs {
 // bytes, one 512-byte block = 2 rows.
 struct OutMaps {
   CUtensorMap dgu_hi, dgu_lo, p_hi, p_lo;
+  // (SPLIT_A3: sfa is the third part of A, tmL the second)
   CUtensorMap sfa, sfb;
   // (EPI_LIN_*: z, in 32 x 32 blocks as C's)
   // SwiGLU forward with bf16 h: h [rows, I], 32 x 32 blocks of 64-byte rows
@@ -197,7 +206,7 @@ struct Cfg {
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of B staged by one CTA
   static constexpr int A_BYTES = BM * BK * 2;        // 16 KB
   static constexpr int B_BYTES = B_ROWS * BK * 2;    // 32 KB (BN=256) / 16 KB (BN=128 or PAIR)
-  static constexpr int A_TILES = SPLIT == SPLIT_A ? 2 : 1;
+  static constexpr int A_TILES = SPLIT == SPLIT_A3 ? 3 : (SPLIT == SPLIT_A ? 2 : 1);
   static constexpr int B_TILES = SPLIT == SPLIT_B ? 2 : 1;
   static constexpr int B_OFF = A_TILES * A_BYTES;  // B tile(s) follow the A tile(s)
   // SPLIT_MX: 128-row x 128-byte code tiles (the bf16 tile sizes) and the two
@@ -250,6 +259,8 @@ static_assert(Cfg<256, SPLIT_MX, true>::STAGES == 5 &&
                   Cfg<256, SPLIT_MX, true>::STAGE_BYTES % 1024 == 0 &&
                   256 + 12 * Cfg<256, SPLIT_MX, true>::STAGES <= 512,
               "MXFP8 pair stages");
+static_assert(Cfg<256, SPLIT_A3, true>::STAGES == 3 && Cfg<128, SPLIT_A3>::STAGES == 3,
+              "three-part stages");
 static_assert(Cfg<256, SPLIT_NONE, true, 2 * kStagingBytes>::STAGES == 5 &&
                   Cfg<256, SPLIT_NONE, false, 2 * kStagingBytes>::STAGES == 3 &&
                   Cfg<128, SPLIT_NONE, false, 2 * kStagingBytes>::STAGES == 5,
@@ -1213,6 +1224,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
     if (kTmaStore) tma_prefetch_desc(&tmC);
+    if (SPLIT == SPLIT_A3) tma_prefetch_desc(&om.sfa);
+    if (linear_epi(EPI) && args.store_z) tma_prefetch_desc(&om.h);
     if (block_scaled(SPLIT) && PAIR) {
       tma_prefetch_desc(&om.sfa);
       tma_prefetch_desc(&om.sfb);
@@ -1355,13 +1368,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // A tile: 128 rows (M) x 64 (K)  (+ its lo tile with SPLIT_A)
           if (!A_MN) {
             load(sA, &tmA, (tl.kb0 + kb) * KX, tl.row0);
-            if (SPLIT == SPLIT_A) load(sA + C::A_BYTES, &tmL, (tl.kb0 + kb) * KX, tl.row0);
+            if (C::A_TILES > 1) load(sA + C::A_BYTES, &tmL, (tl.kb0 + kb) * KX, tl.row0);
+            if (C::A_TILES > 2) load(sA + 2 * C::A_BYTES, &om.sfa, (tl.kb0 + kb) * KX, tl.row0);
           } else {
             const int ky = SCHED == SCHED_KGROUP ? kgy : tl.k_row0 + (tl.kb0 + kb) * 64;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               load(sA + j * 8192, &tmA, tl.row0 + 64 * j, ky);
-              if (SPLIT == SPLIT_A) load(sA + C::A_BYTES + j * 8192, &tmL, tl.row0 + 64 * j, ky);
+              if (C::A_TILES > 1)
+                load(sA + C::A_BYTES + j * 8192, &tmL, tl.row0 + 64 * j, ky);
+              if (C::A_TILES > 2)
+                load(sA + 2 * C::A_BYTES + j * 8192, &om.sfa, tl.row0 + 64 * j, ky);
             }
           }
           // B tile: B_ROWS rows (N) x 64 (K); PAIR: this CTA's half of N
@@ -1502,10 +1519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t ad = smem_desc_sw128(a_base + j * kstep_a, lbo_a, 1024);
               const uint64_t bd = smem_desc_sw128(b_base + j * kstep_b, lbo_b, 1024);
               mma(d_tmem, ad, bd, (kb | j) != 0 ? 1u : 0u);
-              if (SPLIT == SPLIT_A) {
-                const uint64_t ad2 =
-                    smem_desc_sw128(a_base + C::A_BYTES + j * kstep_a, lbo_a, 1024);
-                mma(d_tmem, ad2, bd, 1u);
+              if (C::A_TILES > 1) {
+#pragma unroll
+                for (int p = 1; p < C::A_TILES; ++p)
+                  mma(d_tmem, smem_desc_sw128(a_base + p * C::A_BYTES + j * kstep_a, lbo_a, 1024),
+                      bd, 1u);
               } else if (SPLIT == SPLIT_B) {
                 const uint64_t bd2 =
                     smem_desc_sw128(b_base + C::B_BYTES + j * kstep_b, lbo_b, 1024);
@@ -2371,17 +2389,29 @@ cudaError_t launch_router_logits(const Dims& D, const void* x, const void* w_rou
 
 // ---------------------------------------------------- the dense product --
 
-// A DENSE launch of the dense product's GEMMs: CTA pairs when C has more than
-// one row tile (a pair's second CTA would have no rows otherwise).
+// A DENSE launch of the dense product's GEMMs, C [M, N] = A B (split s of a
+// split-K product at rows s * M): 256 x 256 tiles on CTA pairs when C has more
+// than one row tile (a pair's second CTA would have no rows otherwise), else
+// 128 x BN1 on single CTAs.  B: [N, K] (K-major) or [K, N].
 template <bool A_MN, bool B_MN, int EPI, int SPLIT>
-static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const CUtensorMap& tb,
-                                const CUtensorMap& tc, GemmArgs& a, cudaStream_t st,
-                                const CUtensorMap* tl, const OutMaps* om) {
+static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const void* B,
+                                int64_t K, int64_t ld_b, const CUtensorMap& tc, GemmArgs& a,
+                                cudaStream_t st, const CUtensorMap* tl, const OutMaps* om) {
+  constexpr int BN1 = SPLIT == SPLIT_A3 ? 128 : 256;  // (three stages of 128; two of 256)
+  const bool pair = a.m_tiles > 1;
+  const int bn = pair ? 256 : BN1;
   const int splits = a.k_splits > 1 ? a.k_splits : 1;
-  if (a.m_tiles > 1)
+  a.E = 1;
+  a.n_tiles = (a.n_valid + bn - 1) / bn;
+  a.num_kb = static_cast<int>(((K + 63) / 64 + splits - 1) / splits);
+  CUtensorMap tb;
+  if (!(B_MN ? make_map(&tb, B, a.n_valid, K, ld_b, 64)
+             : make_map(&tb, B, K, a.n_valid, ld_b, pair ? 128 : bn)))
+    return cudaErrorInvalidValue;
+  if (pair)
     return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true>(
         name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
-  return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT>(
+  return launch<BN1, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT>(
       name, ta, tb, tc, a, a.m_tiles * a.n_tiles * splits, st, tl, om);
 }
 
@@ -2394,19 +2424,14 @@ static bool make_lin_map(CUtensorMap* m, const void* base, uint64_t cols, uint64
 cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
                             const void* w, const float* bias, const void* res, int act, void* y,
                             void* z, bool f32, int* status, cudaStream_t st) {
-  CUtensorMap ta, tb, tc;
-  const int b_rows = M > 128 ? 128 : 256;  // rows of w one CTA stages
-  if (!make_map(&ta, x, K, M, ld_x, 128) || !make_map(&tb, w, K, N, K, b_rows) ||
-      !make_lin_map(&tc, y, N, M, f32))
+  CUtensorMap ta, tc;
+  if (!make_map(&ta, x, K, M, ld_x, 128) || !make_lin_map(&tc, y, N, M, f32))
     return cudaErrorInvalidValue;
   OutMaps om;
   memset(&om, 0, sizeof(om));
   if (z && !make_lin_map(&om.h, z, N, M, f32)) return cudaErrorInvalidValue;
   GemmArgs a = blank_args(status);
-  a.E = 1;
   a.m_tiles = (int)((M + 127) / 128);
-  a.n_tiles = (int)((N + 255) / 256);
-  a.num_kb = (int)((K + 63) / 64);
   a.m_valid = (int)M;
   a.n_valid = (int)N;
   a.bias = bias;
@@ -2414,69 +2439,73 @@ cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const
   a.act = act;
   a.store_z = z ? 1 : 0;
   if (f32)
-    return dense_linear<false, false, EPI_LIN_F32, SPLIT_NONE>("linear", ta, tb, tc, a, st,
+    return dense_linear<false, false, EPI_LIN_F32, SPLIT_NONE>("linear", ta, w, K, K, tc, a, st,
                                                                nullptr, &om);
-  return dense_linear<false, false, EPI_LIN_BF16, SPLIT_NONE>("linear", ta, tb, tc, a, st,
+  return dense_linear<false, false, EPI_LIN_BF16, SPLIT_NONE>("linear", ta, w, K, K, tc, a, st,
                                                               nullptr, &om);
 }
 
-cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
-                           const void* dz_lo, const void* w, void* dx, bool f32, bool accumulate,
-                           int* status, cudaStream_t st) {
-  // dx [M, K] = (dz_hi + dz_lo) [M, N] w [N, K]: the reduction runs over N
-  CUtensorMap ta, tl, tb, tc;
-  if (!make_map(&ta, dz_hi, N, M, ld_dz, 128) || !make_map(&tb, w, K, N, K, 64) ||
-      !make_lin_map(&tc, dx, K, M, f32))
+// The parts of dz as A maps with boxes of box_rows rows: part 0 in *ta, the
+// second in *tl, the third in om->sfa.
+static bool dz_maps(const BfParts& dz, int64_t M, int64_t N, uint32_t box_rows, CUtensorMap* ta,
+                    CUtensorMap* tl, OutMaps* om) {
+  memset(om, 0, sizeof(*om));
+  return make_map(ta, dz.part[0], N, M, dz.ld, box_rows) &&
+         (dz.n < 2 || make_map(tl, dz.part[1], N, M, dz.ld, box_rows)) &&
+         (dz.n < 3 || make_map(&om->sfa, dz.part[2], N, M, dz.ld, box_rows));
+}
+
+cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* w,
+                           void* dx, bool f32, bool accumulate, int* status, cudaStream_t st) {
+  // dx [M, K] = dz [M, N] w [N, K]: the reduction runs over N
+  CUtensorMap ta, tl, tc;
+  OutMaps om;
+  if (!dz_maps(dz, M, N, 128, &ta, &tl, &om) || !make_lin_map(&tc, dx, K, M, f32))
     return cudaErrorInvalidValue;
-  if (dz_lo && !make_map(&tl, dz_lo, N, M, ld_dz, 128)) return cudaErrorInvalidValue;
   GemmArgs a = blank_args(status);
-  a.E = 1;
   a.m_tiles = (int)((M + 127) / 128);
-  a.n_tiles = (int)((K + 255) / 256);
-  a.num_kb = (int)((N + 63) / 64);
   a.m_valid = (int)M;
   a.n_valid = (int)K;
   a.accumulate = accumulate ? 1 : 0;
+  const char* name = "linear_dx";
   if (f32) {
-    if (dz_lo)
-      return dense_linear<false, true, EPI_LIN_F32, SPLIT_A>("linear_dx", ta, tb, tc, a, st, &tl,
-                                                             nullptr);
-    return dense_linear<false, true, EPI_LIN_F32, SPLIT_NONE>("linear_dx", ta, tb, tc, a, st,
-                                                              nullptr, nullptr);
+    if (dz.n == 3)
+      return dense_linear<false, true, EPI_LIN_F32, SPLIT_A3>(name, ta, w, N, K, tc, a, st, &tl,
+                                                              &om);
+    return dense_linear<false, true, EPI_LIN_F32, SPLIT_NONE>(name, ta, w, N, K, tc, a, st,
+                                                              nullptr, &om);
   }
-  if (dz_lo)
-    return dense_linear<false, true, EPI_LIN_BF16, SPLIT_A>("linear_dx", ta, tb, tc, a, st, &tl,
-                                                            nullptr);
-  return dense_linear<false, true, EPI_LIN_BF16, SPLIT_NONE>("linear_dx", ta, tb, tc, a, st,
-                                                             nullptr, nullptr);
+  if (dz.n == 2)
+    return dense_linear<false, true, EPI_LIN_BF16, SPLIT_A>(name, ta, w, N, K, tc, a, st, &tl,
+                                                            &om);
+  return dense_linear<false, true, EPI_LIN_BF16, SPLIT_NONE>(name, ta, w, N, K, tc, a, st,
+                                                             nullptr, &om);
 }
 
-cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
-                           const void* dz_lo, const void* x, int64_t ld_x, float* dw,
-                           bool accumulate, int splits, int* status, cudaStream_t st) {
-  // dw [N, K] = (dz_hi + dz_lo)^T [N x M] x [M, K]: the reduction runs over
-  // the tokens, `splits` partial products at rows s * (N padded to 128) of dw
-  CUtensorMap ta, tl, tb, tc;
+cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* x,
+                           int64_t ld_x, float* dw, bool accumulate, int splits, int* status,
+                           cudaStream_t st) {
+  // dw [N, K] = dz^T [N x M] x [M, K]: the reduction runs over the tokens,
+  // `splits` partial products at rows s * (N padded to 128) of dw
+  CUtensorMap ta, tl, tc;
+  OutMaps om;
   const int64_t n_pad = (N + 127) / 128 * 128;
-  if (!make_map(&ta, dz_hi, N, M, ld_dz, 64) || !make_map(&tb, x, K, M, ld_x, 64) ||
+  if (!dz_maps(dz, M, N, 64, &ta, &tl, &om) ||
       !make_out_map(&tc, dw, K, splits > 1 ? splits * n_pad : N))
     return cudaErrorInvalidValue;
-  if (dz_lo && !make_map(&tl, dz_lo, N, M, ld_dz, 64)) return cudaErrorInvalidValue;
   GemmArgs a = blank_args(status);
-  a.E = 1;
   a.m_tiles = (int)(n_pad / 128);
-  a.n_tiles = (int)((K + 255) / 256);
   a.k_splits = splits;
-  a.num_kb = (int)(((M + 63) / 64 + splits - 1) / splits);
   a.m_rows = (int)n_pad;
   a.m_valid = (int)(splits > 1 ? n_pad : N);
   a.n_valid = (int)K;
   a.accumulate = accumulate ? 1 : 0;
-  if (dz_lo)
-    return dense_linear<true, true, EPI_LIN_F32, SPLIT_A>("linear_dw", ta, tb, tc, a, st, &tl,
-                                                          nullptr);
-  return dense_linear<true, true, EPI_LIN_F32, SPLIT_NONE>("linear_dw", ta, tb, tc, a, st,
-                                                           nullptr, nullptr);
+  const char* name = "linear_dw";
+  if (dz.n == 3)
+    return dense_linear<true, true, EPI_LIN_F32, SPLIT_A3>(name, ta, x, M, ld_x, tc, a, st, &tl,
+                                                           &om);
+  return dense_linear<true, true, EPI_LIN_F32, SPLIT_NONE>(name, ta, x, M, ld_x, tc, a, st,
+                                                           nullptr, &om);
 }
 
 cudaError_t gemm_dense_bf16(int64_t M, int64_t N, int64_t K, const void* A, bool a_mn,

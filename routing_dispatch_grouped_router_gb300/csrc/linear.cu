@@ -300,6 +300,10 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
   a.act = D.act;
   a.status = status;
   const bool f32 = D.y_elem == MOK_ELEM_F32;
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(res) |
+                         reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(z);
+  if (D.M > 128 && D.N % 8 == 0 && (bits & 15) == 0)
+    return gemm_linear_fwd(D.M, D.N, D.K, D.ld_x, x, w, bias, res, D.act, y, z, f32, status, st);
   if (D.M <= 16) return f32 ? run_linear<16, true>(D, x, w, a, st) : run_linear<16, false>(D, x, w, a, st);
   if (D.M <= 64) return f32 ? run_linear<64, true>(D, x, w, a, st) : run_linear<64, false>(D, x, w, a, st);
   return f32 ? run_linear<128, true>(D, x, w, a, st) : run_linear<128, false>(D, x, w, a, st);
@@ -311,7 +315,7 @@ namespace {
 
 struct DzArgs {
   const void *dy, *z;
-  __nv_bfloat16 *hi, *lo;  // [M, n_pad], zero past N (NULL: not stored)
+  __nv_bfloat16* dz[3];    // parts [M, n_pad], zero past N (NULL: not stored)
   float* part;             // [ceil(M / kDzRows), N] column sums (NULL: none)
   long long M;
   int N, n_pad, act;
@@ -319,8 +323,8 @@ struct DzArgs {
 
 constexpr int kDzRows = 64;  // rows of a block: 8 for each of its 8 warps
 
-// dz = dy act'(z) as a bf16 hi + lo pair, and its column sums over the block's
-// rows.  A block takes 256 columns, a lane 8 of them.
+// dz = dy act'(z) as the sum of bf16 parts (each the rounding of what those
+// before it leave), and its column sums over the block's rows.  A block takes 256 columns, a lane 8 of them.
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
   __shared__ float s_sum[8][256];
@@ -367,16 +371,19 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += v[j];
-    if (a.hi) {
-      uint32_t h[4], l[4];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      if (!a.dz[p]) break;
+      uint32_t h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float h0 = bf16_round(v[2 * j]), h1 = bf16_round(v[2 * j + 1]);
         h[j] = pack_bf16x2(h0, h1);
-        l[j] = pack_bf16x2(v[2 * j] - h0, v[2 * j + 1] - h1);
+        // (an infinite value leaves nothing: inf - inf would be NaN)
+        v[2 * j] = isinf(h0) ? 0.f : v[2 * j] - h0;
+        v[2 * j + 1] = isinf(h1) ? 0.f : v[2 * j + 1] - h1;
       }
-      st_global_v4(a.hi + r * a.n_pad + c, make_uint4(h[0], h[1], h[2], h[3]));
-      if (a.lo) st_global_v4(a.lo + r * a.n_pad + c, make_uint4(l[0], l[1], l[2], l[3]));
+      st_global_v4(a.dz[p] + r * a.n_pad + c, make_uint4(h[0], h[1], h[2], h[3]));
     }
   }
   if (!a.part) return;
@@ -413,8 +420,8 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float4* __restrict
 // K splits of the weight gradient (over the tokens): as many as its tiles
 // leave SMs for, at least eight 64-token blocks each.
 int dw_splits(const mok_linear_desc& D) {
-  const int64_t mt = (D.N + 127) / 128, nt = (D.K + 255) / 256;
-  const int64_t tiles = mt > 1 ? (mt + 1) / 2 * nt : nt;
+  const int64_t mt = (D.N + 127) / 128;
+  const int64_t tiles = mt > 1 ? (mt + 1) / 2 * ((D.K + 255) / 256) : (D.K + 127) / 128;
   const int64_t slots = mt > 1 ? 76 : 152;  // whatever the device: the sums do not depend on it
   const int64_t nkb = (D.M + 63) / 64;
   int64_t ks = slots / tiles;
@@ -432,9 +439,8 @@ void linear_layout(const mok_linear_desc& D, LinearWs* W) {
   W->bias_rows = (D.M + kDzRows - 1) / kDzRows;
   W->dw_splits = dw_splits(D);
   const size_t dz = static_cast<size_t>(D.M) * W->n_pad * 2;
-  W->dz_hi = 0;
-  W->dz_lo = al(dz);
-  W->part_bias = W->dz_lo + al(dz);
+  for (int p = 0; p < 3; ++p) W->dz[p] = p * al(dz);
+  W->part_bias = 3 * al(dz);
   W->part_dw = W->part_bias + al(static_cast<size_t>(W->bias_rows) * D.N * 4);
   const size_t rows = static_cast<size_t>((D.N + 127) / 128 * 128);
   W->total = W->part_dw + (W->dw_splits > 1 ? al(W->dw_splits * rows * D.K * 4) : 0);
@@ -450,15 +456,19 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
   const bool vec = D.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(z)) & 15) == 0;
   // a bf16 dy without an activation is dz already
   const bool direct = !f32 && D.act == MOK_ACT_NONE && vec;
+  // an fp32 result takes all 24 bits of dz in three parts (16 bits of two
+  // parts leave it 2.4e-6 off, the fp32 sums 5e-7), a bf16 result two
+  const bool dxf = D.dx_elem == MOK_ELEM_F32;
   const bool split = f32 || D.act != MOK_ACT_NONE;
+  const int parts = direct ? 0 : (!split ? 1 : (dw || dxf ? 3 : 2));
   const bool products = D.M > 0 && (dx || dw);
   float* part_bias = reinterpret_cast<float*>(b + W.part_bias);
   if (D.M > 0 && ((products && !direct) || dbias)) {
     DzArgs a;
     a.dy = dy;
     a.z = z;
-    a.hi = products && !direct ? reinterpret_cast<__nv_bfloat16*>(b + W.dz_hi) : nullptr;
-    a.lo = products && split ? reinterpret_cast<__nv_bfloat16*>(b + W.dz_lo) : nullptr;
+    for (int p = 0; p < 3; ++p)
+      a.dz[p] = products && p < parts ? reinterpret_cast<__nv_bfloat16*>(b + W.dz[p]) : nullptr;
     a.part = dbias ? part_bias : nullptr;
     a.M = D.M;
     a.N = static_cast<int>(D.N);
@@ -487,18 +497,22 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     if (dw && !D.accumulate) return cudaMemsetAsync(dw, 0, static_cast<size_t>(D.N) * D.K * 4, st);
     return cudaSuccess;
   }
-  const void* hi = direct ? dy : b + W.dz_hi;
-  const void* lo = split ? b + W.dz_lo : nullptr;
-  const int64_t ld = direct ? D.N : W.n_pad;
+  BfParts dz;
+  dz.n = split ? 3 : 1;
+  dz.ld = direct ? D.N : W.n_pad;
+  for (int p = 0; p < 3; ++p) dz.part[p] = b + W.dz[p];
+  if (direct) dz.part[0] = dy;
   if (dx) {
-    const cudaError_t e = gemm_linear_dx(D.M, D.N, D.K, ld, hi, lo, w, dx,
-                                         D.dx_elem == MOK_ELEM_F32, D.accumulate != 0, status, st);
+    BfParts d = dz;
+    if (split && !dxf) d.n = 2;
+    const cudaError_t e =
+        gemm_linear_dx(D.M, D.N, D.K, d, w, dx, dxf, D.accumulate != 0, status, st);
     if (e != cudaSuccess) return e;
   }
   if (dw) {
     float* part = reinterpret_cast<float*>(b + W.part_dw);
     const bool sum = W.dw_splits > 1;
-    cudaError_t e = gemm_linear_dw(D.M, D.N, D.K, ld, hi, lo, x, D.ld_x, sum ? part : dw,
+    cudaError_t e = gemm_linear_dw(D.M, D.N, D.K, dz, x, D.ld_x, sum ? part : dw,
                                    !sum && D.accumulate != 0, W.dw_splits, status, st);
     if (e != cudaSuccess || !sum) return e;
     const long long n4 = D.N * D.K / 4;

@@ -292,8 +292,8 @@ cudaError_t launch_balance_bwd(const mok_balance_desc& D, const float* dloss,
 
 // The dense product (linear.cu) and its GEMMs on the persistent engine (gemm.cu).
 struct LinearWs {
-  size_t dz_hi, dz_lo, part_bias, part_dw, total;
-  int64_t n_pad;      // row length of dz_hi, dz_lo
+  size_t dz[3], part_bias, part_dw, total;
+  int64_t n_pad;      // row length of dz's parts
   int64_t bias_rows;  // partial bias gradients
   int dw_splits;      // partial weight gradients (1: none)
 };
@@ -308,13 +308,20 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
 cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
                             const void* w, const float* bias, const void* res, int act, void* y,
                             void* z, bool f32, int* status, cudaStream_t st);
-// dz as a bf16 tensor with row stride ld_dz (a multiple of 8); dz_lo may be null
-cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
-                           const void* dz_lo, const void* w, void* dx, bool f32, bool accumulate,
-                           int* status, cudaStream_t st);
-cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, int64_t ld_dz, const void* dz_hi,
-                           const void* dz_lo, const void* x, int64_t ld_x, float* dw,
-                           bool accumulate, int splits, int* status, cudaStream_t st);
+// An fp32 operand as the sum of n bf16 parts (1: a bf16 tensor itself; 2:
+// about 16 significant bits; 3: all 24), each [M, N] with row stride ld (a
+// multiple of 8).
+struct BfParts {
+  const void* part[3];
+  int n;
+  int64_t ld;
+};
+// fp32 dx: one or three parts; bf16 dx: one or two.  dw: one or three.
+cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* w,
+                           void* dx, bool f32, bool accumulate, int* status, cudaStream_t st);
+cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* x,
+                           int64_t ld_x, float* dw, bool accumulate, int splits, int* status,
+                           cudaStream_t st);
 
 // MXFP8 fake quantisation (mx.cu): rows = blocks along each row, cols =
 // blocks of 32 rows; codes/scales may be null.

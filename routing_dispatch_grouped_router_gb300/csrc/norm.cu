@@ -437,10 +437,10 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
   s[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
   if (threadIdx.y == 0 && c < d) {
-    float v = accumulate ? out[c] : 0.f;
+    float v = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v += s[j][threadIdx.x];
-    out[c] = v;
+    out[c] = accumulate ? out[c] + v : v;
   }
 }
 
