@@ -141,6 +141,9 @@ struct GemmArgs {
   const void* res;
   int act;
   int store_z;
+  // EPI_LIN_F32: K blocks of one accumulation on the tensor cores (see
+  // kChunkMmas); the chunks' sums are added in fp32 registers
+  int chunk_kb;
   int* status;
 };
 
@@ -157,6 +160,15 @@ struct OutMaps {
   // (64-byte swizzle); a zeroed map (no h, or h as MXFP8 codes) is unused
   CUtensorMap h;
 };
+
+// The tensor cores' fp32 accumulation truncates: every MMA (16 K values) a sum
+// goes through costs it about 1.7e-8 of its value (measured: K = 2048 in one
+// accumulation, 128 MMAs, 2.1e-6 off; 16384 values in three parts, 768 MMAs,
+// 1.4e-5; an fp32 sum with correct rounding is 4e-7 off).  An fp32 result of
+// the dense product is therefore accumulated over at most this many MMAs at a
+// time, and the chunks are added in registers with correct rounding while the
+// other accumulator takes the next one.
+constexpr int kChunkMmas = 32;
 
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
@@ -645,6 +657,81 @@ __device__ __forceinline__ void stage_and_store_bf16_rows32(uint8_t* buf, const 
   }
 }
 
+// The dense product's epilogue of one 32-column chunk: v = C's values of this
+// lane's row, columns x ..; tl's split writes its partial at rows e * m_rows.
+template <int EPI>
+__device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, int q, int lane,
+                                             int x, float (&v)[32], uint8_t* stage_buf,
+                                             uint32_t& nst, const CUtensorMap* tmC,
+                                             const CUtensorMap* tmH) {
+  const int y = tl.e * a.m_rows + tl.row0 + q * 32;
+  const long long row = tl.row0 + q * 32 + lane;
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (x + 4 * j < a.n_valid) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + x) + j);
+        v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
+      }
+    }
+  }
+  if (a.store_z) {
+    if (EPI == EPI_LIN_F32) stage_and_store_f32(stage_buf, nst, tmH, v, lane, x, y);
+    else stage_and_store_bf16_rows32(stage_buf, tmH, v, lane, x, y);
+  }
+  if (a.act != MOK_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], a.act);
+  }
+  if (a.res && row < a.m_valid) {
+    if (EPI == EPI_LIN_F32) {
+      const float4* p =
+          reinterpret_cast<const float4*>(static_cast<const float*>(a.res) + row * a.n_valid + x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (x + 4 * j < a.n_valid) {
+          const float4 b = p[j];
+          v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
+        }
+      }
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.res) +
+                                                      row * a.n_valid + x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (x + 8 * j < a.n_valid) {
+          const uint4 b = p[j];
+          v[8 * j] += bf16lo(b.x); v[8 * j + 1] += bf16hi(b.x);
+          v[8 * j + 2] += bf16lo(b.y); v[8 * j + 3] += bf16hi(b.y);
+          v[8 * j + 4] += bf16lo(b.z); v[8 * j + 5] += bf16hi(b.z);
+          v[8 * j + 6] += bf16lo(b.w); v[8 * j + 7] += bf16hi(b.w);
+        }
+      }
+    }
+  }
+  if (EPI == EPI_LIN_F32)
+    stage_and_store_f32(stage_buf, nst, tmC, v, lane, x, y, a.accumulate != 0);
+  else
+    stage_and_store_bf16_rows32(stage_buf, tmC, v, lane, x, y);
+}
+
+// ... and of one tile: this warp's 32 rows and half of the columns, from TMEM.
+template <int BN, int EPI>
+__device__ __forceinline__ void linear_tile(const GemmArgs& a, const Tile& tl, uint32_t taddr,
+                                            int q, int lane, int half, uint8_t* stage_buf,
+                                            uint32_t& nst, const CUtensorMap* tmC,
+                                            const CUtensorMap* tmH) {
+  if (tl.row0 + q * 32 >= a.m_valid) return;  // (a partial block is clipped by the TMA)
+  const int col0 = tl.n_tile * BN + half * (BN / 2);
+#pragma unroll 1
+  for (int c = 0; c < BN / 2; c += 32) {
+    if (col0 + c >= a.n_valid) break;
+    float v[32];
+    tmem_ld32(taddr + half * (BN / 2) + c, v);
+    linear_chunk<EPI>(a, tl, q, lane, col0 + c, v, stage_buf, nst, tmC, tmH);
+  }
+}
+
 template <int BN, int SCHED, int EPI, bool DBUF, int SPLIT>
 __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& tl, uint32_t taddr,
                                               int q, int lane, int half, uint8_t* stage_buf,
@@ -700,65 +787,7 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& tl,
       }
     }
   } else if constexpr (linear_epi(EPI)) {
-    // split s of a split-K product writes its partial at rows s * m_rows
-    const int y = tl.e * a.m_rows + tl.row0 + q * 32;
-    if (tl.row0 + q * 32 >= a.m_valid) return;  // (a partial block is clipped)
-    const int col0 = tl.n_tile * BN + half * HALF_COLS;
-    const long long row = tl.row0 + row_in_tile;
-#pragma unroll 1
-    for (int c = 0; c < HALF_COLS; c += 32) {
-      const int x = col0 + c;
-      if (x >= a.n_valid) break;
-      float v[32];
-      tmem_ld32(taddr + half * HALF_COLS + c, v);
-      if (a.bias) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (x + 4 * j < a.n_valid) {
-            const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + x) + j);
-            v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
-          }
-        }
-      }
-      if (a.store_z) {
-        if (EPI == EPI_LIN_F32) stage_and_store_f32<DBUF>(stage_buf, nst, tmH, v, lane, x, y);
-        else stage_and_store_bf16_rows32(stage_buf, tmH, v, lane, x, y);
-      }
-      if (a.act != MOK_ACT_NONE) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], a.act);
-      }
-      if (a.res && row < a.m_valid) {
-        if (EPI == EPI_LIN_F32) {
-          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.res) +
-                                                            row * a.n_valid + x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (x + 4 * j < a.n_valid) {
-              const float4 b = p[j];
-              v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
-            }
-          }
-        } else {
-          const uint4* p = reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(a.res) + row * a.n_valid + x);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (x + 8 * j < a.n_valid) {
-              const uint4 b = p[j];
-              v[8 * j] += bf16lo(b.x); v[8 * j + 1] += bf16hi(b.x);
-              v[8 * j + 2] += bf16lo(b.y); v[8 * j + 3] += bf16hi(b.y);
-              v[8 * j + 4] += bf16lo(b.z); v[8 * j + 5] += bf16hi(b.z);
-              v[8 * j + 6] += bf16lo(b.w); v[8 * j + 7] += bf16hi(b.w);
-            }
-          }
-        }
-      }
-      if (EPI == EPI_LIN_F32)
-        stage_and_store_f32<DBUF>(stage_buf, nst, tmC, v, lane, x, y, a.accumulate != 0);
-      else
-        stage_and_store_bf16_rows32(stage_buf, tmC, v, lane, x, y);
-    }
+    linear_tile<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, nst, tmC, tmH);
   } else if (EPI == EPI_F32_T || EPI == EPI_BF16_T) {
     // C^T through TMA: accumulator rows are output columns; C viewed as
     // [E * N, M] with group e's block at rows e*N
@@ -1162,6 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ GemmArgs args, const __grid_constant__ OutMaps om) {
   using C = Cfg<BN, SPLIT, PAIR, staging_bytes<EPI, SPLIT, SCHED, DB>()>;
   constexpr bool kDbuf = DB;
+  constexpr bool kChunks = EPI == EPI_LIN_F32;
   static_assert(!DB || ((EPI == EPI_F32 || EPI == EPI_F32_T) && SCHED == SCHED_KGROUP) ||
                     (EPI == EPI_SWIGLU_BWD && PAIR),
                 "DB: double-buffered staging of the fp32 weight gradients, or the SwiGLU "
@@ -1454,15 +1484,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = first; t < total && ok; t += step, ++it) {
         bool valid;
         const Tile tl = tile_at(t, &valid);
-        const int acc = C::NACC == 2 ? (it & 1) : 0;
+        int acc = C::NACC == 2 ? (it & 1) : 0;
         const uint32_t acc_par = static_cast<uint32_t>(C::NACC == 2 ? ((it >> 1) & 1) : (it & 1));
         if (!wait(&tempty[acc], acc_par ^ 1u)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        int kb0 = 0;  // first K block of this accumulation
         for (int kb = 0; kb < tl.num_kb; ++kb) {
+          if (kChunks && kb == kb0 + args.chunk_kb) {
+            // the next chunk's sum goes to the other accumulator
+            commit(&tfull[acc]);
+            ++it;
+            kb0 = kb;
+            acc = it & 1;
+            if (!wait(&tempty[acc], static_cast<uint32_t>((it >> 1) & 1) ^ 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+          }
           if (!wait(&full[stage], phase)) {
             ok = false;
             break;
@@ -1518,7 +1562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) {
               const uint64_t ad = smem_desc_sw128(a_base + j * kstep_a, lbo_a, 1024);
               const uint64_t bd = smem_desc_sw128(b_base + j * kstep_b, lbo_b, 1024);
-              mma(d_tmem, ad, bd, (kb | j) != 0 ? 1u : 0u);
+              mma(d_tmem, ad, bd, ((kb - kb0) | j) != 0 ? 1u : 0u);
               if (C::A_TILES > 1) {
 #pragma unroll
                 for (int p = 1; p < C::A_TILES; ++p)
@@ -1568,6 +1612,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = first; t < total; t += step, ++it) {
       bool valid;
       const Tile tl = tile_at(t, &valid);
+      if constexpr (kChunks) {
+        // the chunks' sums of this warp's 32 rows and half of the columns
+        float sum[BN / 2];
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j) sum[j] = 0.f;
+        bool ok = true;
+        for (int kb = 0; kb < tl.num_kb; kb += args.chunk_kb) {
+          if (kb > 0) ++it;
+          if (!wait(&tfull[it & 1], static_cast<uint32_t>((it >> 1) & 1))) {
+            *vabort = 1;
+            set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t src = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                               static_cast<uint32_t>((it & 1) * BN + half * (BN / 2));
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < BN / 2; c += 32) {
+            float v[32];
+            tmem_ld32(src + c, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c + j] += v[j];
+          }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR) mbar_arrive_cluster(tempty_leader + 8u * (it & 1));
+            else mbar_arrive(&tempty[it & 1]);
+          }
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!valid || tl.row0 + q * 32 >= args.m_valid) continue;
+        const int col0 = tl.n_tile * BN + half * (BN / 2);
+#pragma unroll
+        for (int c = 0; c < BN / 2; c += 32) {
+          if (col0 + c >= args.n_valid) continue;
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
+          linear_chunk<EPI>(args, tl, q, lane, col0 + c, v, stage_buf, nst, &tmC, &om.h);
+        }
+        continue;
+      }
       const int acc = C::NACC == 2 ? (it & 1) : 0;
       const uint32_t acc_par = static_cast<uint32_t>(C::NACC == 2 ? ((it >> 1) & 1) : (it & 1));
       // this warp's 32 rows: none of them read by anything (args.coff)
@@ -2404,6 +2493,7 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
   a.E = 1;
   a.n_tiles = (a.n_valid + bn - 1) / bn;
   a.num_kb = static_cast<int>(((K + 63) / 64 + splits - 1) / splits);
+  a.chunk_kb = kChunkMmas / (4 * Cfg<BN1, SPLIT>::A_TILES);
   CUtensorMap tb;
   if (!(B_MN ? make_map(&tb, B, a.n_valid, K, ld_b, 64)
              : make_map(&tb, B, K, a.n_valid, ld_b, pair ? 128 : bn)))

@@ -34,9 +34,10 @@ struct LinCfg {
   static constexpr int STAGES = ROOM / STAGE_BYTES;
   static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
-  static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+  static constexpr int ACC_COLS = BN;  // two accumulators
+  static constexpr int TMEM_COLS = 2 * BN;
   static_assert(BN * 128 * 4 <= BAR_OFF, "the partial sums fit the operand ring");
-  static_assert(SMEM_BYTES <= 232448 && STAGES >= 4 && (2 * STAGES + 2) * 8 + 8 <= 256, "smem");
+  static_assert(SMEM_BYTES <= 232448 && STAGES >= 4 && (2 * STAGES + 4) * 8 + 8 <= 256, "smem");
 };
 
 struct LinArgs {
@@ -44,30 +45,82 @@ struct LinArgs {
   const void* res;
   void *y, *z;
   int M, N, nkb, act;
+  int chunk_kb;  // K blocks of one accumulation on the tensor cores
+  int vec;       // rows of y, z, res and the bias take four elements at a time
   int* status;
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-// One output element (token m, feature n) from its sum.
 template <bool F32>
-__device__ __forceinline__ void finish(const LinArgs& a, long long m, int n, float v, float bias) {
-  const long long o = m * a.N + n;
-  v += bias;
+__device__ __forceinline__ void load4(const void* p, long long o, float (&v)[4]) {
   if (F32) {
-    if (a.z) static_cast<float*>(a.z)[o] = v;
-    v = act_value(v, a.act);
-    if (a.res) v += static_cast<const float*>(a.res)[o];
-    static_cast<float*>(a.y)[o] = v;
+    const float4 t = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + o);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
   } else {
-    if (a.z) static_cast<__nv_bfloat16*>(a.z)[o] = __float2bfloat16_rn(v);
-    v = act_value(v, a.act);
-    if (a.res) v += __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[o]);
-    static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
+    const uint2 t = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + o);
+    v[0] = bf16lo(t.x); v[1] = bf16hi(t.x); v[2] = bf16lo(t.y); v[3] = bf16hi(t.y);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store4(void* p, long long o, const float (&v)[4]) {
+  if (F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + o) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + o) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+template <bool F32>
+__device__ __forceinline__ float load1(const void* p, long long o) {
+  return F32 ? static_cast<const float*>(p)[o]
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[o]);
+}
+template <bool F32>
+__device__ __forceinline__ void store1(void* p, long long o, float v) {
+  if (F32) static_cast<float*>(p)[o] = v;
+  else static_cast<__nv_bfloat16*>(p)[o] = __float2bfloat16_rn(v);
+}
+
+// Features n .. n+3 of token m from their sums.
+template <bool F32>
+__device__ __forceinline__ void finish4(const LinArgs& a, long long m, int n, float (&v)[4]) {
+  const long long o = m * a.N + n;
+  if (a.vec) {
+    if (n >= a.N) return;
+    float t[4];
+    if (a.bias) {
+      load4<true>(a.bias, n, t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += t[j];
+    }
+    if (a.z) store4<F32>(a.z, o, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = act_value(v[j], a.act);
+    if (a.res) {
+      load4<F32>(a.res, o, t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += t[j];
+    }
+    store4<F32>(a.y, o, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + j >= a.N) break;
+      float t = v[j] + (a.bias ? a.bias[n + j] : 0.f);
+      if (a.z) store1<F32>(a.z, o + j, t);
+      t = act_value(t, a.act);
+      if (a.res) t += load1<F32>(a.res, o + j);
+      store1<F32>(a.y, o + j, t);
+    }
   }
 }
 
@@ -82,8 +135,9 @@ __global__ void __launch_bounds__(kLinThreads)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
   uint64_t* empty = full + C::STAGES;
-  uint64_t* done = empty + C::STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* tfull = empty + C::STAGES;  // accumulators written (two)
+  uint64_t* tempty = tfull + 2;         // accumulators read by the four epilogue warps
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ks = gridDim.x, split = blockIdx.x;
@@ -96,7 +150,10 @@ __global__ void __launch_bounds__(kLinThreads)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 4);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
@@ -111,13 +168,13 @@ __global__ void __launch_bounds__(kLinThreads)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   volatile int* vabort = abort_flag;
+  bool ok = true;
 
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
-      bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, vabort)) {
           ok = false;
@@ -150,93 +207,112 @@ __global__ void __launch_bounds__(kLinThreads)
       constexpr uint32_t idesc = idesc_bf16_f32(128, BN, false, false);
       int stage = 0;
       uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full[stage], phase, vabort)) {
+      int it = 0;
+      for (int c0 = kb0; c0 < kb1 && ok; c0 += args.chunk_kb, ++it) {
+        const int acc = it & 1;
+        const uint32_t par = static_cast<uint32_t>((it >> 1) & 1);
+        if (!mbar_wait(&tempty[acc], par ^ 1u, vabort)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t a_base = smem_addr(smem + stage * C::STAGE_BYTES);
-        const uint32_t b_base = a_base + C::A_BYTES;
+        const int c1 = c0 + args.chunk_kb < kb1 ? c0 + args.chunk_kb : kb1;
+        for (int kb = c0; kb < c1; ++kb) {
+          if (!mbar_wait(&full[stage], phase, vabort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a_base = smem_addr(smem + stage * C::STAGE_BYTES);
+          const uint32_t b_base = a_base + C::A_BYTES;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_bf16(tmem, smem_desc_sw128(a_base + j * 32, 16, 1024),
-                   smem_desc_sw128(b_base + j * 32, 16, 1024), idesc,
-                   (kb > kb0 || j > 0) ? 1u : 0u);
-        mma_commit(&empty[stage]);
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
+          for (int j = 0; j < 4; ++j)
+            mma_bf16(tmem + acc * C::ACC_COLS, smem_desc_sw128(a_base + j * 32, 16, 1024),
+                     smem_desc_sw128(b_base + j * 32, 16, 1024), idesc,
+                     (kb > c0 || j > 0) ? 1u : 0u);
+          mma_commit(&empty[stage]);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+        mma_commit(&tfull[acc]);
       }
       if (!ok) {
+        // the MMAs issued are done before TMEM is freed: the last commit above
         *vabort = 1;
         set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
-      }
-      mma_commit(done);
-      const int zero = 0;
-      if (!ok) mbar_wait(done, 0, &zero);
-    }
-  }
-  // every thread waits for the last MMA: the epilogue reads TMEM, and with a
-  // split the partial sums go over the operand ring
-  __syncwarp();
-  const bool good = __all_sync(0xffffffffu, mbar_wait(done, 0, vabort));
-  if (!good) {
-    *vabort = 1;
-    set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
-  }
-  tc_fence_after_sync();
-
-  const int q = warp & 3;  // TMEM lane quarter of an epilogue warp
-  const int f = q * 32 + lane;
-  const int n = n0 + f;
-  if (ks == 1) {
-    if (warp >= 2 && good) {
-      const float bias = args.bias && n < args.N ? args.bias[n] : 0.f;
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 16) {
-        if (m0 + c >= args.M) break;
-        uint32_t r[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (m0 + c + j < args.M && n < args.N)
-            finish<F32>(args, m0 + c + j, n, __uint_as_float(r[j]), bias);
+        const int zero = 0;
+        if (it > 0) mbar_wait(&tfull[(it - 1) & 1], static_cast<uint32_t>(((it - 1) >> 1) & 1), &zero);
       }
     }
   } else {
-    float* part = reinterpret_cast<float*>(smem);  // [BN tokens][128 features]
-    __syncthreads();  // every warp has seen the last MMA
-    if (warp >= 2) {
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 16) {
-        if (m0 + c >= args.M) break;
-        uint32_t r[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, r);
-        tmem_ld_wait();
+    // ---- the chunks' sums: lane f of the tile's 128 features, BN tokens ----
+    const int q = warp & 3;  // TMEM lane quarter this warp may read
+    const int f = q * 32 + lane;
+    float sum[BN];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + f] = __uint_as_float(r[j]);
+    for (int j = 0; j < BN; ++j) sum[j] = 0.f;
+    int it = 0;
+    for (int c0 = kb0; c0 < kb1; c0 += args.chunk_kb, ++it) {
+      const int acc = it & 1;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait(&tfull[acc], static_cast<uint32_t>((it >> 1) & 1), vabort));
+      if (!ok) {
+        *vabort = 1;
+        set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
+        break;
       }
-    }
-    cluster_sync();
-    if (warp >= 2 && good && n < args.N) {
-      const float bias = args.bias ? args.bias[n] : 0.f;
-      const uint32_t mine = smem_addr(part) + f * 4;
-#pragma unroll 1
-      for (int m = split; m < BN && m0 + m < args.M; m += ks) {
-        float v = 0.f;
-        for (int r = 0; r < ks; ++r)
-          v += ld_cluster_f32(mapa_shared(mine + static_cast<uint32_t>(m) * 512u, r));
-        finish<F32>(args, m0 + m, n, v, bias);
+      tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < BN; c += 16) {
+        if (m0 + c < args.M) {
+          uint32_t r[16];
+          tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * C::ACC_COLS + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[c + j] += __uint_as_float(r[j]);
+        }
       }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
     }
-    cluster_sync();  // no CTA leaves while another reads its partial sums
+    // every MMA has read its operands (the last chunk is complete), so the
+    // sums take the ring's place: [BN tokens][128 features]
+    float* part = reinterpret_cast<float*>(smem);
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < BN; ++j)
+        if (m0 + j < args.M) part[j * 128 + f] = sum[j];
+    }
   }
+  __syncwarp();
+  if (ks > 1) cluster_sync(); else __syncthreads();
+  // this CTA's share of the tokens, four features per thread, the cluster's
+  // sums in rank order
+  if (!*vabort) {
+    const uint32_t part = smem_addr(smem);
+    const int f4 = lane * 4;
+    for (int m = split + ks * warp; m < BN && m0 + m < args.M; m += ks * (kLinThreads / 32)) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t at = part + static_cast<uint32_t>(m * 128 + f4) * 4u;
+      if (ks == 1) {
+        const float4 p = *reinterpret_cast<const float4*>(smem + (m * 128 + f4) * 4);
+        v[0] = p.x; v[1] = p.y; v[2] = p.z; v[3] = p.w;
+      } else {
+        for (int r = 0; r < ks; ++r) {
+          const float4 p = ld_cluster_f4(mapa_shared(at, r));
+          v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+        }
+      }
+      finish4<F32>(args, m0 + m, n0 + f4, v);
+    }
+  }
+  __syncwarp();
   tc_fence_before_sync();
-  __syncthreads();
+  // no CTA leaves while another reads its sums
+  if (ks > 1) cluster_sync(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::TMEM_COLS);
@@ -300,8 +376,12 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
   a.act = D.act;
   a.status = status;
   const bool f32 = D.y_elem == MOK_ELEM_F32;
+  // an fp32 result: at most 32 MMAs (8 blocks) in one accumulation, as in the
+  // persistent engine; a bf16 one hides what the accumulation truncates
+  a.chunk_kb = f32 ? 8 : a.nkb;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(res) |
                          reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(z);
+  a.vec = D.N % 4 == 0 && (bits & 15) == 0;
   if (D.M > 128 && D.N % 8 == 0 && (bits & 15) == 0)
     return gemm_linear_fwd(D.M, D.N, D.K, D.ld_x, x, w, bias, res, D.act, y, z, f32, status, st);
   if (D.M <= 16) return f32 ? run_linear<16, true>(D, x, w, a, st) : run_linear<16, false>(D, x, w, a, st);
