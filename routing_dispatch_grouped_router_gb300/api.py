@@ -391,23 +391,30 @@ def router_balance(logits, topk_idx, mask=None, *, balance_coef, z_coef=0.0, wor
     """The router's auxiliary losses over the tokens of `mask` (see
     mok_router_balance_forward): (loss [2] = balance and z loss, counts int32
     [E], prob [E] = mean probability, lse [T], n_valid int32 [1]).  logits fp32
-    [T, E], topk_idx int32 [T, k], mask uint8 or bool [T]."""
+    [T, E], topk_idx int32 [T, k], mask uint8 or bool [T].  The results share
+    two allocations."""
     st = _call_stream(logits, stream)
     dev = logits.device
     _topk_plan(_meta(topk_idx), logits.shape[0], dev)
     desc, n = _balance_plan(_meta(logits), topk_idx.shape[1], _meta(mask), None, balance_coef,
                             z_coef)
-    loss = _alloc((2,), torch.float32, dev, stream)
-    counts = _alloc((desc.E,), torch.int32, dev, stream)
-    prob = _alloc((desc.E,), torch.float32, dev, stream)
-    lse = _alloc((desc.T,), torch.float32, dev, stream)
-    n_valid = _alloc((1,), torch.int32, dev, stream)
-    if workspace is None:
-        workspace = _alloc((n,), torch.uint8, dev, stream)
+    # the fp32 results (and the scratch) in one allocation, the integers in another
+    T, E = desc.T, desc.E
+    at_lse = (E + 2 + 3) // 4 * 4
+    at_ws = (at_lse + T + 3) // 4 * 4
+    buf = _alloc((at_ws + (n + 3) // 4 if workspace is None else at_ws,), torch.float32, dev, stream)
+    ints = _alloc((E + 1,), torch.int32, dev, stream)
+    prob = buf.as_strided((E,), (1,), 0)
+    loss = buf.as_strided((2,), (1,), E)
+    lse = buf.as_strided((T,), (1,), at_lse)
+    counts = ints.as_strided((E,), (1,), 0)
+    n_valid = ints.as_strided((1,), (1,), E)
+    f, i = buf.data_ptr(), ints.data_ptr()
+    ws = f + 4 * at_ws if workspace is None else workspace.data_ptr()
     _lib.check(_lib.load().mok_router_balance_forward(
-        desc, _addr(logits), _addr(topk_idx), _addr(mask), _addr(loss), _addr(counts), _addr(prob),
-        _addr(lse), _addr(n_valid), _addr(workspace), workspace.nbytes,
-        _addr(operator_status(dev)), st), "mok_router_balance_forward")
+        desc, _addr(logits), _addr(topk_idx), _addr(mask), f + 4 * E, i, f, f + 4 * at_lse,
+        i + 4 * E, ws, n if workspace is None else workspace.nbytes, _addr(operator_status(dev)),
+        st), "mok_router_balance_forward")
     return loss, counts, prob, lse, n_valid
 
 

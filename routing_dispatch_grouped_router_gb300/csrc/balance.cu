@@ -22,7 +22,13 @@ namespace mok {
 
 namespace {
 
-constexpr int kBalThreads = 256;
+constexpr int kFwdThreads = 512;
+constexpr int kBwdThreads = 256;
+// Tokens whose loads a group has in flight at once.
+constexpr int kUnroll = 2;
+// Blocks of the forward (one per SM of a GB300, whatever the device, so that
+// the sums do not depend on it).
+constexpr int kFwdBlocks = 152;
 
 struct BalArgs {
   const float* logits;
@@ -32,8 +38,8 @@ struct BalArgs {
   int32_t *counts, *n_valid;
   int* status;       // sticky device status (may be null)
   int* arrivals;     // blocks done (zero before the launch)
-  float* part_prob;  // [gridDim.x, E]
-  int32_t* part_cnt; // [gridDim.x, E]
+  float* part_prob;  // [gridDim.x, E rounded up to 4]
+  int32_t* part_cnt; // [gridDim.x, E rounded up to 4]
   float* part_z;     // [gridDim.x]
   int32_t* part_n;   // [gridDim.x]
   long long T, ld;
@@ -55,11 +61,10 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// Logits 4 (g + L j) .. + 3 of a row for lane g, -inf past E; NaN and +inf are
-// taken as -inf (*bad).
+// Logits 4 (g + L j) .. + 3 of a row for lane g, -inf past E.
 template <int L, int NJ>
 __device__ __forceinline__ void load_logits(const float* row, int g, int E, bool in, bool vec,
-                                            float (&l)[4 * NJ], bool* bad) {
+                                            float (&l)[4 * NJ]) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int e = 4 * (g + L * j);
@@ -72,27 +77,109 @@ __device__ __forceinline__ void load_logits(const float* row, int g, int E, bool
       if (e + 2 < E) v.z = row[e + 2];
       if (e + 3 < E) v.w = row[e + 3];
     }
-    const float q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool ok = q[i] < INFINITY;
-      if (!ok) *bad = true;
-      l[4 * j + i] = ok ? q[i] : -INFINITY;
-    }
+    l[4 * j] = v.x; l[4 * j + 1] = v.y; l[4 * j + 2] = v.z; l[4 * j + 3] = v.w;
   }
 }
 
+// NaN and +inf become -inf; returns whether there were any.
+template <int N>
+__device__ __forceinline__ bool clean(float (&l)[N]) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool ok = l[i] < INFINITY;
+    bad = bad || !ok;
+    l[i] = ok ? l[i] : -INFINITY;
+  }
+  return bad;
+}
+
+// The last block's work: the partials of G blocks added in block order by
+// slices (slice s takes blocks s, s + n, ..), then the losses.
+__device__ void balance_finish(const BalArgs& a, int G, float4* s_f4, int4* s_i4, float* s_red) {
+  const int t = threadIdx.x;
+  const int e4 = (a.E + 3) / 4;  // float4 columns, at most 128
+  int cols = 1;
+  while (cols < e4) cols *= 2;
+  const int n = kFwdThreads / cols;  // slices, at least 4
+  const int col = t & (cols - 1), sl = t / cols;
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+  int4 c = make_int4(0, 0, 0, 0);
+  if (col < e4) {
+    const float4* pp = reinterpret_cast<const float4*>(a.part_prob) + col;
+    const int4* pc = reinterpret_cast<const int4*>(a.part_cnt) + col;
+#pragma unroll 10
+    for (int b = sl; b < G; b += n) {
+      const float4 q = __ldcg(pp + static_cast<long long>(b) * e4);
+      const int4 k = __ldcg(pc + static_cast<long long>(b) * e4);
+      p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
+      c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
+    }
+  }
+  s_f4[t] = p;
+  s_i4[t] = c;
+  // z and N: a warp's lanes over the blocks, then the lanes in a fixed tree
+  float z = 0.f;
+  int nv = 0;
+  if (t < 32) {
+    for (int b = t; b < G; b += 32) {
+      z += __ldcg(a.part_z + b);
+      nv += __ldcg(a.part_n + b);
+    }
+    z = group_sum<32>(z);
+    nv = __reduce_add_sync(0xffffffffu, nv);
+    if (t == 0) {
+      s_red[0] = z;
+      s_red[1] = static_cast<float>(nv);  // (below 2^30; only its reciprocal is used)
+      a.n_valid[0] = nv;
+      // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
+      a.loss[1] = nv > 0 && a.z_coef != 0.f ? a.z_coef * z / static_cast<float>(nv) : 0.f;
+    }
+  }
+  __syncthreads();
+  const float inv_n = s_red[1] > 0.f ? 1.0f / s_red[1] : 0.f;
+  float dot = 0.f;
+  if (t < e4) {
+    for (int q = 1; q < n; ++q) {
+      const float4 f = s_f4[q * cols + t];
+      const int4 k = s_i4[q * cols + t];
+      p.x += f.x; p.y += f.y; p.z += f.z; p.w += f.w;
+      c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
+    }
+    const float pv[4] = {p.x * inv_n, p.y * inv_n, p.z * inv_n, p.w * inv_n};
+    const int cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * t + i < a.E) {
+        a.prob[4 * t + i] = pv[i];
+        a.counts[4 * t + i] = cv[i];
+        dot = fmaf(static_cast<float>(cv[i]), pv[i], dot);
+      }
+    }
+  }
+  if (t < 128) {  // e4 <= 128: four warps hold every product
+    dot = group_sum<32>(dot);
+    if ((t & 31) == 0) s_red[2 + (t >> 5)] = dot;
+  }
+  __syncthreads();
+  if (t == 0)
+    a.loss[0] = a.balance_coef * static_cast<float>(a.E) / static_cast<float>(a.k) *
+                ((s_red[2] + s_red[3]) + (s_red[4] + s_red[5])) * inv_n;
+}
+
 template <int L, int NJ>
-__global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(BalArgs a, int vec) {
-  constexpr int kGroups = kBalThreads / L;  // tokens in flight per block
+__global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int vec) {
+  constexpr int kGroups = kFwdThreads / L;  // tokens of a block at a time
   constexpr int kEP = 4 * L * NJ;           // E padded to the group's lanes
-  __shared__ float s_prob[kGroups * kEP];
-  __shared__ int32_t s_cnt[kMaxExperts];
+  // the groups' sums, later the last block's slices (16 KB)
+  __shared__ __align__(16) float s_prob[kGroups * kEP < 4096 ? 4096 : kGroups * kEP];
+  __shared__ __align__(16) int32_t s_cnt[kMaxExperts];
   __shared__ float s_z[kGroups];
   __shared__ int32_t s_n[kGroups];
+  __shared__ float s_red[8];
   __shared__ int s_last;
   const int t = threadIdx.x, g = t & (L - 1), grp = t / L;
-  for (int e = t; e < a.E; e += kBalThreads) s_cnt[e] = 0;
+  for (int e = t; e < kMaxExperts; e += kFwdThreads) s_cnt[e] = 0;
   __syncthreads();
   float acc[4 * NJ];
 #pragma unroll
@@ -102,47 +189,60 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(BalArgs a, int
   bool bad = false, bad_idx = false;
   const long long step = static_cast<long long>(gridDim.x) * kGroups;
   // every group of a warp makes the same number of rounds (shuffles)
-  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < a.T; base += step) {
-    const long long tok = base + grp;
-    const bool in = tok < a.T;
-    const bool valid = in && (!a.mask || a.mask[tok] != 0);
-    float l[4 * NJ];
-    bool bad_tok = false;
-    load_logits<L, NJ>(a.logits + tok * a.ld, g, a.E, in, vec != 0, l, &bad_tok);
-    bad = bad || (bad_tok && valid);
-    float top = -INFINITY;
+  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < a.T;
+       base += kUnroll * step) {
+    float l[kUnroll][4 * NJ];
+    int id[kUnroll][2];
+    bool in[kUnroll], valid[kUnroll];
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) top = fmaxf(top, l[i]);
-    top = group_max<L>(top);
-    float sum = 0.f;
-    const float ref = top == -INFINITY ? 0.f : top;
+    for (int u = 0; u < kUnroll; ++u) {  // all loads first
+      const long long tok = base + u * step + grp;
+      in[u] = tok < a.T;
+      load_logits<L, NJ>(a.logits + tok * a.ld, g, a.E, in[u], vec != 0, l[u]);
+      valid[u] = in[u] && (!a.mask || a.mask[tok] != 0);
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) {
-      l[i] = expf(l[i] - ref);
-      sum += l[i];
+      for (int s = 0; s < 2; ++s)  // (k <= 8 slots over at least 4 lanes)
+        id[u][s] = in[u] && g + s * L < a.k ? a.idx[tok * a.k + g + s * L] : -1;
     }
-    sum = group_sum<L>(sum);
-    const float lse = sum > 0.f ? ref + logf(sum) : -INFINITY;
-    if (in && g == 0) a.lse[tok] = lse;
-    if (valid) {
-      if (sum > 0.f) {
-        const float inv = 1.0f / sum;
 #pragma unroll
-        for (int i = 0; i < 4 * NJ; ++i) acc[i] = fmaf(l[i], inv, acc[i]);
-        if (g == 0) z = fmaf(lse, lse, z);
+    for (int u = 0; u < kUnroll; ++u) {
+      bad = (clean(l[u]) && valid[u]) || bad;
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) top = fmaxf(top, l[u][i]);
+      top = group_max<L>(top);
+      float sum = 0.f;
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) {
+        l[u][i] = expf(l[u][i] - ref);
+        sum += l[u][i];
       }
-      if (g == 0) ++n;
-      for (int s = g; s < a.k; s += L) {
-        const int e = a.idx[tok * a.k + s];
-        if (e >= 0 && e < a.E) atomicAdd(&s_cnt[e], 1);
-        else bad_idx = true;
+      sum = group_sum<L>(sum);
+      const float lse = sum > 0.f ? ref + logf(sum) : -INFINITY;
+      if (in[u] && g == 0) a.lse[base + u * step + grp] = lse;
+      if (valid[u]) {
+        if (sum > 0.f) {
+          const float inv = 1.0f / sum;
+#pragma unroll
+          for (int i = 0; i < 4 * NJ; ++i) acc[i] = fmaf(l[u][i], inv, acc[i]);
+          if (g == 0) z = fmaf(lse, lse, z);
+        }
+        if (g == 0) ++n;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (g + s * L >= a.k) break;
+          const int e = id[u][s];
+          if (e >= 0 && e < a.E) atomicAdd(&s_cnt[e], 1);
+          else bad_idx = true;
+        }
       }
     }
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_prob[grp * kEP + 4 * (g + L * j) + i] = acc[4 * j + i];
+    *reinterpret_cast<float4*>(s_prob + grp * kEP + 4 * (g + L * j)) =
+        make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
   if (g == 0) {
     s_z[grp] = z;
     s_n[grp] = n;
@@ -150,68 +250,38 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(BalArgs a, int
   if (bad) set_status(a.status, MOK_ERR_DEVICE_NONFINITE);
   if (bad_idx) set_status(a.status, MOK_ERR_DEVICE_INDEX);
   __syncthreads();
-  for (int e = t; e < a.E; e += kBalThreads) {
+  const int e_pad = (a.E + 3) / 4 * 4;
+  for (int e = t; e < e_pad; e += kFwdThreads) {
     float p = 0.f;
     for (int q = 0; q < kGroups; ++q) p += s_prob[q * kEP + e];
-    a.part_prob[static_cast<long long>(blockIdx.x) * a.E + e] = p;
-    a.part_cnt[static_cast<long long>(blockIdx.x) * a.E + e] = s_cnt[e];
+    a.part_prob[static_cast<long long>(blockIdx.x) * e_pad + e] = p;
+    a.part_cnt[static_cast<long long>(blockIdx.x) * e_pad + e] = s_cnt[e];
   }
-  if (t == 0) {
+  if (t < 32) {
     float zz = 0.f;
     int nn = 0;
-    for (int q = 0; q < kGroups; ++q) {
+    for (int q = t; q < kGroups; q += 32) {
       zz += s_z[q];
       nn += s_n[q];
     }
-    a.part_z[blockIdx.x] = zz;
-    a.part_n[blockIdx.x] = nn;
+    zz = group_sum<32>(zz);
+    nn = __reduce_add_sync(0xffffffffu, nn);
+    if (t == 0) {
+      a.part_z[blockIdx.x] = zz;
+      a.part_n[blockIdx.x] = nn;
+    }
   }
   // the last block to arrive adds the partials in block order
   __threadfence();
   __syncthreads();
-  if (t == 0) s_last = gridDim.x == 1 || atomicAdd(a.arrivals, 1) == static_cast<int>(gridDim.x) - 1;
+  if (t == 0)
+    s_last = gridDim.x == 1 || atomicAdd(a.arrivals, 1) == static_cast<int>(gridDim.x) - 1;
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  const int G = gridDim.x;
-  __shared__ float s_red[kBalThreads];
-  __shared__ int s_nall;
-  if (t == 0) {
-    float zz = 0.f;
-    int nn = 0;
-    for (int b = 0; b < G; ++b) {
-      zz += __ldcg(a.part_z + b);
-      nn += __ldcg(a.part_n + b);
-    }
-    s_nall = nn;
-    a.n_valid[0] = nn;
-    // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
-    a.loss[1] = nn > 0 && a.z_coef != 0.f ? a.z_coef * zz / static_cast<float>(nn) : 0.f;
-  }
-  __syncthreads();
-  const float inv_n = s_nall > 0 ? 1.0f / static_cast<float>(s_nall) : 0.f;
-  float dot = 0.f;
-  for (int e = t; e < a.E; e += kBalThreads) {
-    float p = 0.f;
-    int c = 0;
-#pragma unroll 8
-    for (int b = 0; b < G; ++b) {
-      p += __ldcg(a.part_prob + static_cast<long long>(b) * a.E + e);
-      c += __ldcg(a.part_cnt + static_cast<long long>(b) * a.E + e);
-    }
-    p *= inv_n;
-    a.prob[e] = p;
-    a.counts[e] = c;
-    dot = fmaf(static_cast<float>(c), p, dot);
-  }
-  s_red[t] = dot;
-  __syncthreads();
-  for (int o = kBalThreads / 2; o > 0; o >>= 1) {
-    if (t < o) s_red[t] += s_red[t + o];
-    __syncthreads();
-  }
-  if (t == 0)
-    a.loss[0] = a.balance_coef * static_cast<float>(a.E) / static_cast<float>(a.k) * s_red[0] * inv_n;
+  static_assert(sizeof(float4) * kFwdThreads * 2 <= sizeof(s_prob), "the slices fit");
+  float4* s_f4 = reinterpret_cast<float4*>(s_prob);
+  balance_finish(a, gridDim.x, s_f4, reinterpret_cast<int4*>(s_f4 + kFwdThreads), s_red);
 }
 
 struct BalBwd {
@@ -225,60 +295,72 @@ struct BalBwd {
 };
 
 template <int L, int NJ>
-__global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(BalBwd a, int vec) {
-  constexpr int kGroups = kBalThreads / L;
+__global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalBwd a, int vec) {
+  constexpr int kGroups = kBwdThreads / L;
   const int t = threadIdx.x, g = t & (L - 1), grp = t / L;
-  const int nv = *a.n_valid;
-  const float inv_n = nv > 0 ? 1.0f / static_cast<float>(nv) : 0.f;
-  // balance: A (f_e - 1/E), with f_e - 1/E = (c_e E - N k) / (N k E) exact in
-  // the integer numerator; subtracting the constant 1/E changes nothing (sum
-  // of P = 1) and keeps the difference f_e - sum f P from cancelling
-  const float A = a.dloss[0] * a.balance_coef * inv_n * inv_n / static_cast<float>(a.k);
-  const float Z = a.dloss[1] * 2.0f * a.z_coef * inv_n;
-  float f[4 * NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = 4 * (g + L * j) + i;
-      f[4 * j + i] = e < a.E ? static_cast<float>(static_cast<long long>(a.counts[e]) * a.E -
-                                                  static_cast<long long>(nv) * a.k) * A
-                             : 0.f;
-    }
   const long long step = static_cast<long long>(gridDim.x) * kGroups;
-  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < a.T; base += step) {
-    const long long tok = base + grp;
-    const bool in = tok < a.T;
-    const bool valid = in && (!a.mask || a.mask[tok] != 0);
-    float l[4 * NJ];
-    bool bad = false;
-    load_logits<L, NJ>(a.logits + tok * a.ld, g, a.E, in, vec != 0, l, &bad);
-    const float lse = in ? a.lse[tok] : 0.f;
-    const bool some = valid && lse > -INFINITY;
-    float dot = 0.f;
+  float f[4 * NJ];
+  float Z = 0.f;
+  for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < a.T;
+       base += kUnroll * step) {
+    float l[kUnroll][4 * NJ], lse[kUnroll];
+    bool in[kUnroll], some[kUnroll];
 #pragma unroll
-    for (int i = 0; i < 4 * NJ; ++i) {
-      l[i] = some ? expf(l[i] - lse) : 0.f;
-      dot = fmaf(f[i], l[i], dot);
+    for (int u = 0; u < kUnroll; ++u) {  // all loads first
+      const long long tok = base + u * step + grp;
+      in[u] = tok < a.T;
+      load_logits<L, NJ>(a.logits + tok * a.ld, g, a.E, in[u], vec != 0, l[u]);
+      lse[u] = in[u] ? a.lse[tok] : -INFINITY;
+      some[u] = in[u] && (!a.mask || a.mask[tok] != 0);
     }
-    dot = group_sum<L>(dot);
-    const float c = some ? Z * lse - dot : 0.f;
-    float* row = a.dlogits + tok * a.ld;
+    if (base == static_cast<long long>(blockIdx.x) * kGroups) {
+      // (after the first tokens' loads have gone out)
+      // balance: A (f_e - 1/E), with f_e - 1/E = (c_e E - N k) / (N k E) exact
+      // in the integer numerator; subtracting the constant 1/E changes nothing
+      // (sum of P = 1) and keeps the difference f_e - sum f P from cancelling
+      const int nv = *a.n_valid;
+      const float inv_n = nv > 0 ? 1.0f / static_cast<float>(nv) : 0.f;
+      const float A = a.dloss[0] * a.balance_coef * inv_n * inv_n / static_cast<float>(a.k);
+      Z = a.dloss[1] * 2.0f * a.z_coef * inv_n;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int e = 4 * (g + L * j);
-      float4 o;
-      o.x = l[4 * j] * (f[4 * j] + c);
-      o.y = l[4 * j + 1] * (f[4 * j + 1] + c);
-      o.z = l[4 * j + 2] * (f[4 * j + 2] + c);
-      o.w = l[4 * j + 3] * (f[4 * j + 3] + c);
-      if (in && vec && e < a.E) {
-        *reinterpret_cast<float4*>(row + e) = o;
-      } else if (in) {
-        if (e < a.E) row[e] = o.x;
-        if (e + 1 < a.E) row[e + 1] = o.y;
-        if (e + 2 < a.E) row[e + 2] = o.z;
-        if (e + 3 < a.E) row[e + 3] = o.w;
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 4 * (g + L * j) + i;
+          f[4 * j + i] = e < a.E ? static_cast<float>(static_cast<long long>(a.counts[e]) * a.E -
+                                                      static_cast<long long>(nv) * a.k) * A
+                                 : 0.f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      clean(l[u]);
+      some[u] = some[u] && lse[u] > -INFINITY;
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) {
+        l[u][i] = some[u] ? expf(l[u][i] - lse[u]) : 0.f;
+        dot = fmaf(f[i], l[u][i], dot);
+      }
+      dot = group_sum<L>(dot);
+      const float c = some[u] ? Z * lse[u] - dot : 0.f;
+      float* row = a.dlogits + (base + u * step + grp) * a.ld;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int e = 4 * (g + L * j);
+        float4 o;
+        o.x = l[u][4 * j] * (f[4 * j] + c);
+        o.y = l[u][4 * j + 1] * (f[4 * j + 1] + c);
+        o.z = l[u][4 * j + 2] * (f[4 * j + 2] + c);
+        o.w = l[u][4 * j + 3] * (f[4 * j + 3] + c);
+        if (in[u] && vec && e < a.E) {
+          *reinterpret_cast<float4*>(row + e) = o;
+        } else if (in[u]) {
+          if (e < a.E) row[e] = o.x;
+          if (e + 1 < a.E) row[e + 1] = o.y;
+          if (e + 2 < a.E) row[e + 2] = o.z;
+          if (e + 3 < a.E) row[e + 3] = o.w;
+        }
       }
     }
   }
@@ -306,18 +388,22 @@ bool vec4(const void* p, long long ld, int E) {
 }  // namespace
 
 int64_t balance_blocks(const mok_balance_desc& D) {
-  const int64_t groups = kBalThreads / lanes_of(D.E);
-  const int64_t b = (D.T + groups - 1) / groups;
-  return b < 1 ? 1 : (b < 152 ? b : 152);  // whatever the device: the sums do not depend on it
+  // tokens of a block in one round; up to four rounds one block alone is
+  // faster than several, their counter's reset and their last one's sum
+  const int64_t round = kUnroll * (kFwdThreads / lanes_of(D.E));
+  if (D.T <= 4 * round) return 1;
+  const int64_t b = (D.T + round / kUnroll - 1) / (round / kUnroll);
+  return b < kFwdBlocks ? b : kFwdBlocks;
 }
 
 void balance_layout(const mok_balance_desc& D, BalanceWs* W) {
   const size_t G = static_cast<size_t>(balance_blocks(D));
   auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   W->arrivals = 0;
+  const size_t e_pad = (static_cast<size_t>(D.E) + 3) / 4 * 4;
   W->part_prob = 256;
-  W->part_cnt = W->part_prob + al(G * D.E * 4);
-  W->part_z = W->part_cnt + al(G * D.E * 4);
+  W->part_cnt = W->part_prob + al(G * e_pad * 4);
+  W->part_z = W->part_cnt + al(G * e_pad * 4);
   W->part_n = W->part_z + al(G * 4);
   W->total = W->part_n + al(G * 4);
 }
@@ -348,7 +434,7 @@ cudaError_t launch_balance_fwd(const mok_balance_desc& D, const float* logits,
   const int vec = vec4(logits, a.ld, a.E);
   ProfScope prof("router_balance", st);
   by_width(D.E, [&](auto L, auto NJ) {
-    balance_fwd_kernel<decltype(L)::value, decltype(NJ)::value><<<grid, kBalThreads, 0, st>>>(a, vec);
+    balance_fwd_kernel<decltype(L)::value, decltype(NJ)::value><<<grid, kFwdThreads, 0, st>>>(a, vec);
   });
   count_launch();
   return cudaGetLastError();
@@ -364,14 +450,14 @@ cudaError_t launch_balance_bwd(const mok_balance_desc& D, const float* dloss,
   a.mask = mask; a.dlogits = dlogits;
   a.T = D.T; a.ld = D.ld_logits; a.E = D.E; a.k = D.k;
   a.balance_coef = D.balance_coef; a.z_coef = D.z_coef;
-  const int64_t groups = kBalThreads / lanes_of(D.E);
-  const int64_t need = (D.T + groups - 1) / groups;
-  const int64_t cap = 8LL * num_sms_current_device();
+  const int64_t round = kUnroll * (kBwdThreads / lanes_of(D.E));
+  const int64_t need = (D.T + round - 1) / round;
+  const int64_t cap = 4LL * num_sms_current_device();
   const unsigned grid = static_cast<unsigned>(need < cap ? need : cap);
   const int vec = vec4(logits, a.ld, a.E) && vec4(dlogits, a.ld, a.E);
   ProfScope prof("router_balance_bwd", st);
   by_width(D.E, [&](auto L, auto NJ) {
-    balance_bwd_kernel<decltype(L)::value, decltype(NJ)::value><<<grid, kBalThreads, 0, st>>>(a, vec);
+    balance_bwd_kernel<decltype(L)::value, decltype(NJ)::value><<<grid, kBwdThreads, 0, st>>>(a, vec);
   });
   count_launch();
   return cudaGetLastError();

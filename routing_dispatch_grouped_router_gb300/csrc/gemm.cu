@@ -659,7 +659,7 @@ __device__ __forceinline__ void stage_and_store_bf16_rows32(uint8_t* buf, const 
 
 // The dense product's epilogue of one 32-column chunk: v = C's values of this
 // lane's row, columns x ..; tl's split writes its partial at rows e * m_rows.
-template <int EPI>
+template <int EPI, bool DBUF>
 __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, int q, int lane,
                                              int x, float (&v)[32], uint8_t* stage_buf,
                                              uint32_t& nst, const CUtensorMap* tmC,
@@ -676,7 +676,7 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, 
     }
   }
   if (a.store_z) {
-    if (EPI == EPI_LIN_F32) stage_and_store_f32(stage_buf, nst, tmH, v, lane, x, y);
+    if (EPI == EPI_LIN_F32) stage_and_store_f32<DBUF>(stage_buf, nst, tmH, v, lane, x, y);
     else stage_and_store_bf16_rows32(stage_buf, tmH, v, lane, x, y);
   }
   if (a.act != MOK_ACT_NONE) {
@@ -710,7 +710,7 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, 
     }
   }
   if (EPI == EPI_LIN_F32)
-    stage_and_store_f32(stage_buf, nst, tmC, v, lane, x, y, a.accumulate != 0);
+    stage_and_store_f32<DBUF>(stage_buf, nst, tmC, v, lane, x, y, a.accumulate != 0);
   else
     stage_and_store_bf16_rows32(stage_buf, tmC, v, lane, x, y);
 }
@@ -728,7 +728,7 @@ __device__ __forceinline__ void linear_tile(const GemmArgs& a, const Tile& tl, u
     if (col0 + c >= a.n_valid) break;
     float v[32];
     tmem_ld32(taddr + half * (BN / 2) + c, v);
-    linear_chunk<EPI>(a, tl, q, lane, col0 + c, v, stage_buf, nst, tmC, tmH);
+    linear_chunk<EPI, false>(a, tl, q, lane, col0 + c, v, stage_buf, nst, tmC, tmH);
   }
 }
 
@@ -1193,9 +1193,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kDbuf = DB;
   constexpr bool kChunks = EPI == EPI_LIN_F32;
   static_assert(!DB || ((EPI == EPI_F32 || EPI == EPI_F32_T) && SCHED == SCHED_KGROUP) ||
-                    (EPI == EPI_SWIGLU_BWD && PAIR),
-                "DB: double-buffered staging of the fp32 weight gradients, or the SwiGLU "
-                "backward's stores from registers");
+                    (EPI == EPI_SWIGLU_BWD && PAIR) || EPI == EPI_LIN_F32,
+                "DB: double-buffered staging of the fp32 weight gradients or the dense "
+                "product's fp32 results, or the SwiGLU backward's stores from registers");
   static_assert(!PAIR || ((SCHED != SCHED_DENSE || linear_epi(EPI)) && SPLIT != SPLIT_B && BN == 256),
                 "pair");
   static_assert(!linear_epi(EPI) || SCHED == SCHED_DENSE, "the dense product");
@@ -1653,7 +1653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
-          linear_chunk<EPI>(args, tl, q, lane, col0 + c, v, stage_buf, nst, &tmC, &om.h);
+          linear_chunk<EPI, kDbuf>(args, tl, q, lane, col0 + c, v, stage_buf, nst, &tmC, &om.h);
         }
         continue;
       }
@@ -2478,6 +2478,8 @@ cudaError_t launch_router_logits(const Dims& D, const void* x, const void* w_rou
 
 // ---------------------------------------------------- the dense product --
 
+constexpr int kShortKb = 8;
+
 // A DENSE launch of the dense product's GEMMs, C [M, N] = A B (split s of a
 // split-K product at rows s * M): 256 x 256 tiles on CTA pairs when C has more
 // than one row tile (a pair's second CTA would have no rows otherwise), else
@@ -2498,6 +2500,12 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
   if (!(B_MN ? make_map(&tb, B, a.n_valid, K, ld_b, 64)
              : make_map(&tb, B, K, a.n_valid, ld_b, pair ? 128 : bn)))
     return cudaErrorInvalidValue;
+  if constexpr (EPI == EPI_LIN_F32) {
+    // few K blocks: the stores set the pace, so their staging is doubled
+    if (pair && a.num_kb <= kShortKb)
+      return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true, true>(
+          name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
+  }
   if (pair)
     return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true>(
         name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);

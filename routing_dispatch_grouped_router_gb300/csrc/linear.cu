@@ -22,6 +22,7 @@ namespace mok {
 
 namespace {
 
+constexpr int kEngineTiles = 38;
 constexpr int kLinThreads = 192;  // TMA warp, MMA warp, four epilogue warps
 
 template <int BN>
@@ -29,8 +30,8 @@ struct LinCfg {
   static constexpr int A_BYTES = 128 * 64 * 2;
   static constexpr int B_BYTES = BN * 64 * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // two CTAs per SM up to 64 tokens
-  static constexpr int ROOM = BN <= 64 ? 108 * 1024 : 220 * 1024;
+  // one CTA per SM: few tokens want as many weights in flight as fit
+  static constexpr int ROOM = 220 * 1024;
   static constexpr int STAGES = ROOM / STAGE_BYTES;
   static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
@@ -337,8 +338,7 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   if (nt > 65535 || mt > 65535) return cudaErrorInvalidConfiguration;
   // K splits: as many as the CTAs that fit at once leave room for, at least
   // four 64-value blocks each
-  const int64_t slots = static_cast<int64_t>(num_sms_current_device()) * (BN <= 64 ? 2 : 1);
-  int64_t ks = slots / (nt * mt);
+  int64_t ks = num_sms_current_device() / (nt * mt);
   if (ks > 8) ks = 8;
   if (ks > a.nkb / 4) ks = a.nkb / 4;
   if (ks < 1) ks = 1;
@@ -382,7 +382,10 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
   const uintptr_t bits = reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(res) |
                          reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(z);
   a.vec = D.N % 4 == 0 && (bits & 15) == 0;
-  if (D.M > 128 && D.N % 8 == 0 && (bits & 15) == 0)
+  // the persistent engine's 256 x 256 tiles need enough of them to fill its CTA
+  // pairs; below that the tiles here, and their split of K, spread wider
+  const int64_t pair_tiles = ((D.M + 255) / 256) * ((D.N + 255) / 256);
+  if (D.M > 128 && pair_tiles >= kEngineTiles && D.N % 8 == 0 && (bits & 15) == 0)
     return gemm_linear_fwd(D.M, D.N, D.K, D.ld_x, x, w, bias, res, D.act, y, z, f32, status, st);
   if (D.M <= 16) return f32 ? run_linear<16, true>(D, x, w, a, st) : run_linear<16, false>(D, x, w, a, st);
   if (D.M <= 64) return f32 ? run_linear<64, true>(D, x, w, a, st) : run_linear<64, false>(D, x, w, a, st);
@@ -401,80 +404,105 @@ struct DzArgs {
   int N, n_pad, act;
 };
 
-constexpr int kDzRows = 64;  // rows of a block: 8 for each of its 8 warps
+constexpr int kDzRows = 32;  // rows of a block
+
+// Eight consecutive elements of row r from column c.
+template <bool F32, bool VEC>
+struct Dz8 {
+  float f[8];
+  __device__ __forceinline__ void load(const void* base, long long r, int c, int N) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.f;
+    if (VEC) {
+      if (c >= N) return;
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + r * N + c);
+      const float4 x = __ldg(p), y = __ldg(p + 1);
+      f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+      f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < N) f[j] = load1<F32>(base, r * N + c + j);
+    }
+  }
+  __device__ __forceinline__ float get(int j) const { return f[j]; }
+};
+template <>
+struct Dz8<false, true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* base, long long r, int c, int N) {
+    u = make_uint4(0u, 0u, 0u, 0u);
+    if (c < N) u = ld_global_nc_v4(static_cast<const __nv_bfloat16*>(base) + r * N + c);
+  }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t w = j < 2 ? u.x : (j < 4 ? u.y : (j < 6 ? u.z : u.w));
+    return (j & 1) ? bf16hi(w) : bf16lo(w);
+  }
+};
 
 // dz = dy act'(z) as the sum of bf16 parts (each the rounding of what those
-// before it leave), and its column sums over the block's rows.  A block takes 256 columns, a lane 8 of them.
+// before it leave), and its column sums over the block's rows.  A block takes
+// kDzRows rows by 8 * `lanes` columns, a lane 8 columns of every 256/lanes-th
+// row, in batches of four rows whose loads are in flight together.
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
-  __shared__ float s_sum[8][256];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + lane * 8;
+__global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
+  __shared__ float s_sum[256 * 9];
+  grid_dep_launch();
+  const int l = threadIdx.x & (lanes - 1), row0 = threadIdx.x / lanes, rows = 256 / lanes;
+  const int c = (blockIdx.x * lanes + l) * 8;
+  const long long r0 = static_cast<long long>(blockIdx.y) * kDzRows;
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
-  for (int i = 0; i < kDzRows / 8; ++i) {
-    const long long r = static_cast<long long>(blockIdx.y) * kDzRows + i * 8 + warp;
-    if (r >= a.M || c >= a.n_pad) break;
-    float v[8], zz[8];
-    auto load = [&](const void* base, float (&o)[8]) {
-      if (VEC) {
-        if (c >= a.N) {
+  if (c < a.n_pad) {
+    for (int i0 = row0; i0 < kDzRows; i0 += 4 * rows) {
+      Dz8<F32, VEC> dy[4], z[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = 0.f;
-        } else if (F32) {
-          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + r * a.N + c);
-          const float4 x = __ldg(p), y = __ldg(p + 1);
-          o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
-          o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
-        } else {
-          const uint4 x = ld_global_nc_v4(static_cast<const __nv_bfloat16*>(base) + r * a.N + c);
-          o[0] = bf16lo(x.x); o[1] = bf16hi(x.x); o[2] = bf16lo(x.y); o[3] = bf16hi(x.y);
-          o[4] = bf16lo(x.z); o[5] = bf16hi(x.z); o[6] = bf16lo(x.w); o[7] = bf16hi(x.w);
+      for (int i = 0; i < 4; ++i) {
+        const int row = i0 + i * rows;
+        if (row < kDzRows && r0 + row < a.M) {
+          dy[i].load(a.dy, r0 + row, c, a.N);
+          if (a.act != MOK_ACT_NONE) z[i].load(a.z, r0 + row, c, a.N);
         }
-      } else {
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = i0 + i * rows;
+        if (row >= kDzRows || r0 + row >= a.M) break;
+        float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          o[j] = 0.f;
-          if (c + j < a.N)
-            o[j] = F32 ? static_cast<const float*>(base)[r * a.N + c + j]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[r * a.N + c + j]);
+          v[j] = dy[i].get(j);
+          if (a.act != MOK_ACT_NONE && c + j < a.N) v[j] *= act_slope(z[i].get(j), a.act);
+          sum[j] += v[j];
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          if (!a.dz[p]) break;
+          uint32_t h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float h0 = bf16_round(v[2 * j]), h1 = bf16_round(v[2 * j + 1]);
+            h[j] = pack_bf16x2(h0, h1);
+            // (an infinite value leaves nothing: inf - inf would be NaN)
+            v[2 * j] = isinf(h0) ? 0.f : v[2 * j] - h0;
+            v[2 * j + 1] = isinf(h1) ? 0.f : v[2 * j + 1] - h1;
+          }
+          st_global_v4(a.dz[p] + (r0 + row) * a.n_pad + c, make_uint4(h[0], h[1], h[2], h[3]));
         }
       }
-    };
-    load(a.dy, v);
-    if (a.act != MOK_ACT_NONE) {
-      load(a.z, zz);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < a.N) v[j] *= act_slope(zz[j], a.act);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += v[j];
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      if (!a.dz[p]) break;
-      uint32_t h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float h0 = bf16_round(v[2 * j]), h1 = bf16_round(v[2 * j + 1]);
-        h[j] = pack_bf16x2(h0, h1);
-        // (an infinite value leaves nothing: inf - inf would be NaN)
-        v[2 * j] = isinf(h0) ? 0.f : v[2 * j] - h0;
-        v[2 * j + 1] = isinf(h1) ? 0.f : v[2 * j + 1] - h1;
-      }
-      st_global_v4(a.dz[p] + r * a.n_pad + c, make_uint4(h[0], h[1], h[2], h[3]));
     }
   }
   if (!a.part) return;
+  // the row groups' sums of a column in order
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s_sum[warp][lane * 8 + j] = sum[j];
+  for (int j = 0; j < 8; ++j) s_sum[(row0 * lanes + l) * 9 + j] = sum[j];
   __syncthreads();
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col < a.N) {
+  for (int i = threadIdx.x; i < lanes * 8; i += 256) {
+    const int col = blockIdx.x * lanes * 8 + i;
+    if (col >= a.N) break;
     float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) t += s_sum[w][threadIdx.x];
+    for (int r = 0; r < rows; ++r) t += s_sum[(r * lanes + (i >> 3)) * 9 + (i & 7)];
     a.part[static_cast<long long>(blockIdx.y) * a.N + col] = t;
   }
 }
@@ -554,16 +582,17 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     a.N = static_cast<int>(D.N);
     a.n_pad = static_cast<int>(W.n_pad);
     a.act = D.act;
-    const dim3 grid(static_cast<unsigned>((W.n_pad + 255) / 256),
+    // lanes of a row: 8 columns each, up to a warp
+    const int lanes = W.n_pad >= 256 ? 32 : (W.n_pad > 64 ? 16 : 8);
+    const dim3 grid(static_cast<unsigned>((W.n_pad + lanes * 8 - 1) / (lanes * 8)),
                     static_cast<unsigned>(W.bias_rows));
-    if (grid.y > 65535u) return cudaErrorInvalidConfiguration;
     ProfScope prof("linear_dz", st);
     if (f32) {
-      if (vec) linear_dz_kernel<true, true><<<grid, 256, 0, st>>>(a);
-      else linear_dz_kernel<true, false><<<grid, 256, 0, st>>>(a);
+      if (vec) linear_dz_kernel<true, true><<<grid, 256, 0, st>>>(a, lanes);
+      else linear_dz_kernel<true, false><<<grid, 256, 0, st>>>(a, lanes);
     } else {
-      if (vec) linear_dz_kernel<false, true><<<grid, 256, 0, st>>>(a);
-      else linear_dz_kernel<false, false><<<grid, 256, 0, st>>>(a);
+      if (vec) linear_dz_kernel<false, true><<<grid, 256, 0, st>>>(a, lanes);
+      else linear_dz_kernel<false, false><<<grid, 256, 0, st>>>(a, lanes);
     }
     count_launch();
     const cudaError_t e = cudaGetLastError();

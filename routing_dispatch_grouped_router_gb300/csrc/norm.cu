@@ -422,32 +422,32 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_bwd_kernel(N
   }
 }
 
-// out[c] (+)= sum over g < n of part[g, c]: 32 columns per block, 8 threads of
-// each column take every eighth partial, then their sums in order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part,
-                                                         long long n, int d, float* out,
-                                                         int accumulate) {
-  __shared__ float s[8][33];
+// out[c] (+)= sum over g < n of part[g, c]: 32 columns per block, its 32 warps
+// take every 32nd partial (their loads in flight together: the latency of a
+// few loads bounds this), then their sums in order.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part,
+                                                          long long n, int d, float* out,
+                                                          int accumulate) {
+  __shared__ float s[32][33];
+  grid_dep_launch();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float acc = 0.f;
   if (c < d) {
-#pragma unroll 8
-    for (long long g = threadIdx.y; g < n; g += 8) acc += part[g * d + c];
+#pragma unroll 10
+    for (long long g = threadIdx.y; g < n; g += 32) acc += __ldg(part + g * d + c);
   }
   s[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
-  if (threadIdx.y == 0 && c < d) {
-    float v = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v += s[j][threadIdx.x];
-    out[c] = accumulate ? out[c] + v : v;
-  }
+  // column threadIdx.y, partial threadIdx.x
+  const float v = warp_sum(s[threadIdx.x][threadIdx.y]);
+  const int o = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && o < d) out[o] = accumulate ? out[o] + v : v;
 }
 
 cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* out,
                               bool accumulate, cudaStream_t st) {
   ProfScope prof("column_sum", st);
-  column_sum_kernel<<<static_cast<unsigned>((d + 31) / 32), dim3(32, 8), 0, st>>>(
+  column_sum_kernel<<<static_cast<unsigned>((d + 31) / 32), dim3(32, 32), 0, st>>>(
       part, n, static_cast<int>(d), out, accumulate ? 1 : 0);
   count_launch();
   return cudaGetLastError();
