@@ -423,11 +423,13 @@ mok_status mok_add_rmsnorm_forward(const mok_rmsnorm_desc* desc, const void* x,
  *   n = s rstd,  g = dy weight,  dx = rstd (g - n mean(g n)) + ds
  *   dweight [d] fp32 (+)= sum over rows of dy n, in a fixed order
  * dx [rows,d] (s_elem) is the gradient of x and of residual alike; it may
- * equal ds.  dweight NULL: not computed.  workspace: see the size query. */
+ * equal ds.  dweight NULL: not computed.  workspace: see the size query.
+ * status: as in mok_router_balance_forward; a bounded wait that gave up sets
+ * MOK_ERR_DEVICE_TIMEOUT. */
 mok_status mok_add_rmsnorm_backward(const mok_rmsnorm_desc* desc, const void* dy, const void* s,
                                     const void* weight, const void* ds, void* dx,
                                     float* dweight, void* workspace, size_t ws_bytes,
-                                    void* stream);
+                                    int32_t* status, void* stream);
 mok_status mok_add_rmsnorm_workspace_size(const mok_rmsnorm_desc* desc, size_t* bytes);
 
 typedef struct mok_balance_desc {

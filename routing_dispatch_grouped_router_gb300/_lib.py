@@ -82,7 +82,7 @@ _SIGS = {
                                  c_void_p]),
     "mok_add_rmsnorm_forward": (c_int32, [ctypes.POINTER(RmsnormDesc)] + [c_void_p] * 9),
     "mok_add_rmsnorm_backward": (c_int32, [ctypes.POINTER(RmsnormDesc)] + [c_void_p] * 7
-                                 + [c_size_t, c_void_p]),
+                                 + [c_size_t, c_void_p, c_void_p]),
     "mok_add_rmsnorm_workspace_size": (c_int32, [ctypes.POINTER(RmsnormDesc),
                                                  ctypes.POINTER(c_size_t)]),
     "mok_router_balance_forward": (c_int32, [ctypes.POINTER(BalanceDesc)] + [c_void_p] * 9

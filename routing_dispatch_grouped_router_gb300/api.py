@@ -360,7 +360,8 @@ def add_rmsnorm_backward(dy, s, weight, ds=None, eps=1e-6, *, dx=None, dweight=N
         workspace = _alloc((n,), torch.uint8, dy.device, stream)
     _lib.check(_lib.load().mok_add_rmsnorm_backward(desc, _addr(dy), _addr(s), _addr(weight),
                                                     _addr(ds), _addr(dx), _addr(dweight),
-                                                    _addr(workspace), workspace.nbytes, st),
+                                                    _addr(workspace), workspace.nbytes,
+                                                    _addr(operator_status(dy.device)), st),
                "mok_add_rmsnorm_backward")
     return dx, dweight
 

@@ -2,8 +2,7 @@
 // the tanh form of gelu are both z sigmoid(a(z)):
 //   silu: a = z;  gelu: a = 2 sqrt(2/pi) (z + 0.044715 z^3)
 //   (z sigmoid(a))' = sig + z sig (1 - sig) a'
-// The sigmoid through the hardware exponential and a correctly rounded
-// reciprocal, as in the experts' SwiGLU.
+// The sigmoid through the hardware exponential and reciprocal (2 and 1 ulp).
 #pragma once
 
 #include "../../include/mok.h"
@@ -14,7 +13,7 @@ constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluB = 0.044715f;
 
 __device__ __forceinline__ float act_sigmoid(float a) {
-  return __frcp_rn(1.0f + __expf(-a));
+  return __fdividef(1.0f, 1.0f + __expf(-a));
 }
 
 __device__ __forceinline__ float act_value(float z, int act) {

@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kFwdThreads = 512;
 constexpr int kBwdThreads = 256;
-// Tokens whose loads a group has in flight at once.
+// Tokens whose loads a group of the backward has in flight at once.
 constexpr int kUnroll = 2;
 // Blocks of the forward (one per SM of a GB300, whatever the device, so that
 // the sums do not depend on it).
@@ -94,89 +94,66 @@ __device__ __forceinline__ bool clean(float (&l)[N]) {
   return bad;
 }
 
-// The last block's work: the partials of G blocks added in block order by
-// slices (slice s takes blocks s, s + n, ..), then the losses.
-__device__ void balance_finish(const BalArgs& a, int G, float4* s_f4, int4* s_i4, float* s_red) {
-  const int t = threadIdx.x;
-  const int e4 = (a.E + 3) / 4;  // float4 columns, at most 128
-  int cols = 1;
-  while (cols < e4) cols *= 2;
-  const int n = kFwdThreads / cols;  // slices, at least 4
-  const int col = t & (cols - 1), sl = t / cols;
-  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
-  int4 c = make_int4(0, 0, 0, 0);
-  if (col < e4) {
-    const float4* pp = reinterpret_cast<const float4*>(a.part_prob) + col;
-    const int4* pc = reinterpret_cast<const int4*>(a.part_cnt) + col;
-#pragma unroll 10
-    for (int b = sl; b < G; b += n) {
-      const float4 q = __ldcg(pp + static_cast<long long>(b) * e4);
-      const int4 k = __ldcg(pc + static_cast<long long>(b) * e4);
-      p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
-      c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
-    }
+// Sums over the threads of a block: thread t holds float4 / int4 column
+// t % cols (a power of two) of slice t / cols, and z, n of its own.  On return
+// threads t < cols hold column t's sums, and every thread z's and n's.  A fixed
+// tree: lanes, then warps in order.
+__device__ __forceinline__ void block_columns(int cols, float4& p, int4& c, float& z, int& n,
+                                              float4* s_f4, int4* s_i4, float* s_z, int* s_n) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  constexpr int W = kFwdThreads / 32;
+  __syncthreads();  // the shared buffers are free
+  for (int o = 16; o >= cols; o >>= 1) {
+    p.x += __shfl_xor_sync(0xffffffffu, p.x, o);
+    p.y += __shfl_xor_sync(0xffffffffu, p.y, o);
+    p.z += __shfl_xor_sync(0xffffffffu, p.z, o);
+    p.w += __shfl_xor_sync(0xffffffffu, p.w, o);
+    c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
+    c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
+    c.z += __shfl_xor_sync(0xffffffffu, c.z, o);
+    c.w += __shfl_xor_sync(0xffffffffu, c.w, o);
   }
+  z = group_sum<32>(z);
+  n = __reduce_add_sync(0xffffffffu, n);
   s_f4[t] = p;
   s_i4[t] = c;
-  // z and N: a warp's lanes over the blocks, then the lanes in a fixed tree
-  float z = 0.f;
-  int nv = 0;
-  if (t < 32) {
-    for (int b = t; b < G; b += 32) {
-      z += __ldcg(a.part_z + b);
-      nv += __ldcg(a.part_n + b);
-    }
-    z = group_sum<32>(z);
-    nv = __reduce_add_sync(0xffffffffu, nv);
-    if (t == 0) {
-      s_red[0] = z;
-      s_red[1] = static_cast<float>(nv);  // (below 2^30; only its reciprocal is used)
-      a.n_valid[0] = nv;
-      // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
-      a.loss[1] = nv > 0 && a.z_coef != 0.f ? a.z_coef * z / static_cast<float>(nv) : 0.f;
-    }
+  if (lane == 0) {
+    s_z[warp] = z;
+    s_n[warp] = n;
   }
   __syncthreads();
-  const float inv_n = s_red[1] > 0.f ? 1.0f / s_red[1] : 0.f;
-  float dot = 0.f;
-  if (t < e4) {
-    for (int q = 1; q < n; ++q) {
-      const float4 f = s_f4[q * cols + t];
-      const int4 k = s_i4[q * cols + t];
+  if (t < cols) {  // warps (cols <= 32) or slices of several warps
+    const int step = cols < 32 ? 32 : cols;
+    p = make_float4(0.f, 0.f, 0.f, 0.f);
+    c = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int i = t; i < kFwdThreads; i += step) {
+      const float4 f = s_f4[i];
+      const int4 k = s_i4[i];
       p.x += f.x; p.y += f.y; p.z += f.z; p.w += f.w;
       c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
     }
-    const float pv[4] = {p.x * inv_n, p.y * inv_n, p.z * inv_n, p.w * inv_n};
-    const int cv[4] = {c.x, c.y, c.z, c.w};
+  }
+  z = 0.f;
+  n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * t + i < a.E) {
-        a.prob[4 * t + i] = pv[i];
-        a.counts[4 * t + i] = cv[i];
-        dot = fmaf(static_cast<float>(cv[i]), pv[i], dot);
-      }
-    }
+  for (int i = 0; i < W; ++i) {
+    z += s_z[i];
+    n += s_n[i];
   }
-  if (t < 128) {  // e4 <= 128: four warps hold every product
-    dot = group_sum<32>(dot);
-    if ((t & 31) == 0) s_red[2 + (t >> 5)] = dot;
-  }
-  __syncthreads();
-  if (t == 0)
-    a.loss[0] = a.balance_coef * static_cast<float>(a.E) / static_cast<float>(a.k) *
-                ((s_red[2] + s_red[3]) + (s_red[4] + s_red[5])) * inv_n;
 }
 
 template <int L, int NJ>
 __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int vec) {
   constexpr int kGroups = kFwdThreads / L;  // tokens of a block at a time
-  constexpr int kEP = 4 * L * NJ;           // E padded to the group's lanes
-  // the groups' sums, later the last block's slices (16 KB)
-  __shared__ __align__(16) float s_prob[kGroups * kEP < 4096 ? 4096 : kGroups * kEP];
+  constexpr int kE4 = L * NJ;               // float4 columns of the group's lanes
+  constexpr int U = NJ == 1 ? 4 : 2;        // tokens whose loads a group has in flight
+  __shared__ __align__(16) float4 s_prob[kGroups * kE4];
+  __shared__ float4 s_f4[kFwdThreads];
+  __shared__ int4 s_i4[kFwdThreads];
   __shared__ __align__(16) int32_t s_cnt[kMaxExperts];
-  __shared__ float s_z[kGroups];
-  __shared__ int32_t s_n[kGroups];
-  __shared__ float s_red[8];
+  __shared__ float s_z[kFwdThreads / 32];
+  __shared__ int s_n[kFwdThreads / 32];
   __shared__ int s_last;
   const int t = threadIdx.x, g = t & (L - 1), grp = t / L;
   for (int e = t; e < kMaxExperts; e += kFwdThreads) s_cnt[e] = 0;
@@ -190,12 +167,12 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
   const long long step = static_cast<long long>(gridDim.x) * kGroups;
   // every group of a warp makes the same number of rounds (shuffles)
   for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < a.T;
-       base += kUnroll * step) {
-    float l[kUnroll][4 * NJ];
-    int id[kUnroll][2];
-    bool in[kUnroll], valid[kUnroll];
+       base += U * step) {
+    float l[U][4 * NJ];
+    int id[U][2];
+    bool in[U], valid[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {  // all loads first
+    for (int u = 0; u < U; ++u) {  // all loads first
       const long long tok = base + u * step + grp;
       in[u] = tok < a.T;
       load_logits<L, NJ>(a.logits + tok * a.ld, g, a.E, in[u], vec != 0, l[u]);
@@ -205,7 +182,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
         id[u][s] = in[u] && g + s * L < a.k ? a.idx[tok * a.k + g + s * L] : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       bad = (clean(l[u]) && valid[u]) || bad;
       float top = -INFINITY;
 #pragma unroll
@@ -241,47 +218,87 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
-    *reinterpret_cast<float4*>(s_prob + grp * kEP + 4 * (g + L * j)) =
+    s_prob[grp * kE4 + g + L * j] =
         make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-  if (g == 0) {
-    s_z[grp] = z;
-    s_n[grp] = n;
-  }
   if (bad) set_status(a.status, MOK_ERR_DEVICE_NONFINITE);
   if (bad_idx) set_status(a.status, MOK_ERR_DEVICE_INDEX);
   __syncthreads();
-  const int e_pad = (a.E + 3) / 4 * 4;
-  for (int e = t; e < e_pad; e += kFwdThreads) {
-    float p = 0.f;
-    for (int q = 0; q < kGroups; ++q) p += s_prob[q * kEP + e];
-    a.part_prob[static_cast<long long>(blockIdx.x) * e_pad + e] = p;
-    a.part_cnt[static_cast<long long>(blockIdx.x) * e_pad + e] = s_cnt[e];
-  }
-  if (t < 32) {
-    float zz = 0.f;
-    int nn = 0;
-    for (int q = t; q < kGroups; q += 32) {
-      zz += s_z[q];
-      nn += s_n[q];
+  // the groups' sums: slices of the threads over the float4 columns
+  const int e4 = (a.E + 3) / 4;
+  int cols = 1;
+  while (cols < e4) cols *= 2;
+  const int col = t & (cols - 1), sl = t / cols, slices = kFwdThreads / cols;
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+  int4 c = make_int4(0, 0, 0, 0);
+  if (col < e4) {
+    for (int q = sl; q < kGroups; q += slices) {
+      const float4 f = s_prob[q * kE4 + col];
+      p.x += f.x; p.y += f.y; p.z += f.z; p.w += f.w;
     }
-    zz = group_sum<32>(zz);
-    nn = __reduce_add_sync(0xffffffffu, nn);
+    if (sl == 0) c = *reinterpret_cast<const int4*>(s_cnt + 4 * col);
+  }
+  block_columns(cols, p, c, z, n, s_f4, s_i4, s_z, s_n);
+  if (gridDim.x > 1) {
+    // this block's partials; the last block to arrive adds them in block order
+    float4* pp = reinterpret_cast<float4*>(a.part_prob);
+    int4* pc = reinterpret_cast<int4*>(a.part_cnt);
+    if (t < e4) {
+      pp[static_cast<long long>(blockIdx.x) * e4 + t] = p;
+      pc[static_cast<long long>(blockIdx.x) * e4 + t] = c;
+    }
     if (t == 0) {
-      a.part_z[blockIdx.x] = zz;
-      a.part_n[blockIdx.x] = nn;
+      a.part_z[blockIdx.x] = z;
+      a.part_n[blockIdx.x] = n;
+    }
+    __threadfence();
+    __syncthreads();
+    if (t == 0) s_last = atomicAdd(a.arrivals, 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const int G = gridDim.x;  // at most kFwdBlocks, fewer than the threads
+    z = t < G ? __ldcg(a.part_z + t) : 0.f;
+    n = t < G ? __ldcg(a.part_n + t) : 0;
+    p = make_float4(0.f, 0.f, 0.f, 0.f);
+    c = make_int4(0, 0, 0, 0);
+    if (col < e4) {
+#pragma unroll 10
+      for (int b = sl; b < G; b += slices) {
+        const float4 q = __ldcg(pp + static_cast<long long>(b) * e4 + col);
+        const int4 k = __ldcg(pc + static_cast<long long>(b) * e4 + col);
+        p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
+        c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
+      }
+    }
+    block_columns(cols, p, c, z, n, s_f4, s_i4, s_z, s_n);
+  }
+  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
+  float dot = 0.f;
+  if (t < e4) {
+    const float pv[4] = {p.x * inv_n, p.y * inv_n, p.z * inv_n, p.w * inv_n};
+    const int cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * t + i < a.E) {
+        a.prob[4 * t + i] = pv[i];
+        a.counts[4 * t + i] = cv[i];
+        dot = fmaf(static_cast<float>(cv[i]), pv[i], dot);
+      }
     }
   }
-  // the last block to arrive adds the partials in block order
-  __threadfence();
+  __syncthreads();  // s_z has been read
+  if (t < 128) {  // e4 <= 128: four warps hold every product
+    dot = group_sum<32>(dot);
+    if ((t & 31) == 0) s_z[t >> 5] = dot;
+  }
   __syncthreads();
-  if (t == 0)
-    s_last = gridDim.x == 1 || atomicAdd(a.arrivals, 1) == static_cast<int>(gridDim.x) - 1;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  static_assert(sizeof(float4) * kFwdThreads * 2 <= sizeof(s_prob), "the slices fit");
-  float4* s_f4 = reinterpret_cast<float4*>(s_prob);
-  balance_finish(a, gridDim.x, s_f4, reinterpret_cast<int4*>(s_f4 + kFwdThreads), s_red);
+  if (t == 0) {
+    a.n_valid[0] = n;
+    a.loss[0] = a.balance_coef * static_cast<float>(a.E) / static_cast<float>(a.k) *
+                ((s_z[0] + s_z[1]) + (s_z[2] + s_z[3])) * inv_n;
+    // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
+    a.loss[1] = n > 0 && a.z_coef != 0.f ? a.z_coef * z * inv_n : 0.f;
+  }
 }
 
 struct BalBwd {
@@ -388,11 +405,11 @@ bool vec4(const void* p, long long ld, int E) {
 }  // namespace
 
 int64_t balance_blocks(const mok_balance_desc& D) {
-  // tokens of a block in one round; up to four rounds one block alone is
-  // faster than several, their counter's reset and their last one's sum
-  const int64_t round = kUnroll * (kFwdThreads / lanes_of(D.E));
-  if (D.T <= 4 * round) return 1;
-  const int64_t b = (D.T + round / kUnroll - 1) / (round / kUnroll);
+  // up to eight tokens per group, one block alone is faster than several, their
+  // counter's reset and their last one's sum
+  const int64_t groups = kFwdThreads / lanes_of(D.E);
+  if (D.T <= 8 * groups) return 1;
+  const int64_t b = (D.T + groups - 1) / groups;
   return b < kFwdBlocks ? b : kFwdBlocks;
 }
 

@@ -95,14 +95,15 @@ mok_status mok_add_rmsnorm_workspace_size(const mok_rmsnorm_desc* desc, size_t* 
 mok_status mok_add_rmsnorm_backward(const mok_rmsnorm_desc* desc, const void* dy, const void* s,
                                     const void* weight, const void* ds, void* dx,
                                     float* dweight, void* workspace, size_t ws_bytes,
-                                    void* stream) {
+                                    int32_t* status, void* stream) {
   mok_rmsnorm_desc D;
   mok_status st = norm_desc(desc, &D);
   if (st != MOK_OK) return st;
   if (!weight || (D.rows > 0 && (!dy || !s || !dx))) return MOK_ERR_INVALID_ARG;
   const size_t se = elem_size(D.s_elem);
   if (!aligned(dy, elem_size(D.x_elem)) || !aligned(s, se) || !aligned(ds, se) ||
-      !aligned(dx, se) || !aligned(weight, elem_size(D.weight_elem)) || !aligned(dweight, 4))
+      !aligned(dx, se) || !aligned(weight, elem_size(D.weight_elem)) || !aligned(dweight, 4) ||
+      !aligned(status, 4))
     return MOK_ERR_INVALID_ARG;
   if (dweight && D.rows > 0) {
     if (!workspace || !aligned(workspace, 16)) return MOK_ERR_INVALID_ARG;
@@ -113,7 +114,7 @@ mok_status mok_add_rmsnorm_backward(const mok_rmsnorm_desc* desc, const void* dy
   st = mok_check_device();
   if (st != MOK_OK) return st;
   return cuda_status(launch_add_rmsnorm_bwd(D, dy, s, weight, ds, dx, dweight,
-                                            static_cast<float*>(workspace),
+                                            static_cast<float*>(workspace), status,
                                             static_cast<cudaStream_t>(stream)));
 }
 

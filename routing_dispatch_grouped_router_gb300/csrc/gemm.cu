@@ -155,7 +155,7 @@ struct OutMaps {
   CUtensorMap dgu_hi, dgu_lo, p_hi, p_lo;
   // (SPLIT_A3: sfa is the third part of A, tmL the second)
   CUtensorMap sfa, sfb;
-  // (EPI_LIN_*: z, in 32 x 32 blocks as C's)
+  // (EPI_LIN_*: z, in blocks as C's)
   // SwiGLU forward with bf16 h: h [rows, I], 32 x 32 blocks of 64-byte rows
   // (64-byte swizzle); a zeroed map (no h, or h as MXFP8 codes) is unused
   CUtensorMap h;
@@ -214,7 +214,10 @@ constexpr int staging_bytes() {
 
 template <int BN, int SPLIT = SPLIT_NONE, bool PAIR = false, int STG = kStagingBytes>
 struct Cfg {
-  static constexpr int BM = 128, BK = 64;
+  // the three-part weight gradient on single CTAs: half K blocks, so that four
+  // stages fit
+  static constexpr int BM = 128, BK = SPLIT == SPLIT_A3 && !PAIR && BN == 256 ? 32 : 64;
+  static constexpr uint32_t MN_BLOCK = BK * 128;   // MN-major tiles: 64 values x BK rows
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of B staged by one CTA
   static constexpr int A_BYTES = BM * BK * 2;        // 16 KB
   static constexpr int B_BYTES = B_ROWS * BK * 2;    // 32 KB (BN=256) / 16 KB (BN=128 or PAIR)
@@ -271,7 +274,9 @@ static_assert(Cfg<256, SPLIT_MX, true>::STAGES == 5 &&
                   Cfg<256, SPLIT_MX, true>::STAGE_BYTES % 1024 == 0 &&
                   256 + 12 * Cfg<256, SPLIT_MX, true>::STAGES <= 512,
               "MXFP8 pair stages");
-static_assert(Cfg<256, SPLIT_A3, true>::STAGES == 3 && Cfg<128, SPLIT_A3>::STAGES == 3,
+static_assert(Cfg<256, SPLIT_A3, true>::STAGES == 3 && Cfg<128, SPLIT_A3>::STAGES == 3 &&
+                  Cfg<256, SPLIT_A3>::STAGES == 4 &&
+                  Cfg<256, SPLIT_A3, true, 2 * kStagingBytes>::STAGES == 2,
               "three-part stages");
 static_assert(Cfg<256, SPLIT_NONE, true, 2 * kStagingBytes>::STAGES == 5 &&
                   Cfg<256, SPLIT_NONE, false, 2 * kStagingBytes>::STAGES == 3 &&
@@ -657,9 +662,71 @@ __device__ __forceinline__ void stage_and_store_bf16_rows32(uint8_t* buf, const 
   }
 }
 
+// The dense product's epilogue when its stores set the pace (few K blocks per
+// tile): 64 fp32 or 128 bf16 columns leave TMEM, are staged and stored in one
+// go, so that the waits on TMEM, on the staging's readers and on the proxy fence
+// come once or twice a tile instead of four times.
+template <int BN, int EPI>
+__device__ __forceinline__ void linear_tile_wide(const GemmArgs& a, const Tile& tl,
+                                                 uint32_t taddr, int q, int lane, int half,
+                                                 uint8_t* stage_buf, const CUtensorMap* tmC) {
+  constexpr int kCols = EPI == EPI_LIN_F32 ? 64 : 128;  // 8 KB of staging
+  if (tl.row0 + q * 32 >= a.m_valid) return;
+  const int y = tl.e * a.m_rows + tl.row0 + q * 32;
+  const int col0 = tl.n_tile * BN + half * (BN / 2);
+#pragma unroll 1
+  for (int c = 0; c < BN / 2; c += kCols) {
+    const int x = col0 + c;
+    if (x >= a.n_valid) break;
+    uint32_t r[kCols / 16][16];
+#pragma unroll
+    for (int j = 0; j < kCols / 16; ++j) tmem_ld16(taddr + half * (BN / 2) + c + 16 * j, r[j]);
+    tmem_ld_wait();
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+    if constexpr (EPI == EPI_LIN_F32) {
+      // two 32 x 32 blocks of 128-byte rows (as stage_and_store_f32)
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        *reinterpret_cast<uint4*>(stage_buf + (j >> 3) * kStagingBytes + lane * 128 +
+                                  (((j & 7) ^ (lane & 7)) << 4)) =
+            make_uint4(r[j >> 2][4 * (j & 3)], r[j >> 2][4 * (j & 3) + 1],
+                       r[j >> 2][4 * (j & 3) + 2], r[j >> 2][4 * (j & 3) + 3]);
+    } else {
+      // two 32 x 64 blocks of 128-byte rows (as stage_and_store_bf16)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = pack_bf16x2(__uint_as_float(r[j >> 1][8 * (j & 1) + 2 * i]),
+                             __uint_as_float(r[j >> 1][8 * (j & 1) + 2 * i + 1]));
+        *reinterpret_cast<uint4*>(stage_buf + (j >> 3) * kStagingBytes + lane * 128 +
+                                  (((j & 7) ^ (lane & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      constexpr int kBlockCols = kCols / 2;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int xj = x + kBlockCols * j;
+        if (xj >= a.n_valid) break;
+        if (EPI == EPI_LIN_F32 && a.accumulate)
+          tma_reduce_add_2d(tmC, stage_buf + j * kStagingBytes, xj, y);
+        else
+          tma_store_2d(tmC, stage_buf + j * kStagingBytes, xj, y);
+      }
+      bulk_commit();
+    }
+  }
+}
+
 // The dense product's epilogue of one 32-column chunk: v = C's values of this
 // lane's row, columns x ..; tl's split writes its partial at rows e * m_rows.
-template <int EPI, bool DBUF>
+template <int EPI>
 __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, int q, int lane,
                                              int x, float (&v)[32], uint8_t* stage_buf,
                                              uint32_t& nst, const CUtensorMap* tmC,
@@ -676,7 +743,7 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, 
     }
   }
   if (a.store_z) {
-    if (EPI == EPI_LIN_F32) stage_and_store_f32<DBUF>(stage_buf, nst, tmH, v, lane, x, y);
+    if (EPI == EPI_LIN_F32) stage_and_store_f32(stage_buf, nst, tmH, v, lane, x, y);
     else stage_and_store_bf16_rows32(stage_buf, tmH, v, lane, x, y);
   }
   if (a.act != MOK_ACT_NONE) {
@@ -710,7 +777,7 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, 
     }
   }
   if (EPI == EPI_LIN_F32)
-    stage_and_store_f32<DBUF>(stage_buf, nst, tmC, v, lane, x, y, a.accumulate != 0);
+    stage_and_store_f32(stage_buf, nst, tmC, v, lane, x, y, a.accumulate != 0);
   else
     stage_and_store_bf16_rows32(stage_buf, tmC, v, lane, x, y);
 }
@@ -728,7 +795,7 @@ __device__ __forceinline__ void linear_tile(const GemmArgs& a, const Tile& tl, u
     if (col0 + c >= a.n_valid) break;
     float v[32];
     tmem_ld32(taddr + half * (BN / 2) + c, v);
-    linear_chunk<EPI, false>(a, tl, q, lane, col0 + c, v, stage_buf, nst, tmC, tmH);
+    linear_chunk<EPI>(a, tl, q, lane, col0 + c, v, stage_buf, nst, tmC, tmH);
   }
 }
 
@@ -787,7 +854,8 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& tl,
       }
     }
   } else if constexpr (linear_epi(EPI)) {
-    linear_tile<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, nst, tmC, tmH);
+    if constexpr (DBUF) linear_tile_wide<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, tmC);
+    else linear_tile<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, nst, tmC, tmH);
   } else if (EPI == EPI_F32_T || EPI == EPI_BF16_T) {
     // C^T through TMA: accumulator rows are output columns; C viewed as
     // [E * N, M] with group e's block at rows e*N
@@ -1191,14 +1259,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ GemmArgs args, const __grid_constant__ OutMaps om) {
   using C = Cfg<BN, SPLIT, PAIR, staging_bytes<EPI, SPLIT, SCHED, DB>()>;
   constexpr bool kDbuf = DB;
-  constexpr bool kChunks = EPI == EPI_LIN_F32;
+  constexpr bool kChunks = EPI == EPI_LIN_F32 && !DB;
   static_assert(!DB || ((EPI == EPI_F32 || EPI == EPI_F32_T) && SCHED == SCHED_KGROUP) ||
-                    (EPI == EPI_SWIGLU_BWD && PAIR) || EPI == EPI_LIN_F32,
-                "DB: double-buffered staging of the fp32 weight gradients or the dense "
-                "product's fp32 results, or the SwiGLU backward's stores from registers");
+                    (EPI == EPI_SWIGLU_BWD && PAIR) || linear_epi(EPI),
+                "DB: double-buffered staging of the fp32 weight gradients, the SwiGLU "
+                "backward's stores from registers, or the dense product's wide epilogue");
   static_assert(!PAIR || ((SCHED != SCHED_DENSE || linear_epi(EPI)) && SPLIT != SPLIT_B && BN == 256),
                 "pair");
   static_assert(!linear_epi(EPI) || SCHED == SCHED_DENSE, "the dense product");
+  static_assert(C::BK == 64 || (A_MN && B_MN && SCHED == SCHED_DENSE),
+                "half K blocks: MN-major operands");
   static_assert(SPLIT != SPLIT_MX ||
                     (!A_MN && !B_MN && BN == (PAIR ? 256 : 128) && SCHED == SCHED_MGROUP),
                 "MXFP8 operands: K-major, 128-wide tiles (256 on CTA pairs)");
@@ -1401,14 +1471,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (C::A_TILES > 1) load(sA + C::A_BYTES, &tmL, (tl.kb0 + kb) * KX, tl.row0);
             if (C::A_TILES > 2) load(sA + 2 * C::A_BYTES, &om.sfa, (tl.kb0 + kb) * KX, tl.row0);
           } else {
-            const int ky = SCHED == SCHED_KGROUP ? kgy : tl.k_row0 + (tl.kb0 + kb) * 64;
+            const int ky = SCHED == SCHED_KGROUP ? kgy : tl.k_row0 + (tl.kb0 + kb) * C::BK;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              load(sA + j * 8192, &tmA, tl.row0 + 64 * j, ky);
+              load(sA + j * C::MN_BLOCK, &tmA, tl.row0 + 64 * j, ky);
               if (C::A_TILES > 1)
-                load(sA + C::A_BYTES + j * 8192, &tmL, tl.row0 + 64 * j, ky);
+                load(sA + C::A_BYTES + j * C::MN_BLOCK, &tmL, tl.row0 + 64 * j, ky);
               if (C::A_TILES > 2)
-                load(sA + 2 * C::A_BYTES + j * 8192, &om.sfa, tl.row0 + 64 * j, ky);
+                load(sA + 2 * C::A_BYTES + j * C::MN_BLOCK, &om.sfa, tl.row0 + 64 * j, ky);
             }
           }
           // B tile: B_ROWS rows (N) x 64 (K); PAIR: this CTA's half of N
@@ -1430,13 +1500,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             int ky;
             if (SCHED == SCHED_KGROUP) ky = kgy;
-            else if (SCHED == SCHED_DENSE) ky = (tl.kb0 + kb) * 64;
+            else if (SCHED == SCHED_DENSE) ky = (tl.kb0 + kb) * C::BK;
             else ky = tl.e * args.b_group_rows + kb * 64;
             const int x0 = tl.n_tile * BN + rank * C::B_ROWS;
 #pragma unroll
             for (int j = 0; j < C::B_ROWS / 64; ++j) {
-              load(sB + j * 8192, &tmB, x0 + 64 * j, ky);
-              if (SPLIT == SPLIT_B) load(sB + C::B_BYTES + j * 8192, &tmL, x0 + 64 * j, ky);
+              load(sB + j * C::MN_BLOCK, &tmB, x0 + 64 * j, ky);
+              if (SPLIT == SPLIT_B) load(sB + C::B_BYTES + j * C::MN_BLOCK, &tmL, x0 + 64 * j, ky);
             }
           }
           issued_par[stage] = static_cast<int>(phase);
@@ -1465,8 +1535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA --
       constexpr uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, BN, A_MN, B_MN);
-      constexpr uint32_t lbo_a = A_MN ? 8192u : 16u;
-      constexpr uint32_t lbo_b = B_MN ? 8192u : 16u;
+      constexpr uint32_t lbo_a = A_MN ? C::MN_BLOCK : 16u;
+      constexpr uint32_t lbo_b = B_MN ? C::MN_BLOCK : 16u;
       constexpr uint32_t kstep_a = A_MN ? 2048u : 32u;
       constexpr uint32_t kstep_b = B_MN ? 2048u : 32u;
       auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t acc_in) {
@@ -1559,7 +1629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < C::BK / 16; ++j) {
               const uint64_t ad = smem_desc_sw128(a_base + j * kstep_a, lbo_a, 1024);
               const uint64_t bd = smem_desc_sw128(b_base + j * kstep_b, lbo_b, 1024);
               mma(d_tmem, ad, bd, ((kb - kb0) | j) != 0 ? 1u : 0u);
@@ -1653,7 +1723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
-          linear_chunk<EPI, kDbuf>(args, tl, q, lane, col0 + c, v, stage_buf, nst, &tmC, &om.h);
+          linear_chunk<EPI>(args, tl, q, lane, col0 + c, v, stage_buf, nst, &tmC, &om.h);
         }
         continue;
       }
@@ -2478,7 +2548,14 @@ cudaError_t launch_router_logits(const Dims& D, const void* x, const void* w_rou
 
 // ---------------------------------------------------- the dense product --
 
-constexpr int kShortKb = 8;
+constexpr int kWideKb = 8;
+
+// fp32 or bf16 C or z in 32 x 32 blocks; wide: bf16 in 32 x 64 ones
+static bool make_lin_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, bool f32,
+                         bool wide = false) {
+  if (f32) return make_out_map(m, base, cols, rows);
+  return wide ? make_out_map_bf16(m, base, cols, rows) : make_out_map_bf16_t(m, base, cols, rows);
+}
 
 // A DENSE launch of the dense product's GEMMs, C [M, N] = A B (split s of a
 // split-K product at rows s * M): 256 x 256 tiles on CTA pairs when C has more
@@ -2486,26 +2563,35 @@ constexpr int kShortKb = 8;
 // 128 x BN1 on single CTAs.  B: [N, K] (K-major) or [K, N].
 template <bool A_MN, bool B_MN, int EPI, int SPLIT>
 static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const void* B,
-                                int64_t K, int64_t ld_b, const CUtensorMap& tc, GemmArgs& a,
-                                cudaStream_t st, const CUtensorMap* tl, const OutMaps* om) {
-  constexpr int BN1 = SPLIT == SPLIT_A3 ? 128 : 256;  // (three stages of 128; two of 256)
+                                int64_t K, int64_t ld_b, GemmArgs& a, cudaStream_t st,
+                                const CUtensorMap* tl, const OutMaps* om) {
+  // three parts: 128 x 128 tiles of K-major operands (three stages; two of 256),
+  // 128 x 256 in half K blocks of MN-major ones
+  constexpr int BN1 = SPLIT == SPLIT_A3 && !A_MN ? 128 : 256;
   const bool pair = a.m_tiles > 1;
   const int bn = pair ? 256 : BN1;
   const int splits = a.k_splits > 1 ? a.k_splits : 1;
   a.E = 1;
   a.n_tiles = (a.n_valid + bn - 1) / bn;
-  a.num_kb = static_cast<int>(((K + 63) / 64 + splits - 1) / splits);
-  a.chunk_kb = kChunkMmas / (4 * Cfg<BN1, SPLIT>::A_TILES);
+  const int bk = pair ? 64 : Cfg<BN1, SPLIT>::BK;
+  a.num_kb = static_cast<int>(((K + bk - 1) / bk + splits - 1) / splits);
+  a.chunk_kb = kChunkMmas / (bk / 16 * Cfg<BN1, SPLIT>::A_TILES);
   CUtensorMap tb;
-  if (!(B_MN ? make_map(&tb, B, a.n_valid, K, ld_b, 64)
+  if (!(B_MN ? make_map(&tb, B, a.n_valid, K, ld_b, bk)
              : make_map(&tb, B, K, a.n_valid, ld_b, pair ? 128 : bn)))
     return cudaErrorInvalidValue;
-  if constexpr (EPI == EPI_LIN_F32) {
-    // few K blocks: the stores set the pace, so their staging is doubled
-    if (pair && a.num_kb <= kShortKb)
-      return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true, true>(
-          name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
-  }
+  const int parts = Cfg<BN1, SPLIT>::A_TILES;
+  const bool plain = !a.bias && !a.res && a.act == MOK_ACT_NONE && !a.store_z;
+  // short K: the stores set the pace (and an fp32 result is one accumulation)
+  const bool wide = pair && plain && a.num_kb * parts <= kWideKb &&
+                    (EPI != EPI_LIN_F32 || a.num_kb <= a.chunk_kb);
+  CUtensorMap tc;
+  if (!make_lin_map(&tc, a.out, a.n_valid, splits > 1 ? splits * a.m_rows : a.m_valid,
+                    EPI == EPI_LIN_F32, wide))
+    return cudaErrorInvalidValue;
+  if (wide)
+    return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true, true>(
+        name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
   if (pair)
     return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true>(
         name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
@@ -2513,22 +2599,16 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
       name, ta, tb, tc, a, a.m_tiles * a.n_tiles * splits, st, tl, om);
 }
 
-// 32 x 32 blocks of C or z, fp32 or bf16
-static bool make_lin_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
-                         bool f32) {
-  return f32 ? make_out_map(m, base, cols, rows) : make_out_map_bf16_t(m, base, cols, rows);
-}
-
 cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
                             const void* w, const float* bias, const void* res, int act, void* y,
                             void* z, bool f32, int* status, cudaStream_t st) {
-  CUtensorMap ta, tc;
-  if (!make_map(&ta, x, K, M, ld_x, 128) || !make_lin_map(&tc, y, N, M, f32))
-    return cudaErrorInvalidValue;
+  CUtensorMap ta;
+  if (!make_map(&ta, x, K, M, ld_x, 128)) return cudaErrorInvalidValue;
   OutMaps om;
   memset(&om, 0, sizeof(om));
   if (z && !make_lin_map(&om.h, z, N, M, f32)) return cudaErrorInvalidValue;
   GemmArgs a = blank_args(status);
+  a.out = y;
   a.m_tiles = (int)((M + 127) / 128);
   a.m_valid = (int)M;
   a.n_valid = (int)N;
@@ -2537,9 +2617,9 @@ cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const
   a.act = act;
   a.store_z = z ? 1 : 0;
   if (f32)
-    return dense_linear<false, false, EPI_LIN_F32, SPLIT_NONE>("linear", ta, w, K, K, tc, a, st,
+    return dense_linear<false, false, EPI_LIN_F32, SPLIT_NONE>("linear", ta, w, K, K, a, st,
                                                                nullptr, &om);
-  return dense_linear<false, false, EPI_LIN_BF16, SPLIT_NONE>("linear", ta, w, K, K, tc, a, st,
+  return dense_linear<false, false, EPI_LIN_BF16, SPLIT_NONE>("linear", ta, w, K, K, a, st,
                                                               nullptr, &om);
 }
 
@@ -2556,11 +2636,11 @@ static bool dz_maps(const BfParts& dz, int64_t M, int64_t N, uint32_t box_rows, 
 cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* w,
                            void* dx, bool f32, bool accumulate, int* status, cudaStream_t st) {
   // dx [M, K] = dz [M, N] w [N, K]: the reduction runs over N
-  CUtensorMap ta, tl, tc;
+  CUtensorMap ta, tl;
   OutMaps om;
-  if (!dz_maps(dz, M, N, 128, &ta, &tl, &om) || !make_lin_map(&tc, dx, K, M, f32))
-    return cudaErrorInvalidValue;
+  if (!dz_maps(dz, M, N, 128, &ta, &tl, &om)) return cudaErrorInvalidValue;
   GemmArgs a = blank_args(status);
+  a.out = dx;
   a.m_tiles = (int)((M + 127) / 128);
   a.m_valid = (int)M;
   a.n_valid = (int)K;
@@ -2568,15 +2648,15 @@ cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, c
   const char* name = "linear_dx";
   if (f32) {
     if (dz.n == 3)
-      return dense_linear<false, true, EPI_LIN_F32, SPLIT_A3>(name, ta, w, N, K, tc, a, st, &tl,
+      return dense_linear<false, true, EPI_LIN_F32, SPLIT_A3>(name, ta, w, N, K, a, st, &tl,
                                                               &om);
-    return dense_linear<false, true, EPI_LIN_F32, SPLIT_NONE>(name, ta, w, N, K, tc, a, st,
+    return dense_linear<false, true, EPI_LIN_F32, SPLIT_NONE>(name, ta, w, N, K, a, st,
                                                               nullptr, &om);
   }
   if (dz.n == 2)
-    return dense_linear<false, true, EPI_LIN_BF16, SPLIT_A>(name, ta, w, N, K, tc, a, st, &tl,
+    return dense_linear<false, true, EPI_LIN_BF16, SPLIT_A>(name, ta, w, N, K, a, st, &tl,
                                                             &om);
-  return dense_linear<false, true, EPI_LIN_BF16, SPLIT_NONE>(name, ta, w, N, K, tc, a, st,
+  return dense_linear<false, true, EPI_LIN_BF16, SPLIT_NONE>(name, ta, w, N, K, a, st,
                                                              nullptr, &om);
 }
 
@@ -2585,13 +2665,13 @@ cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, const BfParts& dz, c
                            cudaStream_t st) {
   // dw [N, K] = dz^T [N x M] x [M, K]: the reduction runs over the tokens,
   // `splits` partial products at rows s * (N padded to 128) of dw
-  CUtensorMap ta, tl, tc;
+  CUtensorMap ta, tl;
   OutMaps om;
   const int64_t n_pad = (N + 127) / 128 * 128;
-  if (!dz_maps(dz, M, N, 64, &ta, &tl, &om) ||
-      !make_out_map(&tc, dw, K, splits > 1 ? splits * n_pad : N))
-    return cudaErrorInvalidValue;
+  const uint32_t bk = n_pad > 128 || dz.n < 3 ? 64 : Cfg<256, SPLIT_A3>::BK;
+  if (!dz_maps(dz, M, N, bk, &ta, &tl, &om)) return cudaErrorInvalidValue;
   GemmArgs a = blank_args(status);
+  a.out = dw;
   a.m_tiles = (int)(n_pad / 128);
   a.k_splits = splits;
   a.m_rows = (int)n_pad;
@@ -2600,9 +2680,9 @@ cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, const BfParts& dz, c
   a.accumulate = accumulate ? 1 : 0;
   const char* name = "linear_dw";
   if (dz.n == 3)
-    return dense_linear<true, true, EPI_LIN_F32, SPLIT_A3>(name, ta, x, M, ld_x, tc, a, st, &tl,
+    return dense_linear<true, true, EPI_LIN_F32, SPLIT_A3>(name, ta, x, M, ld_x, a, st, &tl,
                                                            &om);
-  return dense_linear<true, true, EPI_LIN_F32, SPLIT_NONE>(name, ta, x, M, ld_x, tc, a, st,
+  return dense_linear<true, true, EPI_LIN_F32, SPLIT_NONE>(name, ta, x, M, ld_x, a, st,
                                                            nullptr, &om);
 }
 

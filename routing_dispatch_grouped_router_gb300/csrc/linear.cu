@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "act.cuh"
 #include "mok_internal.h"
 #include "ptx.cuh"
@@ -23,6 +25,7 @@ namespace mok {
 namespace {
 
 constexpr int kEngineTiles = 38;
+constexpr int kFewTokens = 8;
 constexpr int kLinThreads = 192;  // TMA warp, MMA warp, four epilogue warps
 
 template <int BN>
@@ -30,8 +33,9 @@ struct LinCfg {
   static constexpr int A_BYTES = 128 * 64 * 2;
   static constexpr int B_BYTES = BN * 64 * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // one CTA per SM: few tokens want as many weights in flight as fit
-  static constexpr int ROOM = 220 * 1024;
+  // two CTAs per SM up to 64 tokens: a cluster's CTAs then find room (with one
+  // CTA of 220 KB per SM, 16 clusters of 8 did not all fit at once)
+  static constexpr int ROOM = BN <= 64 ? 108 * 1024 : 220 * 1024;
   static constexpr int STAGES = ROOM / STAGE_BYTES;
   static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
@@ -122,6 +126,93 @@ __device__ __forceinline__ void finish4(const LinArgs& a, long long m, int n, fl
       if (a.res) t += load1<F32>(a.res, o + j);
       store1<F32>(a.y, o + j, t);
     }
+  }
+}
+
+// One output element (token m, feature n) from its sum.
+template <bool F32>
+__device__ __forceinline__ void finish1(const LinArgs& a, long long m, int n, float v) {
+  const long long o = m * a.N + n;
+  if (a.bias) v += a.bias[n];
+  if (a.z) store1<F32>(a.z, o, v);
+  v = act_value(v, a.act);
+  if (a.res) v += load1<F32>(a.res, o);
+  store1<F32>(a.y, o, v);
+}
+
+// Up to MT tokens, on the CUDA cores: bound by the bytes of w, which each
+// thread streams with 16-byte loads, as many in flight as its registers take;
+// no ring, tensor memory or cluster to set up (one token, N = 2048, K = 7168:
+// 13.5 us on the tensor cores).  A block takes R rows of w, its eight warps go
+// round the 256-value chunks of K, a lane eight values of each; the block's
+// sums are the lanes' (shuffles), then the warps' in order.
+constexpr int kFewThreads = 256;
+template <int MT, int R, bool F32>
+__global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
+    const __nv_bfloat16* __restrict__ x, long long ld_x, const __nv_bfloat16* __restrict__ w,
+    int K, LinArgs a) {
+  constexpr int U = 16 / R;  // chunks in flight
+  __shared__ float s_sum[8][R * MT];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n0 = blockIdx.x * R;
+  float acc[R][MT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = 0.f;
+  for (int c0 = warp * 256 + lane * 8; c0 < K; c0 += 8 * 256 * U) {
+    uint4 wv[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = c0 + u * 8 * 256;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        wv[u][r] = make_uint4(0u, 0u, 0u, 0u);
+        if (k < K && n0 + r < a.N)
+          wv[u][r] = ld_global_nc_v4(w + static_cast<long long>(n0 + r) * K + k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = c0 + u * 8 * 256;
+      if (k >= K) break;
+      float xf[MT][8];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint4 t = make_uint4(0u, 0u, 0u, 0u);
+        if (m < a.M) t = ld_global_nc_v4(x + m * ld_x + k);
+        xf[m][0] = bf16lo(t.x); xf[m][1] = bf16hi(t.x); xf[m][2] = bf16lo(t.y);
+        xf[m][3] = bf16hi(t.y); xf[m][4] = bf16lo(t.z); xf[m][5] = bf16hi(t.z);
+        xf[m][6] = bf16lo(t.w); xf[m][7] = bf16hi(t.w);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4 t = wv[u][r];
+        const float wf[8] = {bf16lo(t.x), bf16hi(t.x), bf16lo(t.y), bf16hi(t.y),
+                             bf16lo(t.z), bf16hi(t.z), bf16lo(t.w), bf16hi(t.w)};
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[r][m] = fmaf(wf[j], xf[m][j], acc[r][m]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float v = acc[r][m];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) s_sum[warp][m * R + r] = v;
+    }
+  __syncthreads();
+  if (threadIdx.x < R * MT) {
+    const int m = threadIdx.x / R, n = n0 + threadIdx.x % R;
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v += s_sum[q][threadIdx.x];
+    if (m < a.M && n < a.N) finish1<F32>(a, m, n, v);
   }
 }
 
@@ -338,7 +429,8 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   if (nt > 65535 || mt > 65535) return cudaErrorInvalidConfiguration;
   // K splits: as many as the CTAs that fit at once leave room for, at least
   // four 64-value blocks each
-  int64_t ks = num_sms_current_device() / (nt * mt);
+  const int64_t slots = static_cast<int64_t>(num_sms_current_device()) * (BN <= 64 ? 2 : 1);
+  int64_t ks = slots / (nt * mt);
   if (ks > 8) ks = 8;
   if (ks > a.nkb / 4) ks = a.nkb / 4;
   if (ks < 1) ks = 1;
@@ -387,6 +479,28 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
   const int64_t pair_tiles = ((D.M + 255) / 256) * ((D.N + 255) / 256);
   if (D.M > 128 && pair_tiles >= kEngineTiles && D.N % 8 == 0 && (bits & 15) == 0)
     return gemm_linear_fwd(D.M, D.N, D.K, D.ld_x, x, w, bias, res, D.act, y, z, f32, status, st);
+  if (D.M <= kFewTokens) {
+    ProfScope prof("linear_few", st);
+    const auto* xb = static_cast<const __nv_bfloat16*>(x);
+    const auto* wb = static_cast<const __nv_bfloat16*>(w);
+    const int K = static_cast<int>(D.K);
+    auto run = [&](auto MT, auto R, auto F) {
+      constexpr int r = decltype(R)::value;
+      linear_few_kernel<decltype(MT)::value, r, decltype(F)::value>
+          <<<static_cast<unsigned>((D.N + r - 1) / r), kFewThreads, 0, st>>>(xb, D.ld_x, wb, K, a);
+    };
+    auto by_tokens = [&](auto F) {
+      using std::integral_constant;
+      if (D.M == 1) run(integral_constant<int, 1>(), integral_constant<int, 4>(), F);
+      else if (D.M == 2) run(integral_constant<int, 2>(), integral_constant<int, 4>(), F);
+      else if (D.M <= 4) run(integral_constant<int, 4>(), integral_constant<int, 4>(), F);
+      else run(integral_constant<int, 8>(), integral_constant<int, 8>(), F);
+    };
+    if (f32) by_tokens(std::true_type());
+    else by_tokens(std::false_type());
+    count_launch();
+    return cudaGetLastError();
+  }
   if (D.M <= 16) return f32 ? run_linear<16, true>(D, x, w, a, st) : run_linear<16, false>(D, x, w, a, st);
   if (D.M <= 64) return f32 ? run_linear<64, true>(D, x, w, a, st) : run_linear<64, false>(D, x, w, a, st);
   return f32 ? run_linear<128, true>(D, x, w, a, st) : run_linear<128, false>(D, x, w, a, st);
@@ -401,7 +515,7 @@ struct DzArgs {
   __nv_bfloat16* dz[3];    // parts [M, n_pad], zero past N (NULL: not stored)
   float* part;             // [ceil(M / kDzRows), N] column sums (NULL: none)
   long long M;
-  int N, n_pad, act;
+  int N, n_pad;
 };
 
 constexpr int kDzRows = 32;  // rows of a block
@@ -425,7 +539,10 @@ struct Dz8 {
         if (c + j < N) f[j] = load1<F32>(base, r * N + c + j);
     }
   }
-  __device__ __forceinline__ float get(int j) const { return f[j]; }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = f[j];
+  }
 };
 template <>
 struct Dz8<false, true> {
@@ -434,9 +551,9 @@ struct Dz8<false, true> {
     u = make_uint4(0u, 0u, 0u, 0u);
     if (c < N) u = ld_global_nc_v4(static_cast<const __nv_bfloat16*>(base) + r * N + c);
   }
-  __device__ __forceinline__ float get(int j) const {
-    const uint32_t w = j < 2 ? u.x : (j < 4 ? u.y : (j < 6 ? u.z : u.w));
-    return (j & 1) ? bf16hi(w) : bf16lo(w);
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    o[0] = bf16lo(u.x); o[1] = bf16hi(u.x); o[2] = bf16lo(u.y); o[3] = bf16hi(u.y);
+    o[4] = bf16lo(u.z); o[5] = bf16hi(u.z); o[6] = bf16lo(u.w); o[7] = bf16hi(u.w);
   }
 };
 
@@ -444,7 +561,7 @@ struct Dz8<false, true> {
 // before it leave), and its column sums over the block's rows.  A block takes
 // kDzRows rows by 8 * `lanes` columns, a lane 8 columns of every 256/lanes-th
 // row, in batches of four rows whose loads are in flight together.
-template <bool F32, bool VEC>
+template <bool F32, bool VEC, int ACT>
 __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
   __shared__ float s_sum[256 * 9];
   grid_dep_launch();
@@ -462,18 +579,20 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
         const int row = i0 + i * rows;
         if (row < kDzRows && r0 + row < a.M) {
           dy[i].load(a.dy, r0 + row, c, a.N);
-          if (a.act != MOK_ACT_NONE) z[i].load(a.z, r0 + row, c, a.N);
+          if (ACT != MOK_ACT_NONE) z[i].load(a.z, r0 + row, c, a.N);
         }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = i0 + i * rows;
         if (row >= kDzRows || r0 + row >= a.M) break;
-        float v[8];
+        // (past N dy and z are zeros, and so is dz)
+        float v[8], zz[8];
+        dy[i].get(v);
+        if (ACT != MOK_ACT_NONE) z[i].get(zz);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[j] = dy[i].get(j);
-          if (a.act != MOK_ACT_NONE && c + j < a.N) v[j] *= act_slope(z[i].get(j), a.act);
+          if (ACT != MOK_ACT_NONE) v[j] *= act_slope(zz[j], ACT);
           sum[j] += v[j];
         }
 #pragma unroll
@@ -482,13 +601,17 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
           uint32_t h[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float h0 = bf16_round(v[2 * j]), h1 = bf16_round(v[2 * j + 1]);
-            h[j] = pack_bf16x2(h0, h1);
-            // (an infinite value leaves nothing: inf - inf would be NaN)
-            v[2 * j] = isinf(h0) ? 0.f : v[2 * j] - h0;
-            v[2 * j + 1] = isinf(h1) ? 0.f : v[2 * j + 1] - h1;
+            h[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            v[2 * j] -= bf16lo(h[j]);
+            v[2 * j + 1] -= bf16hi(h[j]);
           }
           st_global_v4(a.dz[p] + (r0 + row) * a.n_pad + c, make_uint4(h[0], h[1], h[2], h[3]));
+          if (p == 0) {
+            // a value that is infinite (or NaN) in the first part leaves nothing:
+            // inf - inf would make the sum of the parts NaN
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = fabsf(v[j]) < INFINITY ? v[j] : 0.f;
+          }
         }
       }
     }
@@ -529,7 +652,7 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float4* __restrict
 // leave SMs for, at least eight 64-token blocks each.
 int dw_splits(const mok_linear_desc& D) {
   const int64_t mt = (D.N + 127) / 128;
-  const int64_t tiles = mt > 1 ? (mt + 1) / 2 * ((D.K + 255) / 256) : (D.K + 127) / 128;
+  const int64_t tiles = (mt + 1) / 2 * ((D.K + 255) / 256);
   const int64_t slots = mt > 1 ? 76 : 152;  // whatever the device: the sums do not depend on it
   const int64_t nkb = (D.M + 63) / 64;
   int64_t ks = slots / tiles;
@@ -581,19 +704,23 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     a.M = D.M;
     a.N = static_cast<int>(D.N);
     a.n_pad = static_cast<int>(W.n_pad);
-    a.act = D.act;
     // lanes of a row: 8 columns each, up to a warp
     const int lanes = W.n_pad >= 256 ? 32 : (W.n_pad > 64 ? 16 : 8);
     const dim3 grid(static_cast<unsigned>((W.n_pad + lanes * 8 - 1) / (lanes * 8)),
                     static_cast<unsigned>(W.bias_rows));
     ProfScope prof("linear_dz", st);
-    if (f32) {
-      if (vec) linear_dz_kernel<true, true><<<grid, 256, 0, st>>>(a, lanes);
-      else linear_dz_kernel<true, false><<<grid, 256, 0, st>>>(a, lanes);
-    } else {
-      if (vec) linear_dz_kernel<false, true><<<grid, 256, 0, st>>>(a, lanes);
-      else linear_dz_kernel<false, false><<<grid, 256, 0, st>>>(a, lanes);
-    }
+    auto run = [&](auto F, auto V, auto A) {
+      linear_dz_kernel<decltype(F)::value, decltype(V)::value, decltype(A)::value>
+          <<<grid, 256, 0, st>>>(a, lanes);
+    };
+    auto by_act = [&](auto F, auto V) {
+      if (D.act == MOK_ACT_NONE) run(F, V, std::integral_constant<int, MOK_ACT_NONE>());
+      else if (D.act == MOK_ACT_RELU) run(F, V, std::integral_constant<int, MOK_ACT_RELU>());
+      else if (D.act == MOK_ACT_SILU) run(F, V, std::integral_constant<int, MOK_ACT_SILU>());
+      else run(F, V, std::integral_constant<int, MOK_ACT_GELU>());
+    };
+    if (f32) vec ? by_act(std::true_type(), std::true_type()) : by_act(std::true_type(), std::false_type());
+    else vec ? by_act(std::false_type(), std::true_type()) : by_act(std::false_type(), std::false_type());
     count_launch();
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -270,7 +270,7 @@ cudaError_t launch_add_rmsnorm(const mok_rmsnorm_desc& D, const void* x, const v
 int64_t norm_bwd_blocks(const mok_rmsnorm_desc& D);  // partial weight gradients [.., d]
 cudaError_t launch_add_rmsnorm_bwd(const mok_rmsnorm_desc& D, const void* dy, const void* s,
                                    const void* w, const void* ds, void* dx, float* dweight,
-                                   float* part, cudaStream_t st);
+                                   float* part, int* status, cudaStream_t st);
 // out[c] (+)= sum over g < n of part[g, c], c < d, in a fixed order
 cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* out,
                               bool accumulate, cudaStream_t st);
@@ -379,6 +379,24 @@ cudaError_t launch_nv_quant_tiled(const void* in, long long rows, long long cols
 cudaError_t launch_bounded_wait_selftest(int* status, cudaStream_t st);
 // zeroes `bytes` (a multiple of 16) at 16-byte aligned dst with bulk stores
 cudaError_t launch_fill_zero(void* dst, size_t bytes, cudaStream_t st);
+
+// A launch that may start while the kernel before it on the stream drains (its
+// grid_dep_wait holds it back from that kernel's results): the launch's own
+// latency then overlaps the other's tail.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t st,
+                             A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
 
 // launches counter (host side)
 void count_launch(int n = 1);

@@ -324,7 +324,9 @@ cudaError_t launch_add_rmsnorm(const mok_rmsnorm_desc& D, const void* x, const v
 
 // ----------------------------------------------------------------- backward --
 
+constexpr int kBulkMaxDepth = 4;
 struct NormBwd {
+  int* status;
   const void *dy, *s, *w, *ds;
   void* dx;
   float* part;  // [gridDim.x, d] partial weight gradients (NULL: not computed)
@@ -333,33 +335,47 @@ struct NormBwd {
   float inv_d, eps;
 };
 
-// Block b takes rows b, b + gridDim.x, ..; its threads keep the weight
-// gradient of their columns in registers over those rows.
+// The three inputs of a thread's vectors of one row.
 template <bool DYF32, bool SF32, bool VEC, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_bwd_kernel(NormBwd a) {
-  __shared__ float red[2][2][32];  // [row parity][sum][warp]
+struct BwdRow {
+  Raw8<SF32, VEC> s[NV], ds[NV];
+  Raw8<DYF32, VEC> dy[NV];
+  __device__ __forceinline__ void load(const NormBwd& a, long long r, int t, int tpr) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vi = t + i * tpr;
+      s[i].zero();
+      dy[i].zero();
+      ds[i].zero();
+      if (r < a.rows && vi < a.nvec) {
+        s[i].load(row_at<SF32>(a.s, r, a.ld_s), vi, a.d);
+        dy[i].load(row_at<DYF32>(a.dy, r, a.ld_dy), vi, a.d);
+        if (a.ds) ds[i].load(row_at<SF32>(a.ds, r, a.ld_ds), vi, a.d);
+      }
+    }
+  }
+};
+
+// blockDim.x threads of whole warps hold a row, blockDim.y rows are in a block
+// at a time (more than one only for rows of one warp).  Row group b takes rows
+// b, b + groups, ..; its threads keep the weight gradient of their columns in
+// registers over those rows.
+template <bool DYF32, bool SF32, bool VEC, int NV>
+__global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(NormBwd a) {
+  __shared__ float red[2][2][16];  // [row parity][sum][warp]
+  __shared__ float s_dw[8][256];
+  grid_dep_launch();
   const int t = threadIdx.x, tpr = blockDim.x, nw = tpr >> 5;
   float dw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-  int par = 0;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, par ^= 1) {
-    Raw8<SF32, VEC> rs[NV], rd[NV];
-    Raw8<DYF32, VEC> ry[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int vi = t + i * tpr;
-      rs[i].zero();
-      ry[i].zero();
-      rd[i].zero();
-      if (vi < a.nvec) {
-        rs[i].load(row_at<SF32>(a.s, r, a.ld_s), vi, a.d);
-        ry[i].load(row_at<DYF32>(a.dy, r, a.ld_dy), vi, a.d);
-        if (a.ds) rd[i].load(row_at<SF32>(a.ds, r, a.ld_ds), vi, a.d);
-      }
-    }
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  for (int par = 0; r < a.rows; r += step, par ^= 1) {
+    BwdRow<DYF32, SF32, VEC, NV> row;
+    row.load(a, r, t, tpr);
     float ss = 0.f, gs = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -368,8 +384,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_bwd_kernel(N
         float w[8], s[8], dy[8];
         if (a.w_f32) load8<true, VEC>(a.w, vi, a.d, w);
         else load8<false, VEC>(a.w, vi, a.d, w);
-        rs[i].get(s);
-        ry[i].get(dy);
+        row.s[i].get(s);
+        row.dy[i].get(dy);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           ss = fmaf(s[j], s[j], ss);
@@ -398,9 +414,9 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_bwd_kernel(N
       float w[8], s[8], dy[8], o[8];
       if (a.w_f32) load8<true, VEC>(a.w, vi, a.d, w);
       else load8<false, VEC>(a.w, vi, a.d, w);
-      rs[i].get(s);
-      ry[i].get(dy);
-      rd[i].get(o);
+      row.s[i].get(s);
+      row.dy[i].get(dy);
+      row.ds[i].get(o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         o[j] = rstd * (dy[j] * w[j] - s[j] * c) + o[j];
@@ -411,6 +427,17 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_bwd_kernel(N
   }
   if (!a.part) return;
   float* p = a.part + static_cast<long long>(blockIdx.x) * a.d;
+  if (blockDim.y > 1) {  // rows of one warp, NV = 1: the block's rows in order
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_dw[threadIdx.y][t * 8 + j] = dw[0][j];
+    __syncthreads();
+    const int i = threadIdx.y * 32 + t;  // vector i / 8, element i % 8
+    float v = 0.f;
+    for (int y = 0; y < 8; ++y) v += s_dw[y][i];
+    const int e = elem_of<VEC>(i >> 3, i & 7);
+    if ((i >> 3) < a.nvec && e < a.d) p[e] = v;
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int vi = t + i * tpr;
@@ -422,6 +449,127 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_bwd_kernel(N
   }
 }
 
+// The same for aligned rows of at least kBulkMinD elements: rows come into a
+// ring of `depth` rows in shared memory by bulk copies (s, dy, ds each one
+// copy), issued a row or more ahead, so that the reductions and barriers of one
+// row do not interrupt the stream of loads.  A slot is filled again after the
+// next row's barrier, which every thread reaches only when done with it.
+constexpr int kBulkMinD = 1024;
+template <bool DYF32, bool SF32, int NV>
+__global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, int depth) {
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  __shared__ __align__(8) uint64_t full[kBulkMaxDepth];
+  __shared__ float red[2][2][16];
+  __shared__ int s_abort;
+  grid_dep_launch();
+  const int t = threadIdx.x, tpr = blockDim.x, nw = tpr >> 5;
+  const uint32_t s_bytes = a.d * (SF32 ? 4 : 2), y_bytes = a.d * (DYF32 ? 4 : 2);
+  const uint32_t row_bytes = s_bytes + y_bytes + (a.ds ? s_bytes : 0);
+  if (t == 0) {
+    for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  volatile int* vabort = &s_abort;
+  auto fill = [&](int slot, long long r) {  // thread 0
+    uint8_t* p = s_rows + slot * row_bytes;
+    mbar_arrive_expect_tx(&full[slot], row_bytes);
+    bulk_load(p, row_at<SF32>(a.s, r, a.ld_s), s_bytes, &full[slot]);
+    bulk_load(p + s_bytes, row_at<DYF32>(a.dy, r, a.ld_dy), y_bytes, &full[slot]);
+    if (a.ds) bulk_load(p + s_bytes + y_bytes, row_at<SF32>(a.ds, r, a.ld_ds), s_bytes, &full[slot]);
+  };
+  const long long step = gridDim.x;
+  int filled = 0;  // thread 0: rows requested
+  if (t == 0) {
+    for (long long r = blockIdx.x; filled < depth && r < a.rows; r += step) fill(filled++, r);
+  }
+  float dw[NV][8], w[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vi = t + i * tpr;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = w[i][j] = 0.f;
+    if (vi < a.nvec) {
+      if (a.w_f32) load8<true, true>(a.w, vi, a.d, w[i]);
+      else load8<false, true>(a.w, vi, a.d, w[i]);
+    }
+  }
+  int it = 0;
+  for (long long r = blockIdx.x; r < a.rows; r += step, ++it) {
+    const int slot = it % depth;
+    const uint8_t* p = s_rows + slot * row_bytes;
+    if (!mbar_wait(&full[slot], static_cast<uint32_t>((it / depth) & 1), vabort)) {
+      *vabort = 1;
+      set_status(a.status, MOK_ERR_DEVICE_TIMEOUT);
+    }
+    float ss = 0.f, gs = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vi = t + i * tpr;
+      if (vi < a.nvec) {
+        float s[8], dy[8];
+        load8<SF32, true>(p, vi, a.d, s);
+        load8<DYF32, true>(p + s_bytes, vi, a.d, dy);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ss = fmaf(s[j], s[j], ss);
+          gs = fmaf(dy[j] * w[i][j], s[j], gs);
+        }
+      }
+    }
+    ss = warp_sum(ss);
+    gs = warp_sum(gs);
+    const int par = it & 1;
+    if ((t & 31) == 0) {
+      red[par][0][t >> 5] = ss;
+      red[par][1][t >> 5] = gs;
+    }
+    __syncthreads();  // (the other parity's buffer may still be read)
+    if (*vabort) break;  // (set before the barrier: every thread sees it)
+    if (t == 0 && it > 0) {  // the row before is done with its slot
+      const long long next = r + (depth - 1) * step;
+      if (next < a.rows) fill((it - 1) % depth, next);
+    }
+    const bool in = (t & 31) < nw;
+    ss = warp_sum(in ? red[par][0][t & 31] : 0.f);
+    gs = warp_sum(in ? red[par][1][t & 31] : 0.f);
+    const float rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+    const float c = gs * rstd * rstd * a.inv_d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vi = t + i * tpr;
+      if (vi >= a.nvec) continue;
+      float s[8], dy[8], o[8];
+      load8<SF32, true>(p, vi, a.d, s);
+      load8<DYF32, true>(p + s_bytes, vi, a.d, dy);
+      if (a.ds) {
+        load8<SF32, true>(p + s_bytes + y_bytes, vi, a.d, o);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[j] = rstd * (dy[j] * w[i][j] - s[j] * c) + o[j];
+        dw[i][j] = fmaf(dy[j], s[j] * rstd, dw[i][j]);
+      }
+      store8<SF32, true>(row_at<SF32>(a.dx, r, a.ld_dx), vi, a.d, o);
+    }
+  }
+  if (*vabort) {
+    spin_ns(1000000ull);  // copies in flight land before the block leaves
+    return;
+  }
+  if (!a.part) return;
+  float* out = a.part + static_cast<long long>(blockIdx.x) * a.d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int vi = t + i * tpr;
+    if (vi < a.nvec) store8<true, true>(out, vi, a.d, dw[i]);
+  }
+}
+
 // out[c] (+)= sum over g < n of part[g, c]: 32 columns per block, its 32 warps
 // take every 32nd partial (their loads in flight together: the latency of a
 // few loads bounds this), then their sums in order.
@@ -430,11 +578,12 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
                                                           int accumulate) {
   __shared__ float s[32][33];
   grid_dep_launch();
+  grid_dep_wait();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float acc = 0.f;
   if (c < d) {
 #pragma unroll 10
-    for (long long g = threadIdx.y; g < n; g += 32) acc += __ldg(part + g * d + c);
+    for (long long g = threadIdx.y; g < n; g += 32) acc += part[g * d + c];
   }
   s[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
@@ -447,42 +596,95 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* out,
                               bool accumulate, cudaStream_t st) {
   ProfScope prof("column_sum", st);
-  column_sum_kernel<<<static_cast<unsigned>((d + 31) / 32), dim3(32, 32), 0, st>>>(
-      part, n, static_cast<int>(d), out, accumulate ? 1 : 0);
+  const cudaError_t e =
+      launch_dependent(column_sum_kernel, dim3(static_cast<unsigned>((d + 31) / 32)),
+                       dim3(32, 32), st, part, n, d, out, accumulate ? 1 : 0);
   count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 namespace {
 
+// Threads of a row, rows of a block and blocks of the backward, by the
+// descriptor alone: the sums do not depend on the device.
+struct BwdShape {
+  int tpr, nv, rpb, depth;
+  int64_t blocks;
+};
+constexpr int kBulkSmem = 216 * 1024;  // of an SM's shared memory, for all its blocks
+BwdShape bwd_shape(int64_t rows, int64_t d, bool vec, int64_t row_bytes) {
+  const int nvec = static_cast<int>(vec ? d / 8 : (d + 255) / 256 * 32);
+  BwdShape b;
+  b.nv = nvec <= 32 ? 1 : (nvec <= 1024 ? 2 : 4);
+  b.tpr = ((nvec + b.nv - 1) / b.nv + 31) / 32 * 32;
+  b.rpb = b.nv == 1 ? 8 : 1;
+  b.depth = 0;
+  int per_sm = 768 / (b.tpr * b.rpb);
+  per_sm = per_sm < 1 ? 1 : (per_sm > 16 ? 16 : per_sm);
+  if (vec && d >= kBulkMinD) {
+    // a ring of at least three rows per block where that leaves two blocks
+    while (per_sm > 2 && per_sm * 3 * row_bytes > kBulkSmem) --per_sm;
+    while (per_sm > 1 && per_sm * 2 * row_bytes > kBulkSmem) --per_sm;
+    b.depth = static_cast<int>(kBulkSmem / per_sm / row_bytes);
+    if (b.depth > kBulkMaxDepth) b.depth = kBulkMaxDepth;
+  }
+  const int64_t need = (rows + b.rpb - 1) / b.rpb;
+  b.blocks = need < 152 * per_sm ? need : 152 * per_sm;
+  return b;
+}
+
+template <bool DYF32, bool SF32, int NV>
+cudaError_t bulk_launch(const NormBwd& a, const BwdShape& b, int64_t row_bytes, cudaStream_t st) {
+  auto kern = add_rmsnorm_bwd_bulk_kernel<DYF32, SF32, NV>;
+  const int smem = static_cast<int>(b.depth * row_bytes);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(b.blocks), b.tpr, smem, st>>>(a, b.depth);
+  return cudaGetLastError();
+}
+
 template <bool DYF32, bool SF32, bool VEC>
-cudaError_t bwd_launch(const NormBwd& a, int64_t grid, cudaStream_t st) {
-  int tpr, nv;
-  norm_shape(a.rows, a.nvec, 2, &tpr, &nv);
+cudaError_t bwd_launch(const NormBwd& a, int64_t row_bytes, cudaStream_t st) {
+  const BwdShape b = bwd_shape(a.rows, a.d, VEC, row_bytes);
   ProfScope prof("add_rmsnorm_bwd", st);
-  const unsigned g = static_cast<unsigned>(grid);
-  if (nv == 1) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 1><<<g, tpr, 0, st>>>(a);
-  else if (nv == 2) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 2><<<g, tpr, 0, st>>>(a);
-  else add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 4><<<g, tpr, 0, st>>>(a);
   count_launch();
+  if constexpr (VEC) {
+    // (with at least two rows in the ring: the next one's copy is under way)
+    if (b.depth >= 2)
+      return b.nv == 2 ? bulk_launch<DYF32, SF32, 2>(a, b, row_bytes, st)
+                       : bulk_launch<DYF32, SF32, 4>(a, b, row_bytes, st);
+  }
+  const unsigned g = static_cast<unsigned>(b.blocks);
+  const dim3 block(b.tpr, b.rpb);
+  if (b.nv == 1) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 1><<<g, block, 0, st>>>(a);
+  else if (b.nv == 2) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 2><<<g, block, 0, st>>>(a);
+  else add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 4><<<g, block, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 int64_t norm_bwd_blocks(const mok_rmsnorm_desc& D) {
-  const int64_t most = 4 * 152;  // whatever the device, so that the sums do not depend on it
-  return D.rows < most ? D.rows : most;
+  // the most that any alignment of the pointers leads to
+  const int64_t se = D.s_elem == MOK_ELEM_F32 ? 4 : 2, ye = D.x_elem == MOK_ELEM_F32 ? 4 : 2;
+  int64_t most = bwd_shape(D.rows, D.d, false, 0).blocks;
+  if (D.d % 8 == 0)
+    for (int skip = 0; skip < 2; ++skip) {
+      const int64_t b = bwd_shape(D.rows, D.d, true, D.d * (se * (1 + skip) + ye)).blocks;
+      if (b > most) most = b;
+    }
+  return most;
 }
 
 cudaError_t launch_add_rmsnorm_bwd(const mok_rmsnorm_desc& D, const void* dy, const void* s,
                                    const void* w, const void* ds, void* dx, float* dweight,
-                                   float* part, cudaStream_t st) {
+                                   float* part, int* status, cudaStream_t st) {
   const bool yf = D.x_elem == MOK_ELEM_F32, sf = D.s_elem == MOK_ELEM_F32;
-  const int64_t grid = norm_bwd_blocks(D);
   cudaError_t e = cudaSuccess;
-  if (grid > 0) {
+  int64_t grid = 0;
+  if (D.rows > 0) {
     NormBwd a;
+    a.status = status;
     a.dy = dy; a.s = s; a.w = w; a.ds = ds; a.dx = dx;
     a.part = dweight ? part : nullptr;
     a.rows = D.rows;
@@ -496,16 +698,18 @@ cudaError_t launch_add_rmsnorm_bwd(const mok_rmsnorm_desc& D, const void* dy, co
     const bool vec = a.d % 8 == 0 && vec_rows(dy, a.ld_dy, ye) && vec_rows(s, a.ld_s, se) &&
                      vec_rows(ds, a.ld_ds, se) && vec_rows(dx, a.ld_dx, se) && vec_rows(w, 0, 4);
     if (!vec) a.nvec = (a.d + 255) / 256 * 32;
+    const int64_t row_bytes = D.d * (se * (ds ? 2 : 1) + ye);
+    grid = bwd_shape(D.rows, D.d, vec, row_bytes).blocks;
     if (yf) {
-      if (sf) e = vec ? bwd_launch<true, true, true>(a, grid, st)
-                      : bwd_launch<true, true, false>(a, grid, st);
-      else e = vec ? bwd_launch<true, false, true>(a, grid, st)
-                   : bwd_launch<true, false, false>(a, grid, st);
+      if (sf) e = vec ? bwd_launch<true, true, true>(a, row_bytes, st)
+                      : bwd_launch<true, true, false>(a, row_bytes, st);
+      else e = vec ? bwd_launch<true, false, true>(a, row_bytes, st)
+                   : bwd_launch<true, false, false>(a, row_bytes, st);
     } else {
-      if (sf) e = vec ? bwd_launch<false, true, true>(a, grid, st)
-                      : bwd_launch<false, true, false>(a, grid, st);
-      else e = vec ? bwd_launch<false, false, true>(a, grid, st)
-                   : bwd_launch<false, false, false>(a, grid, st);
+      if (sf) e = vec ? bwd_launch<false, true, true>(a, row_bytes, st)
+                      : bwd_launch<false, true, false>(a, row_bytes, st);
+      else e = vec ? bwd_launch<false, false, true>(a, row_bytes, st)
+                   : bwd_launch<false, false, false>(a, row_bytes, st);
     }
   }
   if (e != cudaSuccess || !dweight) return e;
