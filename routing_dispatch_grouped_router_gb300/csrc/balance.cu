@@ -8,8 +8,9 @@
 // Bound by the bytes of the logits, and for small routers by the latency of
 // its launches.  L lanes hold a token's E logits (NJ chunks of 4 each), so
 // softmax and dot products are shuffles inside the warp; the sums over tokens
-// stay in registers, then shared memory, then per-block partials that the last
-// block to arrive adds in block order: no floating-point atomics.
+// stay in registers, then shared memory, then per-block partials that a second
+// kernel (launched while the first drains) adds in block order: no
+// floating-point atomics.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -22,7 +23,7 @@ namespace mok {
 
 namespace {
 
-constexpr int kFwdThreads = 512;
+constexpr int kFwdThreads = 1024;
 constexpr int kBwdThreads = 256;
 // Tokens whose loads a group of the backward has in flight at once.
 constexpr int kUnroll = 2;
@@ -37,11 +38,11 @@ struct BalArgs {
   float *loss, *prob, *lse;
   int32_t *counts, *n_valid;
   int* status;       // sticky device status (may be null)
-  int* arrivals;     // blocks done (zero before the launch)
   float* part_prob;  // [gridDim.x, E rounded up to 4]
   int32_t* part_cnt; // [gridDim.x, E rounded up to 4]
   float* part_z;     // [gridDim.x]
   int32_t* part_n;   // [gridDim.x]
+  int blocks;        // of the first kernel
   long long T, ld;
   int E, k;
   float balance_coef, z_coef;
@@ -143,21 +144,94 @@ __device__ __forceinline__ void block_columns(int cols, float4& p, int4& c, floa
   }
 }
 
+struct BalShared {
+  float4 f4[kFwdThreads];
+  int4 i4[kFwdThreads];
+  float z[kFwdThreads / 32];
+  int n[kFwdThreads / 32];
+};
+
+// Float4 columns of E, padded to a power of two.
+__device__ __forceinline__ int pow2_cols(int e4) {
+  int cols = 1;
+  while (cols < e4) cols *= 2;
+  return cols;
+}
+
+// The outputs from the column sums p, c of threads t < E/4 and z, n.
+__device__ __forceinline__ void balance_out(const BalArgs& a, float4 p, int4 c, float z, int n,
+                                            BalShared& s) {
+  const int t = threadIdx.x, e4 = (a.E + 3) / 4;
+  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
+  float dot = 0.f;
+  if (t < e4) {
+    const float pv[4] = {p.x * inv_n, p.y * inv_n, p.z * inv_n, p.w * inv_n};
+    const int cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * t + i < a.E) {
+        a.prob[4 * t + i] = pv[i];
+        a.counts[4 * t + i] = cv[i];
+        dot = fmaf(static_cast<float>(cv[i]), pv[i], dot);
+      }
+    }
+  }
+  __syncthreads();  // s.z has been read
+  if (t < 128) {  // E/4 <= 128: four warps hold every product
+    dot = group_sum<32>(dot);
+    if ((t & 31) == 0) s.z[t >> 5] = dot;
+  }
+  __syncthreads();
+  if (t == 0) {
+    a.n_valid[0] = n;
+    a.loss[0] = a.balance_coef * static_cast<float>(a.E) / static_cast<float>(a.k) *
+                ((s.z[0] + s.z[1]) + (s.z[2] + s.z[3])) * inv_n;
+    // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
+    a.loss[1] = n > 0 && a.z_coef != 0.f ? a.z_coef * z * inv_n : 0.f;
+  }
+}
+
+// The second kernel: one block adds the first one's partials in block order by
+// slices of its threads.
+__global__ void __launch_bounds__(kFwdThreads) balance_sum_kernel(BalArgs a) {
+  __shared__ BalShared s;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int t = threadIdx.x, e4 = (a.E + 3) / 4, cols = pow2_cols(e4);
+  const int col = t & (cols - 1), slices = kFwdThreads / cols, G = a.blocks;
+  float z = t < G ? a.part_z[t] : 0.f;  // (fewer blocks than threads)
+  int n = t < G ? a.part_n[t] : 0;
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+  int4 c = make_int4(0, 0, 0, 0);
+  if (col < e4) {
+    const float4* pp = reinterpret_cast<const float4*>(a.part_prob) + col;
+    const int4* pc = reinterpret_cast<const int4*>(a.part_cnt) + col;
+#pragma unroll 10
+    for (int b = t / cols; b < G; b += slices) {
+      const float4 q = pp[static_cast<long long>(b) * e4];
+      const int4 k = pc[static_cast<long long>(b) * e4];
+      p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
+      c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
+    }
+  }
+  block_columns(cols, p, c, z, n, s.f4, s.i4, s.z, s.n);
+  balance_out(a, p, c, z, n, s);
+}
+
 template <int L, int NJ>
 __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int vec) {
   constexpr int kGroups = kFwdThreads / L;  // tokens of a block at a time
   constexpr int kE4 = L * NJ;               // float4 columns of the group's lanes
-  constexpr int U = NJ == 1 ? 4 : 2;        // tokens whose loads a group has in flight
-  __shared__ __align__(16) float4 s_prob[kGroups * kE4];
-  __shared__ float4 s_f4[kFwdThreads];
-  __shared__ int4 s_i4[kFwdThreads];
+  // tokens whose loads a group has in flight (registers: 64 a thread)
+  constexpr int U = NJ == 1 ? 4 : (NJ == 2 ? 2 : 1);
+  extern __shared__ __align__(16) float4 s_prob[];  // [kGroups][kE4]
+  __shared__ BalShared s;
   __shared__ __align__(16) int32_t s_cnt[kMaxExperts];
-  __shared__ float s_z[kFwdThreads / 32];
-  __shared__ int s_n[kFwdThreads / 32];
-  __shared__ int s_last;
+  grid_dep_launch();
   const int t = threadIdx.x, g = t & (L - 1), grp = t / L;
-  for (int e = t; e < kMaxExperts; e += kFwdThreads) s_cnt[e] = 0;
+  if (t < kMaxExperts) s_cnt[t] = 0;
   __syncthreads();
+  grid_dep_wait();
   float acc[4 * NJ];
 #pragma unroll
   for (int i = 0; i < 4 * NJ; ++i) acc[i] = 0.f;
@@ -178,8 +252,8 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
       load_logits<L, NJ>(a.logits + tok * a.ld, g, a.E, in[u], vec != 0, l[u]);
       valid[u] = in[u] && (!a.mask || a.mask[tok] != 0);
 #pragma unroll
-      for (int s = 0; s < 2; ++s)  // (k <= 8 slots over at least 4 lanes)
-        id[u][s] = in[u] && g + s * L < a.k ? a.idx[tok * a.k + g + s * L] : -1;
+      for (int i = 0; i < 2; ++i)  // (k <= 8 slots over at least 4 lanes)
+        id[u][i] = in[u] && g + i * L < a.k ? a.idx[tok * a.k + g + i * L] : -1;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -207,9 +281,9 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
         }
         if (g == 0) ++n;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (g + s * L >= a.k) break;
-          const int e = id[u][s];
+        for (int i = 0; i < 2; ++i) {
+          if (g + i * L >= a.k) break;
+          const int e = id[u][i];
           if (e >= 0 && e < a.E) atomicAdd(&s_cnt[e], 1);
           else bad_idx = true;
         }
@@ -224,9 +298,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
   if (bad_idx) set_status(a.status, MOK_ERR_DEVICE_INDEX);
   __syncthreads();
   // the groups' sums: slices of the threads over the float4 columns
-  const int e4 = (a.E + 3) / 4;
-  int cols = 1;
-  while (cols < e4) cols *= 2;
+  const int e4 = (a.E + 3) / 4, cols = pow2_cols(e4);
   const int col = t & (cols - 1), sl = t / cols, slices = kFwdThreads / cols;
   float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
   int4 c = make_int4(0, 0, 0, 0);
@@ -237,67 +309,19 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
     }
     if (sl == 0) c = *reinterpret_cast<const int4*>(s_cnt + 4 * col);
   }
-  block_columns(cols, p, c, z, n, s_f4, s_i4, s_z, s_n);
-  if (gridDim.x > 1) {
-    // this block's partials; the last block to arrive adds them in block order
-    float4* pp = reinterpret_cast<float4*>(a.part_prob);
-    int4* pc = reinterpret_cast<int4*>(a.part_cnt);
-    if (t < e4) {
-      pp[static_cast<long long>(blockIdx.x) * e4 + t] = p;
-      pc[static_cast<long long>(blockIdx.x) * e4 + t] = c;
-    }
-    if (t == 0) {
-      a.part_z[blockIdx.x] = z;
-      a.part_n[blockIdx.x] = n;
-    }
-    __threadfence();
-    __syncthreads();
-    if (t == 0) s_last = atomicAdd(a.arrivals, 1) == static_cast<int>(gridDim.x) - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const int G = gridDim.x;  // at most kFwdBlocks, fewer than the threads
-    z = t < G ? __ldcg(a.part_z + t) : 0.f;
-    n = t < G ? __ldcg(a.part_n + t) : 0;
-    p = make_float4(0.f, 0.f, 0.f, 0.f);
-    c = make_int4(0, 0, 0, 0);
-    if (col < e4) {
-#pragma unroll 10
-      for (int b = sl; b < G; b += slices) {
-        const float4 q = __ldcg(pp + static_cast<long long>(b) * e4 + col);
-        const int4 k = __ldcg(pc + static_cast<long long>(b) * e4 + col);
-        p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
-        c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
-      }
-    }
-    block_columns(cols, p, c, z, n, s_f4, s_i4, s_z, s_n);
+  block_columns(cols, p, c, z, n, s.f4, s.i4, s.z, s.n);
+  if (gridDim.x == 1) {
+    balance_out(a, p, c, z, n, s);
+    return;
   }
-  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
-  float dot = 0.f;
+  const long long b = blockIdx.x;  // this block's partials
   if (t < e4) {
-    const float pv[4] = {p.x * inv_n, p.y * inv_n, p.z * inv_n, p.w * inv_n};
-    const int cv[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * t + i < a.E) {
-        a.prob[4 * t + i] = pv[i];
-        a.counts[4 * t + i] = cv[i];
-        dot = fmaf(static_cast<float>(cv[i]), pv[i], dot);
-      }
-    }
+    reinterpret_cast<float4*>(a.part_prob)[b * e4 + t] = p;
+    reinterpret_cast<int4*>(a.part_cnt)[b * e4 + t] = c;
   }
-  __syncthreads();  // s_z has been read
-  if (t < 128) {  // e4 <= 128: four warps hold every product
-    dot = group_sum<32>(dot);
-    if ((t & 31) == 0) s_z[t >> 5] = dot;
-  }
-  __syncthreads();
   if (t == 0) {
-    a.n_valid[0] = n;
-    a.loss[0] = a.balance_coef * static_cast<float>(a.E) / static_cast<float>(a.k) *
-                ((s_z[0] + s_z[1]) + (s_z[2] + s_z[3])) * inv_n;
-    // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
-    a.loss[1] = n > 0 && a.z_coef != 0.f ? a.z_coef * z * inv_n : 0.f;
+    a.part_z[b] = z;
+    a.part_n[b] = n;
   }
 }
 
@@ -316,6 +340,8 @@ __global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalBwd a, int 
   constexpr int kGroups = kBwdThreads / L;
   const int t = threadIdx.x, g = t & (L - 1), grp = t / L;
   const long long step = static_cast<long long>(gridDim.x) * kGroups;
+  grid_dep_launch();
+  grid_dep_wait();
   float f[4 * NJ];
   float Z = 0.f;
   for (long long base = static_cast<long long>(blockIdx.x) * kGroups; base < a.T;
@@ -416,9 +442,8 @@ int64_t balance_blocks(const mok_balance_desc& D) {
 void balance_layout(const mok_balance_desc& D, BalanceWs* W) {
   const size_t G = static_cast<size_t>(balance_blocks(D));
   auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  W->arrivals = 0;
   const size_t e_pad = (static_cast<size_t>(D.E) + 3) / 4 * 4;
-  W->part_prob = 256;
+  W->part_prob = 0;
   W->part_cnt = W->part_prob + al(G * e_pad * 4);
   W->part_z = W->part_cnt + al(G * e_pad * 4);
   W->part_n = W->part_z + al(G * 4);
@@ -436,7 +461,6 @@ cudaError_t launch_balance_fwd(const mok_balance_desc& D, const float* logits,
   a.logits = logits; a.idx = idx; a.mask = mask;
   a.loss = loss; a.prob = prob; a.lse = lse; a.counts = counts; a.n_valid = n_valid;
   a.status = status;
-  a.arrivals = reinterpret_cast<int*>(b + W.arrivals);
   a.part_prob = reinterpret_cast<float*>(b + W.part_prob);
   a.part_cnt = reinterpret_cast<int32_t*>(b + W.part_cnt);
   a.part_z = reinterpret_cast<float*>(b + W.part_z);
@@ -444,17 +468,27 @@ cudaError_t launch_balance_fwd(const mok_balance_desc& D, const float* logits,
   a.T = D.T; a.ld = D.ld_logits; a.E = D.E; a.k = D.k;
   a.balance_coef = D.balance_coef; a.z_coef = D.z_coef;
   const unsigned grid = static_cast<unsigned>(balance_blocks(D));
-  if (grid > 1) {
-    cudaError_t e = cudaMemsetAsync(a.arrivals, 0, 4, st);
-    if (e != cudaSuccess) return e;
-  }
+  a.blocks = static_cast<int>(grid);
   const int vec = vec4(logits, a.ld, a.E);
-  ProfScope prof("router_balance", st);
-  by_width(D.E, [&](auto L, auto NJ) {
-    balance_fwd_kernel<decltype(L)::value, decltype(NJ)::value><<<grid, kFwdThreads, 0, st>>>(a, vec);
-  });
-  count_launch();
-  return cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  {
+    ProfScope prof("router_balance", st);
+    by_width(D.E, [&](auto L, auto NJ) {
+      constexpr int l = decltype(L)::value, nj = decltype(NJ)::value;
+      auto kern = balance_fwd_kernel<l, nj>;
+      const int smem = kFwdThreads / l * l * nj * 16;
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), dim3(kFwdThreads), smem, st, a, vec);
+    });
+    count_launch();
+  }
+  if (e != cudaSuccess) return e;
+  if (grid > 1) {
+    ProfScope prof("router_balance_sum", st);
+    e = launch_dependent(balance_sum_kernel, dim3(1), dim3(kFwdThreads), 0, st, a);
+    count_launch();
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_balance_bwd(const mok_balance_desc& D, const float* dloss,
@@ -473,11 +507,13 @@ cudaError_t launch_balance_bwd(const mok_balance_desc& D, const float* dloss,
   const unsigned grid = static_cast<unsigned>(need < cap ? need : cap);
   const int vec = vec4(logits, a.ld, a.E) && vec4(dlogits, a.ld, a.E);
   ProfScope prof("router_balance_bwd", st);
+  cudaError_t e = cudaSuccess;
   by_width(D.E, [&](auto L, auto NJ) {
-    balance_bwd_kernel<decltype(L)::value, decltype(NJ)::value><<<grid, kBwdThreads, 0, st>>>(a, vec);
+    e = launch_dependent(balance_bwd_kernel<decltype(L)::value, decltype(NJ)::value>, dim3(grid),
+                         dim3(kBwdThreads), 0, st, a, vec);
   });
   count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace mok

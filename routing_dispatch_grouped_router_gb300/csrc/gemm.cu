@@ -737,7 +737,7 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (x + 4 * j < a.n_valid) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + x) + j);
+        const float4 b = *(reinterpret_cast<const float4*>(a.bias + x) + j);
         v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
       }
     }

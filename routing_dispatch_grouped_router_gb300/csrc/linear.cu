@@ -24,6 +24,9 @@ namespace mok {
 
 namespace {
 
+// (These kernels may start before the one in front of them on the stream has
+// ended, so they read with plain loads, after grid_dep_wait: the non-coherent
+// path is for memory that nothing writes while a kernel lives.)
 constexpr int kEngineTiles = 38;
 constexpr int kFewTokens = 8;
 constexpr int kLinThreads = 192;  // TMA warp, MMA warp, four epilogue warps
@@ -149,12 +152,13 @@ __device__ __forceinline__ void finish1(const LinArgs& a, long long m, int n, fl
 constexpr int kFewThreads = 256;
 template <int MT, int R, bool F32>
 __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
-    const __nv_bfloat16* __restrict__ x, long long ld_x, const __nv_bfloat16* __restrict__ w,
-    int K, LinArgs a) {
+    const __nv_bfloat16* x, long long ld_x, const __nv_bfloat16* w, int K, LinArgs a) {
   constexpr int U = 16 / R;  // chunks in flight
   __shared__ float s_sum[8][R * MT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n0 = blockIdx.x * R;
+  grid_dep_launch();
+  grid_dep_wait();
   float acc[R][MT];
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
       for (int r = 0; r < R; ++r) {
         wv[u][r] = make_uint4(0u, 0u, 0u, 0u);
         if (k < K && n0 + r < a.N)
-          wv[u][r] = ld_global_nc_v4(w + static_cast<long long>(n0 + r) * K + k);
+          wv[u][r] = *reinterpret_cast<const uint4*>(w + static_cast<long long>(n0 + r) * K + k);
       }
     }
 #pragma unroll
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         uint4 t = make_uint4(0u, 0u, 0u, 0u);
-        if (m < a.M) t = ld_global_nc_v4(x + m * ld_x + k);
+        if (m < a.M) t = *reinterpret_cast<const uint4*>(x + m * ld_x + k);
         xf[m][0] = bf16lo(t.x); xf[m][1] = bf16hi(t.x); xf[m][2] = bf16lo(t.y);
         xf[m][3] = bf16hi(t.y); xf[m][4] = bf16lo(t.z); xf[m][5] = bf16hi(t.z);
         xf[m][6] = bf16lo(t.w); xf[m][7] = bf16hi(t.w);
@@ -258,6 +262,8 @@ __global__ void __launch_bounds__(kLinThreads)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  grid_dep_wait();
+  grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
   volatile int* vabort = abort_flag;
   bool ok = true;
@@ -386,7 +392,8 @@ __global__ void __launch_bounds__(kLinThreads)
   if (!*vabort) {
     const uint32_t part = smem_addr(smem);
     const int f4 = lane * 4;
-    for (int m = split + ks * warp; m < BN && m0 + m < args.M; m += ks * (kLinThreads / 32)) {
+    const int tokens = n0 + f4 < args.N ? (args.M - m0 < BN ? args.M - m0 : BN) : 0;
+    for (int m = split + ks * warp; m < tokens; m += ks * (kLinThreads / 32)) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
       const uint32_t at = part + static_cast<uint32_t>(m * 128 + f4) * 4u;
       if (ks == 1) {
@@ -435,18 +442,20 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   if (ks > a.nkb / 4) ks = a.nkb / 4;
   if (ks < 1) ks = 1;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ks);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(ks), static_cast<unsigned>(nt),
                      static_cast<unsigned>(mt));
   cfg.blockDim = dim3(kLinThreads, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   ProfScope prof("linear", st);
   e = cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
   count_launch();
@@ -484,10 +493,12 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
     const auto* xb = static_cast<const __nv_bfloat16*>(x);
     const auto* wb = static_cast<const __nv_bfloat16*>(w);
     const int K = static_cast<int>(D.K);
+    cudaError_t e = cudaSuccess;
     auto run = [&](auto MT, auto R, auto F) {
       constexpr int r = decltype(R)::value;
-      linear_few_kernel<decltype(MT)::value, r, decltype(F)::value>
-          <<<static_cast<unsigned>((D.N + r - 1) / r), kFewThreads, 0, st>>>(xb, D.ld_x, wb, K, a);
+      e = launch_dependent(linear_few_kernel<decltype(MT)::value, r, decltype(F)::value>,
+                           dim3(static_cast<unsigned>((D.N + r - 1) / r)), dim3(kFewThreads), 0,
+                           st, xb, D.ld_x, wb, K, a);
     };
     auto by_tokens = [&](auto F) {
       using std::integral_constant;
@@ -499,7 +510,7 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
     if (f32) by_tokens(std::true_type());
     else by_tokens(std::false_type());
     count_launch();
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
   }
   if (D.M <= 16) return f32 ? run_linear<16, true>(D, x, w, a, st) : run_linear<16, false>(D, x, w, a, st);
   if (D.M <= 64) return f32 ? run_linear<64, true>(D, x, w, a, st) : run_linear<64, false>(D, x, w, a, st);
@@ -530,7 +541,7 @@ struct Dz8 {
     if (VEC) {
       if (c >= N) return;
       const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + r * N + c);
-      const float4 x = __ldg(p), y = __ldg(p + 1);
+      const float4 x = p[0], y = p[1];
       f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
       f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
     } else {
@@ -549,7 +560,8 @@ struct Dz8<false, true> {
   uint4 u;
   __device__ __forceinline__ void load(const void* base, long long r, int c, int N) {
     u = make_uint4(0u, 0u, 0u, 0u);
-    if (c < N) u = ld_global_nc_v4(static_cast<const __nv_bfloat16*>(base) + r * N + c);
+    if (c < N)
+      u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + r * N + c);
   }
   __device__ __forceinline__ void get(float (&o)[8]) const {
     o[0] = bf16lo(u.x); o[1] = bf16hi(u.x); o[2] = bf16lo(u.y); o[3] = bf16hi(u.y);
@@ -565,6 +577,7 @@ template <bool F32, bool VEC, int ACT>
 __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
   __shared__ float s_sum[256 * 9];
   grid_dep_launch();
+  grid_dep_wait();
   const int l = threadIdx.x & (lanes - 1), row0 = threadIdx.x / lanes, rows = 256 / lanes;
   const int c = (blockIdx.x * lanes + l) * 8;
   const long long r0 = static_cast<long long>(blockIdx.y) * kDzRows;
@@ -631,13 +644,15 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
 }
 
 // dw[i] (+)= sum over s < n of part[s * stride4 + i], float4s, in order
-__global__ void __launch_bounds__(256) split_sum_kernel(const float4* __restrict__ part, int n,
+__global__ void __launch_bounds__(256) split_sum_kernel(const float4* part, int n,
                                                         long long stride4, long long n4,
                                                         float4* dw, int accumulate) {
+  grid_dep_launch();
+  grid_dep_wait();
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n4; i += gridDim.x * 256LL) {
-    float4 v = __ldg(part + i);
+    float4 v = part[i];
     for (int s = 1; s < n; ++s) {
-      const float4 p = __ldg(part + s * stride4 + i);
+      const float4 p = part[s * stride4 + i];
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
     if (accumulate) {
@@ -709,9 +724,11 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     const dim3 grid(static_cast<unsigned>((W.n_pad + lanes * 8 - 1) / (lanes * 8)),
                     static_cast<unsigned>(W.bias_rows));
     ProfScope prof("linear_dz", st);
+    cudaError_t e = cudaSuccess;
     auto run = [&](auto F, auto V, auto A) {
-      linear_dz_kernel<decltype(F)::value, decltype(V)::value, decltype(A)::value>
-          <<<grid, 256, 0, st>>>(a, lanes);
+      e = launch_dependent(
+          linear_dz_kernel<decltype(F)::value, decltype(V)::value, decltype(A)::value>, grid,
+          dim3(256), 0, st, a, lanes);
     };
     auto by_act = [&](auto F, auto V) {
       if (D.act == MOK_ACT_NONE) run(F, V, std::integral_constant<int, MOK_ACT_NONE>());
@@ -722,7 +739,7 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     if (f32) vec ? by_act(std::true_type(), std::true_type()) : by_act(std::true_type(), std::false_type());
     else vec ? by_act(std::false_type(), std::true_type()) : by_act(std::false_type(), std::false_type());
     count_launch();
-    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (dbias) {
@@ -757,11 +774,11 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     const long long cap = 8LL * num_sms_current_device();
     if (blocks > cap) blocks = cap;
     ProfScope prof("linear_dw_sum", st);
-    split_sum_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
-        reinterpret_cast<const float4*>(part), W.dw_splits, stride4, n4,
-        reinterpret_cast<float4*>(dw), D.accumulate ? 1 : 0);
+    e = launch_dependent(split_sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
+                         reinterpret_cast<const float4*>(part), W.dw_splits, stride4, n4,
+                         reinterpret_cast<float4*>(dw), D.accumulate ? 1 : 0);
     count_launch();
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
   }
   return cudaSuccess;
 }

@@ -277,7 +277,7 @@ cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* ou
 
 // The router's auxiliary losses (balance.cu).
 struct BalanceWs {
-  size_t arrivals, part_prob, part_cnt, part_z, part_n, total;
+  size_t part_prob, part_cnt, part_z, part_n, total;
 };
 int64_t balance_blocks(const mok_balance_desc& D);
 void balance_layout(const mok_balance_desc& D, BalanceWs* W);
@@ -384,14 +384,15 @@ cudaError_t launch_fill_zero(void* dst, size_t bytes, cudaStream_t st);
 // grid_dep_wait holds it back from that kernel's results): the launch's own
 // latency then overlaps the other's tail.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t st,
-                             A... args) {
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -193,6 +193,8 @@ __device__ __forceinline__ void mx_store(const NormFwd& a, long long r, int v, b
 template <bool XF32, bool SF32, bool VEC, int NV, bool MX>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormFwd a) {
   __shared__ float red[32];
+  grid_dep_launch();
+  grid_dep_wait();
   const int t = threadIdx.x, tpr = blockDim.x;
   const long long r = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool row_in = r < a.rows;
@@ -280,11 +282,12 @@ cudaError_t fwd_launch(const NormFwd& a, cudaStream_t st) {
   const dim3 block(tpr, rpb);
   const unsigned grid = static_cast<unsigned>((a.rows + rpb - 1) / rpb);
   ProfScope prof("add_rmsnorm", st);
-  if (nv == 1) add_rmsnorm_kernel<XF32, SF32, VEC, 1, MX><<<grid, block, 0, st>>>(a);
-  else if (nv == 2) add_rmsnorm_kernel<XF32, SF32, VEC, 2, MX><<<grid, block, 0, st>>>(a);
-  else add_rmsnorm_kernel<XF32, SF32, VEC, 4, MX><<<grid, block, 0, st>>>(a);
+  auto kern = nv == 1 ? add_rmsnorm_kernel<XF32, SF32, VEC, 1, MX>
+                      : (nv == 2 ? add_rmsnorm_kernel<XF32, SF32, VEC, 2, MX>
+                                 : add_rmsnorm_kernel<XF32, SF32, VEC, 4, MX>);
+  const cudaError_t e = launch_dependent(kern, dim3(grid), block, 0, st, a);
   count_launch();
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool XF32, bool SF32>
@@ -365,6 +368,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(NormBwd a) {
   __shared__ float red[2][2][16];  // [row parity][sum][warp]
   __shared__ float s_dw[8][256];
   grid_dep_launch();
+  grid_dep_wait();
   const int t = threadIdx.x, tpr = blockDim.x, nw = tpr >> 5;
   float dw[NV][8];
 #pragma unroll
@@ -471,6 +475,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
     fence_barrier_init();
   }
   __syncthreads();
+  grid_dep_wait();
   volatile int* vabort = &s_abort;
   auto fill = [&](int slot, long long r) {  // thread 0
     uint8_t* p = s_rows + slot * row_bytes;
@@ -573,7 +578,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
 // out[c] (+)= sum over g < n of part[g, c]: 32 columns per block, its 32 warps
 // take every 32nd partial (their loads in flight together: the latency of a
 // few loads bounds this), then their sums in order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ part,
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part,
                                                           long long n, int d, float* out,
                                                           int accumulate) {
   __shared__ float s[32][33];
@@ -598,7 +603,7 @@ cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* ou
   ProfScope prof("column_sum", st);
   const cudaError_t e =
       launch_dependent(column_sum_kernel, dim3(static_cast<unsigned>((d + 31) / 32)),
-                       dim3(32, 32), st, part, n, d, out, accumulate ? 1 : 0);
+                       dim3(32, 32), 0, st, part, n, d, out, accumulate ? 1 : 0);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -639,8 +644,8 @@ cudaError_t bulk_launch(const NormBwd& a, const BwdShape& b, int64_t row_bytes, 
   const int smem = static_cast<int>(b.depth * row_bytes);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(b.blocks), b.tpr, smem, st>>>(a, b.depth);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(static_cast<unsigned>(b.blocks)), dim3(b.tpr), smem, st, a,
+                          b.depth);
 }
 
 template <bool DYF32, bool SF32, bool VEC>
@@ -654,12 +659,11 @@ cudaError_t bwd_launch(const NormBwd& a, int64_t row_bytes, cudaStream_t st) {
       return b.nv == 2 ? bulk_launch<DYF32, SF32, 2>(a, b, row_bytes, st)
                        : bulk_launch<DYF32, SF32, 4>(a, b, row_bytes, st);
   }
-  const unsigned g = static_cast<unsigned>(b.blocks);
-  const dim3 block(b.tpr, b.rpb);
-  if (b.nv == 1) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 1><<<g, block, 0, st>>>(a);
-  else if (b.nv == 2) add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 2><<<g, block, 0, st>>>(a);
-  else add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 4><<<g, block, 0, st>>>(a);
-  return cudaGetLastError();
+  auto kern = b.nv == 1 ? add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 1>
+                        : (b.nv == 2 ? add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 2>
+                                     : add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 4>);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(b.blocks)), dim3(b.tpr, b.rpb), 0, st,
+                          a);
 }
 
 }  // namespace
