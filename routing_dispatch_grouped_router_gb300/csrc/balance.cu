@@ -23,10 +23,11 @@ namespace mok {
 
 namespace {
 
-constexpr int kFwdThreads = 1024;
+// Threads of the forward's blocks: 1024 so that the tokens of a large batch are
+// in flight at once; 256 where one block does it all (shorter barriers).
+constexpr int kManyThreads = 1024;
+constexpr int kFewThreads = 256;
 constexpr int kBwdThreads = 256;
-// Tokens whose loads a group of the backward has in flight at once.
-constexpr int kUnroll = 2;
 // Blocks of the forward (one per SM of a GB300, whatever the device, so that
 // the sums do not depend on it).
 constexpr int kFwdBlocks = 152;
@@ -99,10 +100,11 @@ __device__ __forceinline__ bool clean(float (&l)[N]) {
 // t % cols (a power of two) of slice t / cols, and z, n of its own.  On return
 // threads t < cols hold column t's sums, and every thread z's and n's.  A fixed
 // tree: lanes, then warps in order.
+template <int TH>
 __device__ __forceinline__ void block_columns(int cols, float4& p, int4& c, float& z, int& n,
                                               float4* s_f4, int4* s_i4, float* s_z, int* s_n) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  constexpr int W = kFwdThreads / 32;
+  constexpr int W = TH / 32;
   __syncthreads();  // the shared buffers are free
   for (int o = 16; o >= cols; o >>= 1) {
     p.x += __shfl_xor_sync(0xffffffffu, p.x, o);
@@ -128,7 +130,7 @@ __device__ __forceinline__ void block_columns(int cols, float4& p, int4& c, floa
     p = make_float4(0.f, 0.f, 0.f, 0.f);
     c = make_int4(0, 0, 0, 0);
 #pragma unroll 4
-    for (int i = t; i < kFwdThreads; i += step) {
+    for (int i = t; i < TH; i += step) {
       const float4 f = s_f4[i];
       const int4 k = s_i4[i];
       p.x += f.x; p.y += f.y; p.z += f.z; p.w += f.w;
@@ -144,11 +146,12 @@ __device__ __forceinline__ void block_columns(int cols, float4& p, int4& c, floa
   }
 }
 
+template <int TH>
 struct BalShared {
-  float4 f4[kFwdThreads];
-  int4 i4[kFwdThreads];
-  float z[kFwdThreads / 32];
-  int n[kFwdThreads / 32];
+  float4 f4[TH];
+  int4 i4[TH];
+  float z[TH / 32];
+  int n[TH / 32];
 };
 
 // Float4 columns of E, padded to a power of two.
@@ -160,7 +163,7 @@ __device__ __forceinline__ int pow2_cols(int e4) {
 
 // The outputs from the column sums p, c of threads t < E/4 and z, n.
 __device__ __forceinline__ void balance_out(const BalArgs& a, float4 p, int4 c, float z, int n,
-                                            BalShared& s) {
+                                            float* s_z) {
   const int t = threadIdx.x, e4 = (a.E + 3) / 4;
   const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
   float dot = 0.f;
@@ -176,16 +179,16 @@ __device__ __forceinline__ void balance_out(const BalArgs& a, float4 p, int4 c, 
       }
     }
   }
-  __syncthreads();  // s.z has been read
+  __syncthreads();  // s_z has been read
   if (t < 128) {  // E/4 <= 128: four warps hold every product
     dot = group_sum<32>(dot);
-    if ((t & 31) == 0) s.z[t >> 5] = dot;
+    if ((t & 31) == 0) s_z[t >> 5] = dot;
   }
   __syncthreads();
   if (t == 0) {
     a.n_valid[0] = n;
     a.loss[0] = a.balance_coef * static_cast<float>(a.E) / static_cast<float>(a.k) *
-                ((s.z[0] + s.z[1]) + (s.z[2] + s.z[3])) * inv_n;
+                ((s_z[0] + s_z[1]) + (s_z[2] + s_z[3])) * inv_n;
     // (without a z loss its sum may be beyond fp32: 0 inf would be NaN)
     a.loss[1] = n > 0 && a.z_coef != 0.f ? a.z_coef * z * inv_n : 0.f;
   }
@@ -193,12 +196,12 @@ __device__ __forceinline__ void balance_out(const BalArgs& a, float4 p, int4 c, 
 
 // The second kernel: one block adds the first one's partials in block order by
 // slices of its threads.
-__global__ void __launch_bounds__(kFwdThreads) balance_sum_kernel(BalArgs a) {
-  __shared__ BalShared s;
+__global__ void __launch_bounds__(kManyThreads) balance_sum_kernel(BalArgs a) {
+  __shared__ BalShared<kManyThreads> s;
   grid_dep_launch();
   grid_dep_wait();
   const int t = threadIdx.x, e4 = (a.E + 3) / 4, cols = pow2_cols(e4);
-  const int col = t & (cols - 1), slices = kFwdThreads / cols, G = a.blocks;
+  const int col = t & (cols - 1), slices = kManyThreads / cols, G = a.blocks;
   float z = t < G ? a.part_z[t] : 0.f;  // (fewer blocks than threads)
   int n = t < G ? a.part_n[t] : 0;
   float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -214,22 +217,22 @@ __global__ void __launch_bounds__(kFwdThreads) balance_sum_kernel(BalArgs a) {
       c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
     }
   }
-  block_columns(cols, p, c, z, n, s.f4, s.i4, s.z, s.n);
-  balance_out(a, p, c, z, n, s);
+  block_columns<kManyThreads>(cols, p, c, z, n, s.f4, s.i4, s.z, s.n);
+  balance_out(a, p, c, z, n, s.z);
 }
 
-template <int L, int NJ>
-__global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int vec) {
-  constexpr int kGroups = kFwdThreads / L;  // tokens of a block at a time
+template <int TH, int L, int NJ>
+__global__ void __launch_bounds__(TH) balance_fwd_kernel(BalArgs a, int vec) {
+  constexpr int kGroups = TH / L;           // tokens of a block at a time
   constexpr int kE4 = L * NJ;               // float4 columns of the group's lanes
   // tokens whose loads a group has in flight (registers: 64 a thread)
   constexpr int U = NJ == 1 ? 4 : (NJ == 2 ? 2 : 1);
   extern __shared__ __align__(16) float4 s_prob[];  // [kGroups][kE4]
-  __shared__ BalShared s;
+  __shared__ BalShared<TH> s;
   __shared__ __align__(16) int32_t s_cnt[kMaxExperts];
   grid_dep_launch();
   const int t = threadIdx.x, g = t & (L - 1), grp = t / L;
-  if (t < kMaxExperts) s_cnt[t] = 0;
+  for (int e = t; e < kMaxExperts; e += TH) s_cnt[e] = 0;
   __syncthreads();
   grid_dep_wait();
   float acc[4 * NJ];
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
   __syncthreads();
   // the groups' sums: slices of the threads over the float4 columns
   const int e4 = (a.E + 3) / 4, cols = pow2_cols(e4);
-  const int col = t & (cols - 1), sl = t / cols, slices = kFwdThreads / cols;
+  const int col = t & (cols - 1), sl = t / cols, slices = TH / cols;
   float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
   int4 c = make_int4(0, 0, 0, 0);
   if (col < e4) {
@@ -309,9 +312,9 @@ __global__ void __launch_bounds__(kFwdThreads) balance_fwd_kernel(BalArgs a, int
     }
     if (sl == 0) c = *reinterpret_cast<const int4*>(s_cnt + 4 * col);
   }
-  block_columns(cols, p, c, z, n, s.f4, s.i4, s.z, s.n);
+  block_columns<TH>(cols, p, c, z, n, s.f4, s.i4, s.z, s.n);
   if (gridDim.x == 1) {
-    balance_out(a, p, c, z, n, s);
+    balance_out(a, p, c, z, n, s.z);
     return;
   }
   const long long b = blockIdx.x;  // this block's partials
@@ -335,8 +338,13 @@ struct BalBwd {
   float balance_coef, z_coef;
 };
 
+// Tokens whose loads a group of the backward has in flight at once: 64 registers
+// a thread, so that four blocks share an SM.
+constexpr int bwd_unroll(int nj) { return nj <= 3 ? 2 : 1; }
+
 template <int L, int NJ>
-__global__ void __launch_bounds__(kBwdThreads) balance_bwd_kernel(BalBwd a, int vec) {
+__global__ void __launch_bounds__(kBwdThreads, 4) balance_bwd_kernel(BalBwd a, int vec) {
+  constexpr int kUnroll = bwd_unroll(NJ);
   constexpr int kGroups = kBwdThreads / L;
   const int t = threadIdx.x, g = t & (L - 1), grp = t / L;
   const long long step = static_cast<long long>(gridDim.x) * kGroups;
@@ -431,9 +439,9 @@ bool vec4(const void* p, long long ld, int E) {
 }  // namespace
 
 int64_t balance_blocks(const mok_balance_desc& D) {
-  // up to eight tokens per group, one block alone is faster than several, their
-  // counter's reset and their last one's sum
-  const int64_t groups = kFwdThreads / lanes_of(D.E);
+  // one block of 256 threads for up to eight tokens per group, one of 1024 for
+  // up to eight of its groups: faster than several blocks and their sum
+  const int64_t groups = kManyThreads / lanes_of(D.E);
   if (D.T <= 8 * groups) return 1;
   const int64_t b = (D.T + groups - 1) / groups;
   return b < kFwdBlocks ? b : kFwdBlocks;
@@ -475,17 +483,19 @@ cudaError_t launch_balance_fwd(const mok_balance_desc& D, const float* logits,
     ProfScope prof("router_balance", st);
     by_width(D.E, [&](auto L, auto NJ) {
       constexpr int l = decltype(L)::value, nj = decltype(NJ)::value;
-      auto kern = balance_fwd_kernel<l, nj>;
-      const int smem = kFwdThreads / l * l * nj * 16;
+      const bool few = D.T <= 8 * (kFewThreads / l);
+      auto kern = few ? balance_fwd_kernel<kFewThreads, l, nj> : balance_fwd_kernel<kManyThreads, l, nj>;
+      const int th = few ? kFewThreads : kManyThreads;
+      const int smem = th * nj * 16;
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), dim3(kFwdThreads), smem, st, a, vec);
+      if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), dim3(th), smem, st, a, vec);
     });
     count_launch();
   }
   if (e != cudaSuccess) return e;
   if (grid > 1) {
     ProfScope prof("router_balance_sum", st);
-    e = launch_dependent(balance_sum_kernel, dim3(1), dim3(kFwdThreads), 0, st, a);
+    e = launch_dependent(balance_sum_kernel, dim3(1), dim3(kManyThreads), 0, st, a);
     count_launch();
   }
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -501,7 +511,7 @@ cudaError_t launch_balance_bwd(const mok_balance_desc& D, const float* dloss,
   a.mask = mask; a.dlogits = dlogits;
   a.T = D.T; a.ld = D.ld_logits; a.E = D.E; a.k = D.k;
   a.balance_coef = D.balance_coef; a.z_coef = D.z_coef;
-  const int64_t round = kUnroll * (kBwdThreads / lanes_of(D.E));
+  const int64_t round = bwd_unroll((D.E + 127) / 128) * (kBwdThreads / lanes_of(D.E));
   const int64_t need = (D.T + round - 1) / round;
   const int64_t cap = 4LL * num_sms_current_device();
   const unsigned grid = static_cast<unsigned>(need < cap ? need : cap);

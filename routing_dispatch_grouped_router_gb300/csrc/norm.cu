@@ -625,11 +625,18 @@ BwdShape bwd_shape(int64_t rows, int64_t d, bool vec, int64_t row_bytes) {
   b.rpb = b.nv == 1 ? 8 : 1;
   b.depth = 0;
   int per_sm = 768 / (b.tpr * b.rpb);
-  per_sm = per_sm < 1 ? 1 : (per_sm > 16 ? 16 : per_sm);
   if (vec && d >= kBulkMinD) {
+    // a row's chain of barrier and reductions is about 1100 cycles, in which an
+    // SM's share of the memory moves 26 KB: enough blocks to cover it half as
+    // much again, and few, since each leaves a partial weight gradient
+    const int64_t cover = 40 * 1024 / (row_bytes + row_bytes / 3) + 1;
+    if (per_sm > cover) per_sm = static_cast<int>(cover < 2 ? 2 : cover);
     // a ring of at least three rows per block where that leaves two blocks
     while (per_sm > 2 && per_sm * 3 * row_bytes > kBulkSmem) --per_sm;
     while (per_sm > 1 && per_sm * 2 * row_bytes > kBulkSmem) --per_sm;
+  }
+  per_sm = per_sm < 1 ? 1 : (per_sm > 16 ? 16 : per_sm);
+  if (vec && d >= kBulkMinD) {
     b.depth = static_cast<int>(kBulkSmem / per_sm / row_bytes);
     if (b.depth > kBulkMaxDepth) b.depth = kBulkMaxDepth;
   }
