@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -125,6 +126,26 @@ def load(path: str | None = None):
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+_block = None
+
+
+def block():
+    """The module of block_binding.cpp (built beside libmok.so, which it calls)."""
+    global _block
+    if _block is None:
+        load()
+        from . import build
+        path = build.BINDING
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m routing_dispatch_grouped_router_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_block", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        _block = m
+    return _block
 
 
 def exported_names():

@@ -6,7 +6,6 @@ libmok.so.  Shapes and dtypes are checked here, everything else by the library.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import torch
 
@@ -180,49 +179,29 @@ def gemm_nvfp4(A, sa, ga, B, sb, gb, C, workspace, stream=None):
 
 
 # -------------------------------------------- operators around the layer --
-# One decode step makes several of these calls, so their host time counts: the
-# checks of shapes, types, strides and devices run once for each combination of
-# them and leave the C descriptor (nothing else is kept).
+# Checks of shapes, types, strides and devices, and the outputs that a call is
+# given none for: csrc/block_binding.cpp.  What it refuses raises ValueError,
+# what the library refuses MokError.
 
-_ELEM = {torch.bfloat16: 0, torch.float32: 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
-_BF, _F32, _I32, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
-_MASK = (torch.uint8, torch.bool)
-_plan = functools.lru_cache(maxsize=8192)
 _status_words = {}
+_block = None
 
 
-def _meta(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _call_stream(t, stream):
-    """The raw stream of a call on the GPU of `t`, which must be the current one."""
-    index = t.get_device()
-    if index < 0 or index != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors must be on the current GPU, not on {t.device}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream
-
-
-def _alloc(shape, dtype, device, stream):
-    """A tensor of the stream that the call runs on, so that its memory is not
-    handed out again before that stream is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _ops():
+    global _block
+    if _block is None:
+        m = _lib.block()
+        m.setup(_lib.check, lambda index: operator_status(index).data_ptr())
+        _block = m
+    return _block
 
 
 def operator_status(device=None):
     """The device int32 that the operators below report into (sticky: the
     first error stays; read it with `device_status`, zero it to go on)."""
-    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    index = torch.cuda.current_device() if device is None else torch.device("cuda", device).index \
+        if isinstance(device, int) else torch.device(device).index
     word = _status_words.get(index)
     if word is None:
         word = torch.zeros(64, dtype=torch.int32, device=torch.device("cuda", index))
@@ -231,59 +210,11 @@ def operator_status(device=None):
     return word
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
-def _matrix(m, name, shape=None, dtypes=_ELEM, device=None):
-    """Checks the metadata of a matrix with consecutive columns; returns its row stride."""
-    sh, st, dt, dev = m
-    _need(len(sh) == 2, f"{name} must be a matrix, got {tuple(sh)}")
-    _need(shape is None or sh == shape, f"{name} must be {shape}, got {tuple(sh)}")
-    _need(dt in dtypes, f"{name} must not be {dt}")
-    _need(dev.type == "cuda" and (device is None or dev == device),
-          f"{name} must be on the GPU of the other tensors, not on {dev}")
-    _need(sh[1] <= 1 or st[1] == 1, f"{name} must have consecutive columns")
-    if sh[0] <= 1:
-        return sh[1]
-    _need(st[0] >= sh[1], f"{name} must have rows that do not overlap")
-    return st[0]
-
-
-def _dense(m, name, shape, dtypes, device):
-    """Checks the metadata of a contiguous tensor of a given shape."""
-    sh, st, dt, dev = m
-    _need(sh == shape, f"{name} must be {shape}, got {tuple(sh)}")
-    _need(dt in dtypes, f"{name} must not be {dt}")
-    _need(dev == device, f"{name} must be on the GPU of the other tensors, not on {dev}")
-    n = 1
-    for size, step in zip(reversed(sh), reversed(st)):
-        _need(size <= 1 or step == n, f"{name} must be contiguous")
-        n *= size
-
-
-@_plan
-def _norm_plan(x, weight, res, s, y, eps, mx):
-    ld_x = _matrix(x, "x")
-    (rows, d), dev = x[0], x[3]
-    _dense(weight, "weight", (d,), _ELEM, dev)
-    ld_r = 0 if res is None else _matrix(res, "residual", (rows, d), device=dev)
-    stream_dt = x[2] if res is None else res[2]
-    ld_s = 0 if s is None else _matrix(s, "s", (rows, d), (stream_dt,), dev)
-    ld_y = 0 if y is None else _matrix(y, "y", (rows, d), _BF, dev)
-    _need(not mx or d % 32 == 0, "MXFP8 needs d a multiple of 32")
-    return _lib.RmsnormDesc(rows, d, ld_x, ld_r, ld_s, ld_y, eps, _ELEM[x[2]], _ELEM[stream_dt],
-                            _ELEM[weight[2]], 0, 0)
-
-
-@_plan
-def _mx_out_plan(x, codes, scales, values):
-    (rows, d), dev = x[0], x[3]
-    _dense(codes, "codes", (rows, d), _U8, dev)
-    _dense(scales, "scales", (rows, d // 32), _U8, dev)
-    if values is not None:
-        _dense(values, "values", (rows, d), _BF, dev)
+def _act(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, not {act!r}")
+    return code
 
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-6, *, s=None, y=None, stream=None):
@@ -291,16 +222,7 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, *, s=None, y=None, stream=No
     mok_add_rmsnorm_forward): (s, y), s in the residual's type (x itself
     without a residual), y bf16.  x, residual bf16 or fp32 matrices, weight
     bf16 or fp32; rows may be strided."""
-    st = _call_stream(x, stream)
-    if residual is not None and s is None:
-        s = _alloc(x.shape, residual.dtype, x.device, stream)
-    if y is None:
-        y = _alloc(x.shape, torch.bfloat16, x.device, stream)
-    desc = _norm_plan(_meta(x), _meta(weight), _meta(residual), _meta(s), _meta(y), eps, False)
-    _lib.check(_lib.load().mok_add_rmsnorm_forward(desc, _addr(x), _addr(residual), _addr(weight),
-                                                   _addr(s), _addr(y), None, None, None, st),
-               "mok_add_rmsnorm_forward")
-    return (x if s is None else s), y
+    return _ops().add_rmsnorm(x, weight, residual, eps, s, y, stream)
 
 
 def add_rmsnorm_mx(x, weight, residual=None, eps=1e-6, *, s=None, y=None, values=None, codes=None,
@@ -309,37 +231,7 @@ def add_rmsnorm_mx(x, weight, residual=None, eps=1e-6, *, s=None, y=None, values
     [rows, d] (E4M3), scales uint8 [rows, d/32] (E8M0), as `gemm_mxfp8` takes
     them.  y (the bf16 norm) and values (the bf16 values of the codes) are
     written if given.  d a multiple of 32."""
-    st = _call_stream(x, stream)
-    if residual is not None and s is None:
-        s = _alloc(x.shape, residual.dtype, x.device, stream)
-    desc = _norm_plan(_meta(x), _meta(weight), _meta(residual), _meta(s), _meta(y), eps, True)
-    rows, d = x.shape
-    if codes is None:
-        codes = _alloc((rows, d), torch.uint8, x.device, stream)
-    if scales is None:
-        scales = _alloc((rows, d // 32), torch.uint8, x.device, stream)
-    _mx_out_plan(_meta(x), _meta(codes), _meta(scales), _meta(values))
-    _lib.check(_lib.load().mok_add_rmsnorm_forward(desc, _addr(x), _addr(residual), _addr(weight),
-                                                   _addr(s), _addr(y), _addr(values), _addr(codes),
-                                                   _addr(scales), st), "mok_add_rmsnorm_forward")
-    return (x if s is None else s), codes, scales
-
-
-@_plan
-def _norm_bwd_plan(dy, s, weight, ds, dx, dweight, eps, accumulate):
-    ld_dy = _matrix(dy, "dy")
-    (rows, d), dev = dy[0], dy[3]
-    ld_s = _matrix(s, "s", (rows, d), device=dev)
-    _dense(weight, "weight", (d,), _ELEM, dev)
-    ld_ds = 0 if ds is None else _matrix(ds, "ds", (rows, d), (s[2],), dev)
-    ld_dx = _matrix(dx, "dx", (rows, d), (s[2],), dev)
-    _dense(dweight, "dweight", (d,), _F32, dev)
-    desc = _lib.RmsnormDesc(rows, d, ld_dy, ld_ds, ld_s, ld_dx, eps, _ELEM[dy[2]], _ELEM[s[2]],
-                            _ELEM[weight[2]], int(accumulate), 0)
-    n = ctypes.c_size_t()
-    _lib.check(_lib.load().mok_add_rmsnorm_workspace_size(desc, n),
-               "mok_add_rmsnorm_workspace_size")
-    return desc, n.value
+    return _ops().add_rmsnorm_mx(x, weight, residual, eps, s, y, values, codes, scales, stream)
 
 
 def add_rmsnorm_backward(dy, s, weight, ds=None, eps=1e-6, *, dx=None, dweight=None,
@@ -348,43 +240,8 @@ def add_rmsnorm_backward(dy, s, weight, ds=None, eps=1e-6, *, dx=None, dweight=N
     mok_add_rmsnorm_backward): (dx, dweight).  dx, in the type of s, is the
     gradient of x and of residual alike, with ds (the gradient that reaches s by
     other ways) added; dweight fp32, added into with `accumulate`."""
-    st = _call_stream(dy, stream)
-    _need(dweight is not None or not accumulate, "accumulate needs dweight")
-    if dx is None:
-        dx = _alloc(dy.shape, s.dtype, dy.device, stream)
-    if dweight is None:
-        dweight = _alloc(dy.shape[1:], torch.float32, dy.device, stream)
-    desc, n = _norm_bwd_plan(_meta(dy), _meta(s), _meta(weight), _meta(ds), _meta(dx),
-                             _meta(dweight), eps, accumulate)
-    if workspace is None:
-        workspace = _alloc((n,), torch.uint8, dy.device, stream)
-    _lib.check(_lib.load().mok_add_rmsnorm_backward(desc, _addr(dy), _addr(s), _addr(weight),
-                                                    _addr(ds), _addr(dx), _addr(dweight),
-                                                    _addr(workspace), workspace.nbytes,
-                                                    _addr(operator_status(dy.device)), st),
-               "mok_add_rmsnorm_backward")
-    return dx, dweight
-
-
-@_plan
-def _balance_plan(logits, k, mask, lse, balance_coef, z_coef):
-    ld = _matrix(logits, "logits", None, _F32)
-    (T, E), dev = logits[0], logits[3]
-    if mask is not None:
-        _dense(mask, "mask", (T,), _MASK, dev)
-    if lse is not None:
-        _dense(lse, "lse", (T,), _F32, dev)
-    desc = _lib.BalanceDesc(T, ld, E, k, balance_coef, z_coef)
-    n = ctypes.c_size_t()
-    _lib.check(_lib.load().mok_router_balance_workspace_size(desc, n),
-               "mok_router_balance_workspace_size")
-    return desc, n.value
-
-
-@_plan
-def _topk_plan(idx, T, dev):
-    _need(len(idx[0]) == 2, "topk_idx must be a matrix")
-    _dense(idx, "topk_idx", (T, idx[0][1]), _I32, dev)
+    return _ops().add_rmsnorm_backward(dy, s, weight, ds, eps, dx, dweight, accumulate, workspace,
+                                       stream)
 
 
 def router_balance(logits, topk_idx, mask=None, *, balance_coef, z_coef=0.0, workspace=None,
@@ -392,75 +249,16 @@ def router_balance(logits, topk_idx, mask=None, *, balance_coef, z_coef=0.0, wor
     """The router's auxiliary losses over the tokens of `mask` (see
     mok_router_balance_forward): (loss [2] = balance and z loss, counts int32
     [E], prob [E] = mean probability, lse [T], n_valid int32 [1]).  logits fp32
-    [T, E], topk_idx int32 [T, k], mask uint8 or bool [T].  The results share
-    two allocations."""
-    st = _call_stream(logits, stream)
-    dev = logits.device
-    _topk_plan(_meta(topk_idx), logits.shape[0], dev)
-    desc, n = _balance_plan(_meta(logits), topk_idx.shape[1], _meta(mask), None, balance_coef,
-                            z_coef)
-    # the fp32 results (and the scratch) in one allocation, the integers in another
-    T, E = desc.T, desc.E
-    at_lse = (E + 2 + 3) // 4 * 4
-    at_ws = (at_lse + T + 3) // 4 * 4
-    buf = _alloc((at_ws + (n + 3) // 4 if workspace is None else at_ws,), torch.float32, dev, stream)
-    ints = _alloc((E + 1,), torch.int32, dev, stream)
-    prob = buf.as_strided((E,), (1,), 0)
-    loss = buf.as_strided((2,), (1,), E)
-    lse = buf.as_strided((T,), (1,), at_lse)
-    counts = ints.as_strided((E,), (1,), 0)
-    n_valid = ints.as_strided((1,), (1,), E)
-    f, i = buf.data_ptr(), ints.data_ptr()
-    ws = f + 4 * at_ws if workspace is None else workspace.data_ptr()
-    _lib.check(_lib.load().mok_router_balance_forward(
-        desc, _addr(logits), _addr(topk_idx), _addr(mask), f + 4 * E, i, f, f + 4 * at_lse,
-        i + 4 * E, ws, n if workspace is None else workspace.nbytes, _addr(operator_status(dev)),
-        st), "mok_router_balance_forward")
-    return loss, counts, prob, lse, n_valid
-
-
-@_plan
-def _balance_bwd_plan(dloss, logits, counts, n_valid, dlogits):
-    dev = logits[3]
-    _dense(dloss, "dloss", (2,), _F32, dev)
-    _dense(counts, "counts", (logits[0][1],), _I32, dev)
-    _dense(n_valid, "n_valid", (1,), _I32, dev)
-    _need(_matrix(dlogits, "dlogits", logits[0], _F32, dev) ==
-          _matrix(logits, "logits", None, _F32), "dlogits must have the row stride of logits")
+    [T, E], topk_idx int32 [T, k], mask uint8 or bool [T]."""
+    return _ops().router_balance(logits, topk_idx, mask, balance_coef, z_coef, workspace, stream)
 
 
 def router_balance_backward(dloss, logits, lse, counts, n_valid, k, mask=None, *, balance_coef,
                             z_coef=0.0, dlogits=None, stream=None):
     """dlogits [T, E] of dloss[0] * balance loss + dloss[1] * z loss, from the
     forward's lse, counts and n_valid (see mok_router_balance_backward)."""
-    st = _call_stream(logits, stream)
-    desc, _ = _balance_plan(_meta(logits), k, _meta(mask), _meta(lse), balance_coef, z_coef)
-    if dlogits is None:
-        dlogits = _alloc((desc.T, desc.ld_logits), torch.float32, logits.device, stream)
-        if desc.ld_logits != desc.E:
-            dlogits = dlogits[:, :desc.E]
-    _balance_bwd_plan(_meta(dloss), _meta(logits), _meta(counts), _meta(n_valid), _meta(dlogits))
-    _lib.check(_lib.load().mok_router_balance_backward(
-        desc, _addr(dloss), _addr(logits), _addr(lse), _addr(counts), _addr(n_valid), _addr(mask),
-        _addr(dlogits), st), "mok_router_balance_backward")
-    return dlogits
-
-
-@_plan
-def _linear_plan(x, w, bias, residual, y, z, act):
-    ld_x = _matrix(x, "x", None, _BF)
-    (M, K), dev = x[0], x[3]
-    _need(len(w[0]) == 2, "w must be a matrix")
-    N = w[0][0]
-    _dense(w, "w", (N, K), _BF, dev)
-    _need(act in ACTIVATIONS, f"act must be one of {tuple(ACTIVATIONS)}")
-    _need(y[2] in _ELEM, f"y must not be {y[2]}")
-    if bias is not None:
-        _dense(bias, "bias", (N,), _F32, dev)
-    for t, name in ((y, "y"), (residual, "residual"), (z, "z")):
-        if t is not None:
-            _dense(t, name, (M, N), (y[2],), dev)
-    return _lib.LinearDesc(M, N, K, ld_x, ACTIVATIONS[act], _ELEM[y[2]], 0, 0)
+    return _ops().router_balance_backward(dloss, logits, lse, counts, n_valid, k, mask,
+                                          balance_coef, z_coef, dlogits, stream)
 
 
 def linear(x, w, bias=None, *, act="none", residual=None, out_dtype=None, y=None, z=None,
@@ -469,44 +267,7 @@ def linear(x, w, bias=None, *, act="none", residual=None, out_dtype=None, y=None
     (y, z) with the pre-activation z for `linear_backward`.  x [M, K] and w
     [N, K] bf16 (K a multiple of 8), bias fp32 [N]; y, z and residual [M, N] of
     out_dtype, bf16 (the default) or fp32."""
-    st = _call_stream(x, stream)
-    if y is None or (keep_z and z is None):
-        shape = (x.shape[0], w.shape[0])
-        dt = out_dtype if out_dtype is not None else (torch.bfloat16 if y is None else y.dtype)
-        if y is None:
-            y = _alloc(shape, dt, x.device, stream)
-        if keep_z and z is None:
-            z = _alloc(shape, dt, x.device, stream)
-    _need(out_dtype is None or y.dtype == out_dtype, "y must have out_dtype")
-    desc = _linear_plan(_meta(x), _meta(w), _meta(bias), _meta(residual), _meta(y), _meta(z), act)
-    _lib.check(_lib.load().mok_linear_forward(desc, _addr(x), _addr(w), _addr(bias),
-                                              _addr(residual), _addr(y), _addr(z),
-                                              _addr(operator_status(x.device)), st),
-               "mok_linear_forward")
-    return (y, z) if keep_z else y
-
-
-@_plan
-def _linear_bwd_plan(dy, x, w, z, act, dx, dw, dbias, accumulate):
-    ld_x = _matrix(x, "x", None, _BF)
-    (M, K), dev = x[0], x[3]
-    _need(len(w[0]) == 2, "w must be a matrix")
-    N = w[0][0]
-    _dense(w, "w", (N, K), _BF, dev)
-    _dense(dy, "dy", (M, N), _ELEM, dev)
-    _need(act in ACTIVATIONS, f"act must be one of {tuple(ACTIVATIONS)}")
-    _need(act == "none" or z is not None, "the activation's gradient needs z")
-    if z is not None:
-        _dense(z, "z", (M, N), (dy[2],), dev)
-    _dense(dx, "dx", (M, K), _ELEM, dev)
-    _dense(dw, "dw", (N, K), _F32, dev)
-    if dbias is not None:
-        _dense(dbias, "dbias", (N,), _F32, dev)
-    desc = _lib.LinearDesc(M, N, K, ld_x, ACTIVATIONS[act], _ELEM[dy[2]], _ELEM[dx[2]],
-                           int(accumulate))
-    n = ctypes.c_size_t()
-    _lib.check(_lib.load().mok_linear_workspace_size(desc, n), "mok_linear_workspace_size")
-    return desc, n.value
+    return _ops().linear(x, w, bias, _act(act), residual, out_dtype, y, z, keep_z, stream)
 
 
 def linear_backward(dy, x, w, z=None, *, act="none", bias=False, dx_dtype=None, dx=None, dw=None,
@@ -515,28 +276,8 @@ def linear_backward(dy, x, w, z=None, *, act="none", bias=False, dx_dtype=None, 
     None unless `bias` is true or a tensor for it is given.  dy [M, N] bf16 or
     fp32, z of its type; dx bf16 (the default) or fp32; dw, dbias fp32.
     `accumulate` adds into the given dx (fp32), dw and dbias."""
-    st = _call_stream(x, stream)
-    _need(not accumulate or (dx is not None and dw is not None and not (bias and dbias is None)),
-          "accumulate needs dx, dw and dbias to add into")
-    if dx is None:
-        dx = _alloc(x.shape, torch.bfloat16 if dx_dtype is None else dx_dtype, x.device, stream)
-    _need(dx_dtype is None or dx.dtype == dx_dtype, "dx must have dx_dtype")
-    if dw is None:
-        dw = _alloc(w.shape, torch.float32, x.device, stream)
-    if bias and dbias is None:
-        dbias = _alloc(w.shape[:1], torch.float32, x.device, stream)
-    if act == "none":
-        z = None
-    desc, n = _linear_bwd_plan(_meta(dy), _meta(x), _meta(w), _meta(z), act, _meta(dx), _meta(dw),
-                               _meta(dbias), accumulate)
-    if workspace is None:
-        workspace = _alloc((n,), torch.uint8, x.device, stream)
-    _lib.check(_lib.load().mok_linear_backward(desc, _addr(dy), _addr(x), _addr(w), _addr(z),
-                                               _addr(dx), _addr(dw), _addr(dbias),
-                                               _addr(workspace), workspace.nbytes,
-                                               _addr(operator_status(x.device)), st),
-               "mok_linear_backward")
-    return dx, dw, dbias
+    return _ops().linear_backward(dy, x, w, z, _act(act), bias, dx_dtype, dx, dw, dbias,
+                                  accumulate, workspace, stream)
 
 
 def device_status(buf, stream=None) -> int:
