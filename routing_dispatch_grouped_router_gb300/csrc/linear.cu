@@ -29,6 +29,7 @@ namespace {
 // path is for memory that nothing writes while a kernel lives.)
 constexpr int kEngineTiles = 38;
 constexpr int kFewTokens = 8;
+constexpr int kMaxSplits = 8;  // CTAs of a portable cluster
 constexpr int kLinThreads = 192;  // TMA warp, MMA warp, four epilogue warps
 
 template <int BN>
@@ -388,21 +389,27 @@ __global__ void __launch_bounds__(kLinThreads)
   __syncwarp();
   if (ks > 1) cluster_sync(); else __syncthreads();
   // this CTA's share of the tokens, four features per thread, the cluster's
-  // sums in rank order
+  // sums in rank order; all of an element's remote loads go out together
   if (!*vabort) {
     const uint32_t part = smem_addr(smem);
-    const int f4 = lane * 4;
-    const int tokens = n0 + f4 < args.N ? (args.M - m0 < BN ? args.M - m0 : BN) : 0;
-    for (int m = split + ks * warp; m < tokens; m += ks * (kLinThreads / 32)) {
+    const int tokens = args.M - m0 < BN ? args.M - m0 : BN;
+    const int share = (tokens - split + ks - 1) / ks;  // tokens split, split + ks, ..
+    const int nf = args.N - n0 < 128 ? (args.N - n0 + 3) / 4 : 32;
+    for (int i = threadIdx.x; i < share * nf; i += kLinThreads) {
+      const int m = split + ks * (i / nf), f4 = 4 * (i % nf);
       float v[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t at = part + static_cast<uint32_t>(m * 128 + f4) * 4u;
       if (ks == 1) {
         const float4 p = *reinterpret_cast<const float4*>(smem + (m * 128 + f4) * 4);
         v[0] = p.x; v[1] = p.y; v[2] = p.z; v[3] = p.w;
       } else {
-        for (int r = 0; r < ks; ++r) {
-          const float4 p = ld_cluster_f4(mapa_shared(at, r));
-          v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+        const uint32_t at = part + static_cast<uint32_t>(m * 128 + f4) * 4u;
+        float4 p[kMaxSplits];
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          p[r] = r < ks ? ld_cluster_f4(mapa_shared(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r) {
+          v[0] += p[r].x; v[1] += p[r].y; v[2] += p[r].z; v[3] += p[r].w;
         }
       }
       finish4<F32>(args, m0 + m, n0 + f4, v);
@@ -438,7 +445,7 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   // four 64-value blocks each
   const int64_t slots = static_cast<int64_t>(num_sms_current_device()) * (BN <= 64 ? 2 : 1);
   int64_t ks = slots / (nt * mt);
-  if (ks > 8) ks = 8;
+  if (ks > kMaxSplits) ks = kMaxSplits;
   if (ks > a.nkb / 4) ks = a.nkb / 4;
   if (ks < 1) ks = 1;
   cudaLaunchConfig_t cfg = {};

@@ -575,35 +575,35 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
   }
 }
 
-// out[c] (+)= sum over g < n of part[g, c]: 32 columns per block, its 32 warps
-// take every 32nd partial (their loads in flight together: the latency of a
-// few loads bounds this), then their sums in order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part,
-                                                          long long n, int d, float* out,
-                                                          int accumulate) {
-  __shared__ float s[32][33];
+// out[c] (+)= sum over g < n of part[g, c]: 16 columns per block (so that more
+// SMs take part), 64 threads of each take every 64th partial, their loads in
+// flight together, then their sums in a fixed tree.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, long long n, int d,
+                                                          float* out, int accumulate) {
+  __shared__ float s[64][17];
   grid_dep_launch();
   grid_dep_wait();
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  const int c = blockIdx.x * 16 + threadIdx.x;
   float acc = 0.f;
   if (c < d) {
 #pragma unroll 10
-    for (long long g = threadIdx.y; g < n; g += 32) acc += part[g * d + c];
+    for (long long g = threadIdx.y; g < n; g += 64) acc += part[g * d + c];
   }
   s[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
-  // column threadIdx.y, partial threadIdx.x
-  const float v = warp_sum(s[threadIdx.x][threadIdx.y]);
-  const int o = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && o < d) out[o] = accumulate ? out[o] + v : v;
+  const int t = threadIdx.y * 16 + threadIdx.x, col = t >> 5, lane = t & 31;
+  if (col >= 16) return;
+  const float v = warp_sum(s[lane][col] + s[lane + 32][col]);
+  const int o = blockIdx.x * 16 + col;
+  if (lane == 0 && o < d) out[o] = accumulate ? out[o] + v : v;
 }
 
 cudaError_t launch_column_sum(const float* part, int64_t n, int64_t d, float* out,
                               bool accumulate, cudaStream_t st) {
   ProfScope prof("column_sum", st);
   const cudaError_t e =
-      launch_dependent(column_sum_kernel, dim3(static_cast<unsigned>((d + 31) / 32)),
-                       dim3(32, 32), 0, st, part, n, d, out, accumulate ? 1 : 0);
+      launch_dependent(column_sum_kernel, dim3(static_cast<unsigned>((d + 15) / 16)),
+                       dim3(16, 64), 0, st, part, n, d, out, accumulate ? 1 : 0);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -626,10 +626,11 @@ BwdShape bwd_shape(int64_t rows, int64_t d, bool vec, int64_t row_bytes) {
   b.depth = 0;
   int per_sm = 768 / (b.tpr * b.rpb);
   if (vec && d >= kBulkMinD) {
-    // a row's chain of barrier and reductions is about 1100 cycles, in which an
-    // SM's share of the memory moves 26 KB: enough blocks to cover it half as
-    // much again, and few, since each leaves a partial weight gradient
-    const int64_t cover = 40 * 1024 / (row_bytes + row_bytes / 3) + 1;
+    // a row's chain of barrier and reductions takes a block long enough for an
+    // SM's share of the memory to move some 70 KB: enough blocks to cover it
+    // (4099 x 2880 bf16: 29.7 us with two, 24.5 with three, 23.8 with four or
+    // more), and no more, since each leaves a partial weight gradient
+    const int64_t cover = 72 * 1024 / (row_bytes + row_bytes / 3) + 1;
     if (per_sm > cover) per_sm = static_cast<int>(cover < 2 ? 2 : cover);
     // a ring of at least three rows per block where that leaves two blocks
     while (per_sm > 2 && per_sm * 3 * row_bytes > kBulkSmem) --per_sm;
