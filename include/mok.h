@@ -492,12 +492,12 @@ typedef struct mok_linear_desc {
  * cores and rounded once to y_elem.  x bf16 [M,K] (stride ld_x), w bf16 [N,K],
  * bias fp32 [N] or NULL, residual [M,N] or NULL (may equal y), y [M,N];
  * z [M,N] or NULL: the pre-activation, for the backward.  x, w 16-byte
- * aligned, the others to their elements.  status: as in
- * mok_router_balance_forward; a bounded wait that gave up sets
- * MOK_ERR_DEVICE_TIMEOUT. */
+ * aligned, the others to their elements.  workspace: see the size query (NULL
+ * where it says 0).  status: as in mok_router_balance_forward; a bounded wait
+ * that gave up sets MOK_ERR_DEVICE_TIMEOUT. */
 mok_status mok_linear_forward(const mok_linear_desc* desc, const void* x, const void* w,
                               const float* bias, const void* residual, void* y, void* z,
-                              int32_t* status, void* stream);
+                              void* workspace, size_t ws_bytes, int32_t* status, void* stream);
 
 /* Backward from dy [M,N] (y_elem):  dz = dy act'(z);
  *   dx [M,K] (dx_elem) = dz w,  dw fp32 [N,K] = dz^T x,  dbias fp32 [N] =
@@ -510,7 +510,8 @@ mok_status mok_linear_forward(const mok_linear_desc* desc, const void* x, const 
 mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, const void* x,
                                const void* w, const void* z, void* dx, float* dw, float* dbias,
                                void* workspace, size_t ws_bytes, int32_t* status, void* stream);
-mok_status mok_linear_workspace_size(const mok_linear_desc* desc, size_t* bytes);
+/* Bytes of scratch of the forward (backward = 0; may be 0) or the backward (1). */
+mok_status mok_linear_workspace_size(const mok_linear_desc* desc, int backward, size_t* bytes);
 
 /* Waits for `stream`, then reads the device status word at the start of
  * `buf` (the `saved` buffer of forward/backward, or the workspace of the

@@ -91,10 +91,11 @@ _SIGS = {
     "mok_router_balance_workspace_size": (c_int32, [ctypes.POINTER(BalanceDesc),
                                                     ctypes.POINTER(c_size_t)]),
     "mok_router_balance_backward": (c_int32, [ctypes.POINTER(BalanceDesc)] + [c_void_p] * 8),
-    "mok_linear_forward": (c_int32, [ctypes.POINTER(LinearDesc)] + [c_void_p] * 8),
+    "mok_linear_forward": (c_int32, [ctypes.POINTER(LinearDesc)] + [c_void_p] * 7
+                           + [c_size_t, c_void_p, c_void_p]),
     "mok_linear_backward": (c_int32, [ctypes.POINTER(LinearDesc)] + [c_void_p] * 8
                             + [c_size_t, c_void_p, c_void_p]),
-    "mok_linear_workspace_size": (c_int32, [ctypes.POINTER(LinearDesc),
+    "mok_linear_workspace_size": (c_int32, [ctypes.POINTER(LinearDesc), c_int32,
                                             ctypes.POINTER(c_size_t)]),
     "mok_selftest_bounded_wait": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_fill_zero": (c_int32, [c_void_p, c_size_t, c_void_p]),

@@ -262,12 +262,13 @@ def router_balance_backward(dloss, logits, lse, counts, n_valid, k, mask=None, *
 
 
 def linear(x, w, bias=None, *, act="none", residual=None, out_dtype=None, y=None, z=None,
-           keep_z=False, stream=None):
+           keep_z=False, workspace=None, stream=None):
     """y = act(x w^T + bias) + residual (see mok_linear_forward); with keep_z,
     (y, z) with the pre-activation z for `linear_backward`.  x [M, K] and w
     [N, K] bf16 (K a multiple of 8), bias fp32 [N]; y, z and residual [M, N] of
     out_dtype, bf16 (the default) or fp32."""
-    return _ops().linear(x, w, bias, _act(act), residual, out_dtype, y, z, keep_z, stream)
+    return _ops().linear(x, w, bias, _act(act), residual, out_dtype, y, z, keep_z, workspace,
+                         stream)
 
 
 def linear_backward(dy, x, w, z=None, *, act="none", bias=False, dx_dtype=None, dx=None, dw=None,

@@ -173,26 +173,33 @@ mok_status mok_router_balance_backward(const mok_balance_desc* desc, const float
 
 mok_status mok_linear_forward(const mok_linear_desc* desc, const void* x, const void* w,
                               const float* bias, const void* residual, void* y, void* z,
-                              int32_t* status, void* stream) {
+                              void* workspace, size_t ws_bytes, int32_t* status, void* stream) {
   mok_linear_desc D;
   mok_status st = linear_desc(desc, &D);
   if (st != MOK_OK) return st;
   if (!w || (D.M > 0 && (!x || !y))) return MOK_ERR_INVALID_ARG;
   const size_t ye = elem_size(D.y_elem);
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(residual, ye) ||
-      !aligned(y, ye) || !aligned(z, ye) || !aligned(status, 4))
+      !aligned(y, ye) || !aligned(z, ye) || !aligned(status, 4) || !aligned(workspace, 16))
     return MOK_ERR_INVALID_ARG;
+  const size_t need = linear_fwd_bytes(D);
+  if (need > 0 && !workspace) return MOK_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MOK_ERR_WORKSPACE;
   st = mok_check_device();
   if (st != MOK_OK) return st;
-  return cuda_status(launch_linear(D, x, w, bias, residual, y, z, status,
+  return cuda_status(launch_linear(D, x, w, bias, residual, y, z, workspace, status,
                                    static_cast<cudaStream_t>(stream)));
 }
 
-mok_status mok_linear_workspace_size(const mok_linear_desc* desc, size_t* bytes) {
+mok_status mok_linear_workspace_size(const mok_linear_desc* desc, int backward, size_t* bytes) {
   mok_linear_desc D;
   const mok_status st = linear_desc(desc, &D);
   if (st != MOK_OK) return st;
   if (!bytes) return MOK_ERR_INVALID_ARG;
+  if (!backward) {
+    *bytes = linear_fwd_bytes(D);
+    return MOK_OK;
+  }
   LinearWs W;
   linear_layout(D, &W);
   *bytes = W.total;

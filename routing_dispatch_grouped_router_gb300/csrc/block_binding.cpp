@@ -186,9 +186,11 @@ struct Scratch {
       p = given->data_ptr();
       n = given->nbytes();
     } else {
-      own = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
-      p = bytes ? own.data_ptr() : nullptr;
+      p = nullptr;
       n = bytes;
+      if (bytes == 0) return;
+      own = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
+      p = own.data_ptr();
     }
   }
 };
@@ -438,7 +440,7 @@ mok_linear_desc linear_desc(const Call& c, const at::Tensor& x, const at::Tensor
   return D;
 }
 
-// (x, w, bias, act, residual, out_dtype, y, z, keep_z, stream) -> y or (y, z)
+// (x, w, bias, act, residual, out_dtype, y, z, keep_z, workspace, stream) -> y or (y, z)
 PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t) {
   return guarded([&] {
     const at::Tensor& x = tensor(a[0], "x");
@@ -447,7 +449,7 @@ PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t) {
     const at::Tensor* res = tensor_or_null(a[4], "residual");
     const at::Tensor *y0 = tensor_or_null(a[6], "y"), *z0 = tensor_or_null(a[7], "z");
     const bool keep = PyObject_IsTrue(a[8]) == 1;
-    const Call c(x, a[9]);
+    const Call c(x, a[10]);
     mok_linear_desc D = linear_desc(c, x, w, integer(a[3]));
     const at::ScalarType dt =
         dtype_or(a[5], y0 ? y0->scalar_type() : at::kBFloat16, "out_dtype");
@@ -469,8 +471,11 @@ PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t) {
       type_is(*res, "residual", dt);
     }
     D.y_elem = elem(dt);
+    size_t n = 0;
+    check(mok_linear_workspace_size(&D, 0, &n), "mok_linear_workspace_size");
+    const Scratch ws(c, tensor_or_null(a[9], "workspace"), n);
     check(mok_linear_forward(&D, addr(x), addr(w), static_cast<float*>(addr(bias)), addr(res),
-                             addr(y), addr(z), c.status(), c.raw),
+                             addr(y), addr(z), ws.p, ws.n, c.status(), c.raw),
           "mok_linear_forward");
     return keep ? tuple({y, z}) : wrap(y);
   });
@@ -518,7 +523,7 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     D.dx_elem = elem(dt);
     D.accumulate = acc;
     size_t n = 0;
-    check(mok_linear_workspace_size(&D, &n), "mok_linear_workspace_size");
+    check(mok_linear_workspace_size(&D, 1, &n), "mok_linear_workspace_size");
     const Scratch ws(c, tensor_or_null(a[11], "workspace"), n);
     check(mok_linear_backward(&D, addr(dy), addr(x), addr(w), addr(z), addr(dx),
                               static_cast<float*>(addr(dw)), static_cast<float*>(addr(db)), ws.p,
@@ -562,7 +567,7 @@ PyMethodDef methods[] = {
     MOK_METHOD(add_rmsnorm_backward, 10),
     MOK_METHOD(router_balance, 7),
     MOK_METHOD(router_balance_backward, 11),
-    MOK_METHOD(linear, 10),
+    MOK_METHOD(linear, 11),
     MOK_METHOD(linear_backward, 13),
     {nullptr, nullptr, 0, nullptr},
 };

@@ -58,8 +58,14 @@ enum Epi : int {
   // (the dense product with its epilogue, and plain C for its gradients)
   EPI_LIN_F32 = 7,
   EPI_LIN_BF16 = 8,
+  // the same by plain accesses, for C, z, residual or bias without 16-byte
+  // aligned rows: a warp's 32 lanes the 32 columns of a row
+  EPI_LIN_F32_D = 9,
+  EPI_LIN_BF16_D = 10,
 };
-constexpr bool linear_epi(int epi) { return epi == EPI_LIN_F32 || epi == EPI_LIN_BF16; }
+constexpr bool linear_epi(int epi) { return epi >= EPI_LIN_F32; }
+constexpr bool linear_f32(int epi) { return epi == EPI_LIN_F32 || epi == EPI_LIN_F32_D; }
+constexpr bool linear_direct(int epi) { return epi >= EPI_LIN_F32_D; }
 // Split operands: a bf16 "hi" tile plus a bf16 "lo" tile (value - hi) whose
 // products are accumulated into the same fp32 accumulator, giving the GEMM
 // an operand with ~16 significant bits.
@@ -141,9 +147,10 @@ struct GemmArgs {
   const void* res;
   int act;
   int store_z;
-  // EPI_LIN_F32: K blocks of one accumulation on the tensor cores (see
+  // EPI_LIN_F32*: K blocks of one accumulation on the tensor cores (see
   // kChunkMmas); the chunks' sums are added in fp32 registers
   int chunk_kb;
+  void* z;  // EPI_LIN_*_D: z (NULL: not stored)
   int* status;
 };
 
@@ -165,10 +172,10 @@ struct OutMaps {
 // goes through costs it about 1.7e-8 of its value (measured: K = 2048 in one
 // accumulation, 128 MMAs, 2.1e-6 off; 16384 values in three parts, 768 MMAs,
 // 1.4e-5; an fp32 sum with correct rounding is 4e-7 off).  An fp32 result of
-// the dense product is therefore accumulated over at most this many MMAs at a
+// the dense product is therefore accumulated over at most this many MMAs (6e-7) at a
 // time, and the chunks are added in registers with correct rounding while the
 // other accumulator takes the next one.
-constexpr int kChunkMmas = 32;
+constexpr int kChunkMmas = 36;
 
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
@@ -733,6 +740,40 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, 
                                              const CUtensorMap* tmH) {
   const int y = tl.e * a.m_rows + tl.row0 + q * 32;
   const long long row = tl.row0 + q * 32 + lane;
+  if constexpr (linear_direct(EPI)) {
+    // C's values through the staging buffer (fp32, the swizzled layout), so that
+    // lane i then holds column x + i of each row in turn
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<float4*>(stage_buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+          make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+    const int col = x + lane;
+    if (col >= a.n_valid) return;
+    const float bias = a.bias ? a.bias[col] : 0.f;
+    const int rows = a.m_valid - (tl.row0 + q * 32) < 32 ? a.m_valid - (tl.row0 + q * 32) : 32;
+    const long long o0 = static_cast<long long>(y) * a.n_valid + col;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) {
+      const long long o = o0 + static_cast<long long>(r) * a.n_valid;
+      float t = *reinterpret_cast<const float*>(
+          stage_buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+      t += bias;
+      if (linear_f32(EPI)) {
+        if (a.z) static_cast<float*>(a.z)[o] = t;
+        t = act_value(t, a.act);
+        if (a.res) t += static_cast<const float*>(a.res)[o];
+        static_cast<float*>(a.out)[o] = t;
+      } else {
+        if (a.z) static_cast<__nv_bfloat16*>(a.z)[o] = __float2bfloat16_rn(t);
+        t = act_value(t, a.act);
+        if (a.res) t += __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[o]);
+        static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(t);
+      }
+    }
+    return;
+  }
   if (a.bias) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -1259,7 +1300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ GemmArgs args, const __grid_constant__ OutMaps om) {
   using C = Cfg<BN, SPLIT, PAIR, staging_bytes<EPI, SPLIT, SCHED, DB>()>;
   constexpr bool kDbuf = DB;
-  constexpr bool kChunks = EPI == EPI_LIN_F32 && !DB;
+  constexpr bool kChunks = linear_f32(EPI) && !DB;
   static_assert(!DB || ((EPI == EPI_F32 || EPI == EPI_F32_T) && SCHED == SCHED_KGROUP) ||
                     (EPI == EPI_SWIGLU_BWD && PAIR) || linear_epi(EPI),
                 "DB: double-buffered staging of the fp32 weight gradients, the SwiGLU "
@@ -1294,7 +1335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* gu_bar = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF + 256);
   constexpr bool kTmaStore = (EPI == EPI_F32 && SCHED != SCHED_DENSE) || EPI == EPI_SWIGLU_FWD ||
                              EPI == EPI_F32_T || EPI == EPI_SWIGLU_BWD || EPI == EPI_BF16_TMA ||
-                             EPI == EPI_BF16_T || linear_epi(EPI);
+                             EPI == EPI_BF16_T ||
+                             (linear_epi(EPI) && !linear_direct(EPI));
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1325,7 +1367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmB);
     if (kTmaStore) tma_prefetch_desc(&tmC);
     if (SPLIT == SPLIT_A3) tma_prefetch_desc(&om.sfa);
-    if (linear_epi(EPI) && args.store_z) tma_prefetch_desc(&om.h);
+    if (linear_epi(EPI) && !linear_direct(EPI) && args.store_z) tma_prefetch_desc(&om.h);
     if (block_scaled(SPLIT) && PAIR) {
       tma_prefetch_desc(&om.sfa);
       tma_prefetch_desc(&om.sfb);
@@ -2552,8 +2594,10 @@ constexpr int kWideKb = 8;
 
 // fp32 or bf16 C or z in 32 x 32 blocks; wide: bf16 in 32 x 64 ones
 static bool make_lin_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, bool f32,
-                         bool wide = false) {
-  if (f32) return make_out_map(m, base, cols, rows);
+                         bool wide = false, uint64_t ld = 0) {
+  if (f32)
+    return make_map_t(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, cols, rows, ld ? ld : cols, 32,
+                      32);
   return wide ? make_out_map_bf16(m, base, cols, rows) : make_out_map_bf16_t(m, base, cols, rows);
 }
 
@@ -2581,17 +2625,21 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
              : make_map(&tb, B, K, a.n_valid, ld_b, pair ? 128 : bn)))
     return cudaErrorInvalidValue;
   const int parts = Cfg<BN1, SPLIT>::A_TILES;
-  const bool plain = !a.bias && !a.res && a.act == MOK_ACT_NONE && !a.store_z;
+  const bool plain = !a.bias && !a.res && a.act == MOK_ACT_NONE && !a.store_z &&
+                     !linear_direct(EPI);
   // short K: the stores set the pace (and an fp32 result is one accumulation)
   const bool wide = pair && plain && a.num_kb * parts <= kWideKb &&
                     (EPI != EPI_LIN_F32 || a.num_kb <= a.chunk_kb);
-  CUtensorMap tc;
-  if (!make_lin_map(&tc, a.out, a.n_valid, splits > 1 ? splits * a.m_rows : a.m_valid,
-                    EPI == EPI_LIN_F32, wide))
+  CUtensorMap tc = ta;
+  if (!linear_direct(EPI) &&
+      !make_lin_map(&tc, a.out, a.n_valid, splits > 1 ? splits * a.m_rows : a.m_valid,
+                    EPI == EPI_LIN_F32, wide, static_cast<uint64_t>(a.ldo)))
     return cudaErrorInvalidValue;
-  if (wide)
-    return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true, true>(
-        name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
+  if constexpr (!linear_direct(EPI)) {
+    if (wide)
+      return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true, true>(
+          name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
+  }
   if (pair)
     return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true>(
         name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
@@ -2601,12 +2649,12 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
 
 cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
                             const void* w, const float* bias, const void* res, int act, void* y,
-                            void* z, bool f32, int* status, cudaStream_t st) {
+                            void* z, bool f32, bool direct, int* status, cudaStream_t st) {
   CUtensorMap ta;
   if (!make_map(&ta, x, K, M, ld_x, 128)) return cudaErrorInvalidValue;
   OutMaps om;
   memset(&om, 0, sizeof(om));
-  if (z && !make_lin_map(&om.h, z, N, M, f32)) return cudaErrorInvalidValue;
+  if (z && !direct && !make_lin_map(&om.h, z, N, M, f32)) return cudaErrorInvalidValue;
   GemmArgs a = blank_args(status);
   a.out = y;
   a.m_tiles = (int)((M + 127) / 128);
@@ -2616,11 +2664,36 @@ cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const
   a.res = res;
   a.act = act;
   a.store_z = z ? 1 : 0;
+  a.z = z;
+  if (direct)
+    return f32 ? dense_linear<false, false, EPI_LIN_F32_D, SPLIT_NONE>("linear", ta, w, K, K, a,
+                                                                       st, nullptr, &om)
+               : dense_linear<false, false, EPI_LIN_BF16_D, SPLIT_NONE>("linear", ta, w, K, K, a,
+                                                                        st, nullptr, &om);
   if (f32)
     return dense_linear<false, false, EPI_LIN_F32, SPLIT_NONE>("linear", ta, w, K, K, a, st,
                                                                nullptr, &om);
   return dense_linear<false, false, EPI_LIN_BF16, SPLIT_NONE>("linear", ta, w, K, K, a, st,
                                                               nullptr, &om);
+}
+
+cudaError_t gemm_linear_part(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
+                             const void* w, float* part, int splits, int* status,
+                             cudaStream_t st) {
+  CUtensorMap ta;
+  if (!make_map(&ta, x, K, M, ld_x, 128)) return cudaErrorInvalidValue;
+  OutMaps om;
+  memset(&om, 0, sizeof(om));
+  GemmArgs a = blank_args(status);
+  a.out = part;
+  a.ldo = (N + 3) / 4 * 4;
+  a.m_tiles = (int)((M + 127) / 128);
+  a.k_splits = splits;
+  a.m_rows = a.m_tiles * 128;
+  a.m_valid = a.m_rows;
+  a.n_valid = (int)N;
+  return dense_linear<false, false, EPI_LIN_F32, SPLIT_NONE>("linear_part", ta, w, K, K, a, st,
+                                                             nullptr, &om);
 }
 
 // The parts of dz as A maps with boxes of box_rows rows: part 0 in *ta, the
@@ -2634,7 +2707,8 @@ static bool dz_maps(const BfParts& dz, int64_t M, int64_t N, uint32_t box_rows, 
 }
 
 cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* w,
-                           void* dx, bool f32, bool accumulate, int* status, cudaStream_t st) {
+                           void* dx, bool f32, bool accumulate, int splits, int* status,
+                           cudaStream_t st) {
   // dx [M, K] = dz [M, N] w [N, K]: the reduction runs over N
   CUtensorMap ta, tl;
   OutMaps om;
@@ -2643,10 +2717,17 @@ cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, c
   a.out = dx;
   a.m_tiles = (int)((M + 127) / 128);
   a.m_valid = (int)M;
+  if (splits > 1) {
+    a.k_splits = splits;
+    a.m_rows = a.m_tiles * 128;
+    a.m_valid = a.m_rows;
+  }
   a.n_valid = (int)K;
   a.accumulate = accumulate ? 1 : 0;
   const char* name = "linear_dx";
   if (f32) {
+    if (dz.n == 2)
+      return dense_linear<false, true, EPI_LIN_F32, SPLIT_A>(name, ta, w, N, K, a, st, &tl, &om);
     if (dz.n == 3)
       return dense_linear<false, true, EPI_LIN_F32, SPLIT_A3>(name, ta, w, N, K, a, st, &tl,
                                                               &om);

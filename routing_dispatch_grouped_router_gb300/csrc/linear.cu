@@ -27,7 +27,6 @@ namespace {
 // (These kernels may start before the one in front of them on the stream has
 // ended, so they read with plain loads, after grid_dep_wait: the non-coherent
 // path is for memory that nothing writes while a kernel lives.)
-constexpr int kEngineTiles = 38;
 constexpr int kFewTokens = 8;
 constexpr int kMaxSplits = 8;  // CTAs of a portable cluster
 constexpr int kLinThreads = 192;  // TMA warp, MMA warp, four epilogue warps
@@ -63,8 +62,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return v;
 }
 
@@ -99,36 +97,57 @@ __device__ __forceinline__ void store1(void* p, long long o, float v) {
   else static_cast<__nv_bfloat16*>(p)[o] = __float2bfloat16_rn(v);
 }
 
-// Features n .. n+3 of token m from their sums.
+// The bias of features n .. n+3, and the residual of token m there (zeros where
+// there is none).
+__device__ __forceinline__ void bias4(const LinArgs& a, int n, float (&t)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) t[j] = 0.f;
+  if (!a.bias || n >= a.N) return;
+  if (a.vec) {
+    load4<true>(a.bias, n, t);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < a.N) t[j] = a.bias[n + j];
+  }
+}
 template <bool F32>
-__device__ __forceinline__ void finish4(const LinArgs& a, long long m, int n, float (&v)[4]) {
+__device__ __forceinline__ void res4(const LinArgs& a, long long m, int n, float (&t)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) t[j] = 0.f;
+  if (!a.res || n >= a.N) return;
   const long long o = m * a.N + n;
   if (a.vec) {
-    if (n >= a.N) return;
-    float t[4];
-    if (a.bias) {
-      load4<true>(a.bias, n, t);
+    load4<F32>(a.res, o, t);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += t[j];
-    }
+    for (int j = 0; j < 4; ++j)
+      if (n + j < a.N) t[j] = load1<F32>(a.res, o + j);
+  }
+}
+
+// Features n .. n+3 of token m from their sums, with their bias and residual
+// (loaded beforehand: the stores here would hold the loads of the next back).
+template <bool F32>
+__device__ __forceinline__ void finish4(const LinArgs& a, long long m, int n, float (&v)[4],
+                                        const float (&bias)[4], const float (&res)[4]) {
+  if (n >= a.N) return;
+  const long long o = m * a.N + n;
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] += bias[j];
+    y[j] = act_value(v[j], a.act) + res[j];
+  }
+  if (a.vec) {
     if (a.z) store4<F32>(a.z, o, v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = act_value(v[j], a.act);
-    if (a.res) {
-      load4<F32>(a.res, o, t);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += t[j];
-    }
-    store4<F32>(a.y, o, v);
+    store4<F32>(a.y, o, y);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (n + j >= a.N) break;
-      float t = v[j] + (a.bias ? a.bias[n + j] : 0.f);
-      if (a.z) store1<F32>(a.z, o + j, t);
-      t = act_value(t, a.act);
-      if (a.res) t += load1<F32>(a.res, o + j);
-      store1<F32>(a.y, o + j, t);
+      if (a.z) store1<F32>(a.z, o + j, v[j]);
+      store1<F32>(a.y, o + j, y[j]);
     }
   }
 }
@@ -145,19 +164,22 @@ __device__ __forceinline__ void finish1(const LinArgs& a, long long m, int n, fl
 }
 
 // Up to MT tokens, on the CUDA cores: bound by the bytes of w, which each
-// thread streams with 16-byte loads, as many in flight as its registers take;
-// no ring, tensor memory or cluster to set up (one token, N = 2048, K = 7168:
-// 13.5 us on the tensor cores).  A block takes R rows of w, its eight warps go
-// round the 256-value chunks of K, a lane eight values of each; the block's
-// sums are the lanes' (shuffles), then the warps' in order.
+// thread streams with 16-byte loads, sixteen of them in flight; no ring, tensor
+// memory or cluster to set up (one token, N = 2048, K = 7168: 13.5 us on the
+// tensor cores, 5.9 here).  A warp takes R rows of w and goes round the
+// 256-value chunks of K, a lane eight values of each; `wk` of the block's eight
+// warps share K (a power of two), the others take further rows.  The sums are
+// the lanes' (shuffles), then the wk warps' in order.
 constexpr int kFewThreads = 256;
-template <int MT, int R, bool F32>
-__global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
-    const __nv_bfloat16* x, long long ld_x, const __nv_bfloat16* w, int K, LinArgs a) {
+template <int MT, int R, int wk, bool F32>
+__global__ void __launch_bounds__(kFewThreads)
+    linear_few_kernel(const __nv_bfloat16* x, long long ld_x, const __nv_bfloat16* w, int K,
+                      LinArgs a) {
   constexpr int U = 16 / R;  // chunks in flight
   __shared__ float s_sum[8][R * MT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n0 = blockIdx.x * R;
+  const int kw = warp & (wk - 1), rw = warp / wk;  // share of K, row group
+  const int n0 = (blockIdx.x * (8 / wk) + rw) * R;
   grid_dep_launch();
   grid_dep_wait();
   float acc[R][MT];
@@ -165,11 +187,12 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = 0.f;
-  for (int c0 = warp * 256 + lane * 8; c0 < K; c0 += 8 * 256 * U) {
+  constexpr int step = wk * 256;
+  for (int c0 = kw * 256 + lane * 8; c0 < K; c0 += step * U) {
     uint4 wv[U][R];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = c0 + u * 8 * 256;
+      const int k = c0 + u * step;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         wv[u][r] = make_uint4(0u, 0u, 0u, 0u);
@@ -179,7 +202,7 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = c0 + u * 8 * 256;
+      const int k = c0 + u * step;
       if (k >= K) break;
       float xf[MT][8];
 #pragma unroll
@@ -212,17 +235,18 @@ __global__ void __launch_bounds__(kFewThreads) linear_few_kernel(
       if (lane == 0) s_sum[warp][m * R + r] = v;
     }
   __syncthreads();
-  if (threadIdx.x < R * MT) {
-    const int m = threadIdx.x / R, n = n0 + threadIdx.x % R;
+  for (int i = threadIdx.x; i < 8 / wk * R * MT; i += kFewThreads) {
+    const int g = i / (R * MT), o = i % (R * MT);  // row group, element
+    const int m = o / R, n = (blockIdx.x * (8 / wk) + g) * R + o % R;
     float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v += s_sum[q][threadIdx.x];
+    for (int q = 0; q < wk; ++q) v += s_sum[g * wk + q][o];
     if (m < a.M && n < a.N) finish1<F32>(a, m, n, v);
   }
 }
 
 // grid (K splits = the cluster, feature tiles, token tiles)
-template <int BN, bool F32>
+template <int BN, bool F32, int KS>
 __global__ void __launch_bounds__(kLinThreads)
     linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const LinArgs args) {
@@ -237,7 +261,8 @@ __global__ void __launch_bounds__(kLinThreads)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ks = gridDim.x, split = blockIdx.x;
+  constexpr int ks = KS;  // = gridDim.x, the cluster
+  const int split = blockIdx.x;
   const int n0 = blockIdx.y * 128, m0 = blockIdx.z * BN;
   const int kb0 = static_cast<int>(static_cast<long long>(args.nkb) * split / ks);
   const int kb1 = static_cast<int>(static_cast<long long>(args.nkb) * (split + 1) / ks);
@@ -389,30 +414,40 @@ __global__ void __launch_bounds__(kLinThreads)
   __syncwarp();
   if (ks > 1) cluster_sync(); else __syncthreads();
   // this CTA's share of the tokens, four features per thread, the cluster's
-  // sums in rank order; all of an element's remote loads go out together
+  // sums in rank order; the remote loads of several elements go out together
+  // (their latency is most of a small call's epilogue)
   if (!*vabort) {
-    const uint32_t part = smem_addr(smem);
+    const uint32_t part = smem_addr(smem) + lane * 16u;
+    const int n = n0 + 4 * lane;
+    float bias[4];
+    bias4(args, n, bias);
     const int tokens = args.M - m0 < BN ? args.M - m0 : BN;
-    const int share = (tokens - split + ks - 1) / ks;  // tokens split, split + ks, ..
-    const int nf = args.N - n0 < 128 ? (args.N - n0 + 3) / 4 : 32;
-    for (int i = threadIdx.x; i < share * nf; i += kLinThreads) {
-      const int m = split + ks * (i / nf), f4 = 4 * (i % nf);
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (ks == 1) {
-        const float4 p = *reinterpret_cast<const float4*>(smem + (m * 128 + f4) * 4);
-        v[0] = p.x; v[1] = p.y; v[2] = p.z; v[3] = p.w;
-      } else {
-        const uint32_t at = part + static_cast<uint32_t>(m * 128 + f4) * 4u;
-        float4 p[kMaxSplits];
+    constexpr int B = KS >= 8 ? 2 : (KS == 4 ? 4 : 8);  // a warp's tokens at a time
+    constexpr int kStep = ks * (kLinThreads / 32);
+    for (int t0 = split + ks * warp; t0 < tokens; t0 += B * kStep) {
+      float4 p[B][KS];
+      float res[B][4];
 #pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-          p[r] = r < ks ? ld_cluster_f4(mapa_shared(at, r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int b = 0; b < B; ++b) {
+        const int m = t0 + b * kStep;
+        if (m >= tokens || n >= args.N) break;
+        res4<F32>(args, m0 + m, n, res[b]);
 #pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r) {
-          v[0] += p[r].x; v[1] += p[r].y; v[2] += p[r].z; v[3] += p[r].w;
-        }
+        for (int r = 0; r < KS; ++r)
+          p[b][r] = KS == 1 ? *reinterpret_cast<const float4*>(smem + (m * 128 + 4 * lane) * 4)
+                            : ld_cluster_f4(mapa_shared(part + static_cast<uint32_t>(m) * 512u, r));
       }
-      finish4<F32>(args, m0 + m, n0 + f4, v);
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int m = t0 + b * kStep;
+        if (m >= tokens || n >= args.N) break;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < KS; ++r) {
+          v[0] += p[b][r].x; v[1] += p[b][r].y; v[2] += p[b][r].z; v[3] += p[b][r].w;
+        }
+        finish4<F32>(args, m0 + m, n, v, bias, res[b]);
+      }
     }
   }
   __syncwarp();
@@ -435,19 +470,20 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   if (!make_tensor_map_2d(&tw, bf, 2, w, D.K, D.N, D.K, 64, 128, sw) ||
       !make_tensor_map_2d(&tx, bf, 2, x, D.K, D.M, D.ld_x, 64, BN, sw))
     return cudaErrorInvalidValue;
-  auto kern = linear_kernel<BN, F32>;
+  const int64_t nt = (D.N + 127) / 128, mt = (D.M + BN - 1) / BN;
+  if (nt > 65535 || mt > 65535) return cudaErrorInvalidConfiguration;
+  // K splits: a power of two, as many as the CTAs that fit at once leave room
+  // for, at least four 64-value blocks each
+  const int64_t slots = static_cast<int64_t>(num_sms_current_device()) * (BN <= 64 ? 2 : 1);
+  int ks = 1;
+  while (ks < kMaxSplits && nt * mt * ks * 2 <= slots && a.nkb >= ks * 8) ks *= 2;
+  auto kern = ks == 1   ? linear_kernel<BN, F32, 1>
+              : ks == 2 ? linear_kernel<BN, F32, 2>
+              : ks == 4 ? linear_kernel<BN, F32, 4>
+                        : linear_kernel<BN, F32, 8>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t nt = (D.N + 127) / 128, mt = (D.M + BN - 1) / BN;
-  if (nt > 65535 || mt > 65535) return cudaErrorInvalidConfiguration;
-  // K splits: as many as the CTAs that fit at once leave room for, at least
-  // four 64-value blocks each
-  const int64_t slots = static_cast<int64_t>(num_sms_current_device()) * (BN <= 64 ? 2 : 1);
-  int64_t ks = slots / (nt * mt);
-  if (ks > kMaxSplits) ks = kMaxSplits;
-  if (ks > a.nkb / 4) ks = a.nkb / 4;
-  if (ks < 1) ks = 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -470,11 +506,77 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   return cudaGetLastError();
 }
 
+// Split-K products: y = act(sum of the parts + bias) + residual, part s in rows
+// s * m_pad.. of `part` (row stride N rounded up to 4), added in order.
+template <bool F32>
+__global__ void __launch_bounds__(256) linear_finish_kernel(LinArgs a, const float* part,
+                                                            int splits, long long stride) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int n4 = (a.N + 3) / 4;
+  const long long items = static_cast<long long>(a.M) * n4;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < items; i += gridDim.x * 256LL) {
+    const float4* p = reinterpret_cast<const float4*>(part) + i;
+    const long long m = i / n4;
+    const int n = static_cast<int>(i - m * n4) * 4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, bias[4], res[4];
+    bias4(a, n, bias);
+    res4<F32>(a, m, n, res);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4 t = p[s * stride];
+      v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;
+    }
+    finish4<F32>(a, m, n, v, bias, res);
+  }
+}
+
+cudaError_t launch_finish(const LinArgs& a, const float* part, int splits, bool f32,
+                          cudaStream_t st) {
+  const long long n4 = (a.N + 3) / 4, items = a.M * n4;
+  const long long stride = (static_cast<long long>(a.M) + 127) / 128 * 128 * n4;
+  long long blocks = (items + 255) / 256;
+  const long long cap = 8LL * num_sms_current_device();
+  if (blocks > cap) blocks = cap;
+  ProfScope prof("linear_finish", st);
+  const cudaError_t e =
+      launch_dependent(f32 ? linear_finish_kernel<true> : linear_finish_kernel<false>,
+                       dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, part, splits,
+                       stride);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Shapes for the persistent engine: more than one 128-row tile of tokens.
+bool engine_takes(const mok_linear_desc& D) { return D.M > 128; }
+
+// K splits of an engine product C [M, N], reduction K: as many as its 256 x 256
+// tiles leave CTA pairs for (76 of a GB300, whatever the device, so that sums
+// do not depend on it), at least four K blocks each.  A second kernel adds them.
+int engine_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), nkb = (K + 63) / 64;
+  int64_t ks = 76 / tiles;
+  if (ks > nkb / 4) ks = nkb / 4;
+  if (ks > 16) ks = 16;
+  if (ks < 2) return 1;
+  const int64_t kb = (nkb + ks - 1) / ks;
+  return static_cast<int>((nkb + kb - 1) / kb);  // no empty split
+}
+
+size_t part_bytes(int splits, int64_t M, int64_t N) {
+  return splits > 1 ? static_cast<size_t>(splits) * ((M + 127) / 128 * 128) * ((N + 3) / 4) * 16
+                    : 0;
+}
+
 }  // namespace
 
+size_t linear_fwd_bytes(const mok_linear_desc& D) {
+  return engine_takes(D) ? part_bytes(engine_splits(D.M, D.N, D.K), D.M, D.N) : 0;
+}
+
 cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w,
-                          const float* bias, const void* res, void* y, void* z, int* status,
-                          cudaStream_t st) {
+                          const float* bias, const void* res, void* y, void* z, void* ws,
+                          int* status, cudaStream_t st) {
   if (D.M == 0) return cudaSuccess;
   LinArgs a;
   a.bias = bias; a.res = res; a.y = y; a.z = z;
@@ -484,35 +586,54 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
   a.act = D.act;
   a.status = status;
   const bool f32 = D.y_elem == MOK_ELEM_F32;
-  // an fp32 result: at most 32 MMAs (8 blocks) in one accumulation, as in the
+  // an fp32 result: at most 36 MMAs (9 blocks) in one accumulation, as in the
   // persistent engine; a bf16 one hides what the accumulation truncates
-  a.chunk_kb = f32 ? 8 : a.nkb;
+  a.chunk_kb = f32 ? 9 : a.nkb;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(res) |
                          reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(z);
   a.vec = D.N % 4 == 0 && (bits & 15) == 0;
-  // the persistent engine's 256 x 256 tiles need enough of them to fill its CTA
-  // pairs; below that the tiles here, and their split of K, spread wider
-  const int64_t pair_tiles = ((D.M + 255) / 256) * ((D.N + 255) / 256);
-  if (D.M > 128 && pair_tiles >= kEngineTiles && D.N % 8 == 0 && (bits & 15) == 0)
-    return gemm_linear_fwd(D.M, D.N, D.K, D.ld_x, x, w, bias, res, D.act, y, z, f32, status, st);
-  if (D.M <= kFewTokens) {
+  if (engine_takes(D)) {
+    const int splits = engine_splits(D.M, D.N, D.K);
+    const bool direct = D.N % 8 != 0 || (bits & 15) != 0;
+    if (splits == 1)
+      return gemm_linear_fwd(D.M, D.N, D.K, D.ld_x, x, w, bias, res, D.act, y, z, f32, direct,
+                             status, st);
+    float* part = static_cast<float*>(ws);
+    const cudaError_t e =
+        gemm_linear_part(D.M, D.N, D.K, D.ld_x, x, w, part, splits, status, st);
+    if (e != cudaSuccess) return e;
+    return launch_finish(a, part, splits, f32, st);
+  }
+  // few tokens: on the CUDA cores while their products (M N K) do not take
+  // longer than the tensor-core kernel's setup (measured even at 6e7: M = 4,
+  // N = 2048, K = 7168, both 9 us; M = 8: 15 against 9)
+  if (D.M <= 2 || (D.M <= kFewTokens && D.M * D.N * D.K <= 50000000)) {
     ProfScope prof("linear_few", st);
     const auto* xb = static_cast<const __nv_bfloat16*>(x);
     const auto* wb = static_cast<const __nv_bfloat16*>(w);
     const int K = static_cast<int>(D.K);
     cudaError_t e = cudaSuccess;
-    auto run = [&](auto MT, auto R, auto F) {
-      constexpr int r = decltype(R)::value;
-      e = launch_dependent(linear_few_kernel<decltype(MT)::value, r, decltype(F)::value>,
-                           dim3(static_cast<unsigned>((D.N + r - 1) / r)), dim3(kFewThreads), 0,
-                           st, xb, D.ld_x, wb, K, a);
+    // warps along K while each has its chunks in flight full, or while the rows
+    // alone would leave SMs idle
+    auto launch = [&](auto MT, auto WK, auto F) {
+      constexpr int wk = decltype(WK)::value, rows = 4 * (8 / wk);
+      e = launch_dependent(linear_few_kernel<decltype(MT)::value, 4, wk, decltype(F)::value>,
+                           dim3(static_cast<unsigned>((D.N + rows - 1) / rows)),
+                           dim3(kFewThreads), 0, st, xb, D.ld_x, wb, K, a);
+    };
+    auto run = [&](auto MT, auto F) {
+      using std::integral_constant;
+      const int64_t many = 2LL * num_sms_current_device();
+      if (K <= 2048 && D.N >= 16 * many) launch(MT, integral_constant<int, 2>(), F);
+      else if (K <= 4096 && D.N >= 8 * many) launch(MT, integral_constant<int, 4>(), F);
+      else launch(MT, integral_constant<int, 8>(), F);
     };
     auto by_tokens = [&](auto F) {
       using std::integral_constant;
-      if (D.M == 1) run(integral_constant<int, 1>(), integral_constant<int, 4>(), F);
-      else if (D.M == 2) run(integral_constant<int, 2>(), integral_constant<int, 4>(), F);
-      else if (D.M <= 4) run(integral_constant<int, 4>(), integral_constant<int, 4>(), F);
-      else run(integral_constant<int, 8>(), integral_constant<int, 8>(), F);
+      if (D.M == 1) run(integral_constant<int, 1>(), F);
+      else if (D.M == 2) run(integral_constant<int, 2>(), F);
+      else if (D.M <= 4) run(integral_constant<int, 4>(), F);
+      else run(integral_constant<int, 8>(), F);
     };
     if (f32) by_tokens(std::true_type());
     else by_tokens(std::false_type());
@@ -695,8 +816,12 @@ void linear_layout(const mok_linear_desc& D, LinearWs* W) {
   for (int p = 0; p < 3; ++p) W->dz[p] = p * al(dz);
   W->part_bias = 3 * al(dz);
   W->part_dw = W->part_bias + al(static_cast<size_t>(W->bias_rows) * D.N * 4);
+  // partial products of dx, then of dw: one region
+  W->dx_splits = D.M > 128 ? engine_splits(D.M, D.K, W->n_pad) : 1;
   const size_t rows = static_cast<size_t>((D.N + 127) / 128 * 128);
-  W->total = W->part_dw + (W->dw_splits > 1 ? al(W->dw_splits * rows * D.K * 4) : 0);
+  const size_t a = part_bytes(W->dx_splits, D.M, D.K);
+  const size_t b = W->dw_splits > 1 ? W->dw_splits * rows * D.K * 4 : 0;
+  W->total = W->part_dw + al(a > b ? a : b);
 }
 
 cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const void* x,
@@ -765,9 +890,23 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
   if (dx) {
     BfParts d = dz;
     if (split && !dxf) d.n = 2;
-    const cudaError_t e =
-        gemm_linear_dx(D.M, D.N, D.K, d, w, dx, dxf, D.accumulate != 0, status, st);
+    const bool sum = W.dx_splits > 1;
+    float* part = reinterpret_cast<float*>(b + W.part_dw);
+    if (sum && split && !dxf && parts == 2) d.n = 2;
+    cudaError_t e = gemm_linear_dx(D.M, D.N, D.K, d, w, sum ? part : dx, sum || dxf,
+                                   !sum && D.accumulate != 0, W.dx_splits, status, st);
     if (e != cudaSuccess) return e;
+    if (sum) {
+      LinArgs f = {};
+      f.y = dx;
+      f.res = D.accumulate ? dx : nullptr;  // (fp32)
+      f.M = static_cast<int>(D.M);
+      f.N = static_cast<int>(D.K);
+      f.act = MOK_ACT_NONE;
+      f.vec = 1;
+      e = launch_finish(f, part, W.dx_splits, dxf, st);
+      if (e != cudaSuccess) return e;
+    }
   }
   if (dw) {
     float* part = reinterpret_cast<float*>(b + W.part_dw);

@@ -296,18 +296,25 @@ struct LinearWs {
   int64_t n_pad;      // row length of dz's parts
   int64_t bias_rows;  // partial bias gradients
   int dw_splits;      // partial weight gradients (1: none)
+  int dx_splits;      // partial products of dx (1: none)
 };
 void linear_layout(const mok_linear_desc& D, LinearWs* W);
 cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w,
-                          const float* bias, const void* res, void* y, void* z, int* status,
-                          cudaStream_t st);
+                          const float* bias, const void* res, void* y, void* z, void* ws,
+                          int* status, cudaStream_t st);
+size_t linear_fwd_bytes(const mok_linear_desc& D);  // scratch of launch_linear
 cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const void* x,
                               const void* w, const void* z, void* dx, float* dw, float* dbias,
                               void* ws, int* status, cudaStream_t st);
-// y, res, z, bias 16-byte aligned, N a multiple of 8
+// direct: y, res, z or bias not 16-byte aligned, or N not a multiple of 8
 cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
                             const void* w, const float* bias, const void* res, int act, void* y,
-                            void* z, bool f32, int* status, cudaStream_t st);
+                            void* z, bool f32, bool direct, int* status, cudaStream_t st);
+// split s's part of x w^T at rows s * (M padded to 128) of part, row stride N
+// rounded up to 4
+cudaError_t gemm_linear_part(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,
+                             const void* w, float* part, int splits, int* status,
+                             cudaStream_t st);
 // An fp32 operand as the sum of n bf16 parts (1: a bf16 tensor itself; 2:
 // about 16 significant bits; 3: all 24), each [M, N] with row stride ld (a
 // multiple of 8).
@@ -316,9 +323,11 @@ struct BfParts {
   int n;
   int64_t ld;
 };
-// fp32 dx: one or three parts; bf16 dx: one or two.  dw: one or three.
+// fp32 dx: one, two or three parts; bf16 dx: one or two.  dw: one or three.
+// splits > 1: fp32 parts of dx as gemm_linear_part's.
 cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* w,
-                           void* dx, bool f32, bool accumulate, int* status, cudaStream_t st);
+                           void* dx, bool f32, bool accumulate, int splits, int* status,
+                           cudaStream_t st);
 cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* x,
                            int64_t ld_x, float* dw, bool accumulate, int splits, int* status,
                            cudaStream_t st);
