@@ -754,22 +754,35 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, 
     const float bias = a.bias ? a.bias[col] : 0.f;
     const int rows = a.m_valid - (tl.row0 + q * 32) < 32 ? a.m_valid - (tl.row0 + q * 32) : 32;
     const long long o0 = static_cast<long long>(y) * a.n_valid + col;
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-      const long long o = o0 + static_cast<long long>(r) * a.n_valid;
-      float t = *reinterpret_cast<const float*>(
-          stage_buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-      t += bias;
-      if (linear_f32(EPI)) {
-        if (a.z) static_cast<float*>(a.z)[o] = t;
-        t = act_value(t, a.act);
-        if (a.res) t += static_cast<const float*>(a.res)[o];
-        static_cast<float*>(a.out)[o] = t;
-      } else {
-        if (a.z) static_cast<__nv_bfloat16*>(a.z)[o] = __float2bfloat16_rn(t);
-        t = act_value(t, a.act);
-        if (a.res) t += __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[o]);
-        static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(t);
+    // eight rows at a time, their residuals loaded before the stores, which
+    // would hold later loads back
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      float res[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const long long o = o0 + static_cast<long long>(r0 + i) * a.n_valid;
+        res[i] = 0.f;
+        if (a.res && r0 + i < rows)
+          res[i] = linear_f32(EPI) ? static_cast<const float*>(a.res)[o]
+                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[o]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i;
+        if (r >= rows) break;
+        const long long o = o0 + static_cast<long long>(r) * a.n_valid;
+        const float z = bias + *reinterpret_cast<const float*>(
+                                   stage_buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                   (lane & 3) * 4);
+        const float t = act_value(z, a.act) + res[i];
+        if (linear_f32(EPI)) {
+          if (a.z) static_cast<float*>(a.z)[o] = z;
+          static_cast<float*>(a.out)[o] = t;
+        } else {
+          if (a.z) static_cast<__nv_bfloat16*>(a.z)[o] = __float2bfloat16_rn(z);
+          static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(t);
+        }
       }
     }
     return;

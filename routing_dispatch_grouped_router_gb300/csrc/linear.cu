@@ -36,16 +36,16 @@ struct LinCfg {
   static constexpr int A_BYTES = 128 * 64 * 2;
   static constexpr int B_BYTES = BN * 64 * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // two CTAs per SM up to 64 tokens: a cluster's CTAs then find room (with one
-  // CTA of 220 KB per SM, 16 clusters of 8 did not all fit at once)
-  static constexpr int ROOM = BN <= 64 ? 108 * 1024 : 220 * 1024;
+  // two CTAs per SM, so that a cluster's CTAs find room (with one CTA of 220 KB
+  // per SM, 16 clusters of 8 did not all fit at once: 22 us instead of 13.5)
+  static constexpr int ROOM = 108 * 1024;
   static constexpr int STAGES = ROOM / STAGE_BYTES;
   static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
   static constexpr int ACC_COLS = BN;  // two accumulators
   static constexpr int TMEM_COLS = 2 * BN;
   static_assert(BN * 128 * 4 <= BAR_OFF, "the partial sums fit the operand ring");
-  static_assert(SMEM_BYTES <= 232448 && STAGES >= 4 && (2 * STAGES + 4) * 8 + 8 <= 256, "smem");
+  static_assert(SMEM_BYTES <= 232448 / 2 && STAGES >= 3 && (2 * STAGES + 4) * 8 + 8 <= 256, "smem");
 };
 
 struct LinArgs {
@@ -474,7 +474,7 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   if (nt > 65535 || mt > 65535) return cudaErrorInvalidConfiguration;
   // K splits: a power of two, as many as the CTAs that fit at once leave room
   // for, at least four 64-value blocks each
-  const int64_t slots = static_cast<int64_t>(num_sms_current_device()) * (BN <= 64 ? 2 : 1);
+  const int64_t slots = 2LL * num_sms_current_device();
   int ks = 1;
   while (ks < kMaxSplits && nt * mt * ks * 2 <= slots && a.nkb >= ks * 8) ks *= 2;
   auto kern = ks == 1   ? linear_kernel<BN, F32, 1>
