@@ -485,8 +485,11 @@ typedef struct mok_linear_desc {
   int32_t act;           /* mok_act */
   int32_t y_elem;        /* forward: mok_elem of y, z, residual; backward: of dy, z */
   int32_t dx_elem;       /* backward: mok_elem of dx */
-  int32_t accumulate;    /* backward: add into dx (fp32 only), dw and dbias */
+  int32_t accumulate;    /* backward: MOK_ADD_* */
 } mok_linear_desc;
+
+#define MOK_ADD_DX 0x1 /* add into dx (fp32 only) */
+#define MOK_ADD_DW 0x2 /* add into dw and dbias */
 
 /* z = x w^T + bias,  y = act(z) + residual, accumulated in fp32 on the tensor
  * cores and rounded once to y_elem.  x bf16 [M,K] (stride ld_x), w bf16 [N,K],

@@ -184,6 +184,7 @@ def gemm_nvfp4(A, sa, ga, B, sb, gb, C, workspace, stream=None):
 # what the library refuses MokError.
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+_ACCUMULATE = {False: 0, True: 3, "dx": 1, "dw": 2}
 _status_words = {}
 _block = None
 
@@ -276,9 +277,13 @@ def linear_backward(dy, x, w, z=None, *, act="none", bias=False, dx_dtype=None, 
     """Gradients of `linear` (see mok_linear_backward): (dx, dw, dbias), dbias
     None unless `bias` is true or a tensor for it is given.  dy [M, N] bf16 or
     fp32, z of its type; dx bf16 (the default) or fp32; dw, dbias fp32.
-    `accumulate` adds into the given dx (fp32), dw and dbias."""
-    return _ops().linear_backward(dy, x, w, z, _act(act), bias, dx_dtype, dx, dw, dbias,
-                                  accumulate, workspace, stream)
+    `accumulate` adds into the given dx (fp32), dw and dbias; "dx" into dx alone,
+    "dw" into dw and dbias."""
+    add = _ACCUMULATE.get(accumulate)
+    if add is None:
+        raise ValueError(f"accumulate must be one of {tuple(_ACCUMULATE)}, not {accumulate!r}")
+    return _ops().linear_backward(dy, x, w, z, _act(act), bias, dx_dtype, dx, dw, dbias, add,
+                                  workspace, stream)
 
 
 def device_status(buf, stream=None) -> int:

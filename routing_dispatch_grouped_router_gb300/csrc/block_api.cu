@@ -53,6 +53,7 @@ mok_status linear_desc(const mok_linear_desc* desc, mok_linear_desc* D) {
     return MOK_ERR_UNSUPPORTED;
   if (D->act < MOK_ACT_NONE || D->act > MOK_ACT_GELU) return MOK_ERR_UNSUPPORTED;
   if (!elem_ok(D->y_elem) || !elem_ok(D->dx_elem)) return MOK_ERR_UNSUPPORTED;
+  if (D->accumulate & ~(MOK_ADD_DX | MOK_ADD_DW)) return MOK_ERR_UNSUPPORTED;
   if (!stride(&D->ld_x, D->K)) return MOK_ERR_INVALID_ARG;
   if (D->ld_x % 8) return MOK_ERR_UNSUPPORTED;
   return MOK_OK;
@@ -212,7 +213,8 @@ mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, cons
   mok_linear_desc D;
   mok_status st = linear_desc(desc, &D);
   if (st != MOK_OK) return st;
-  if (D.accumulate && dx && D.dx_elem != MOK_ELEM_F32) return MOK_ERR_UNSUPPORTED;
+  if ((D.accumulate & MOK_ADD_DX) && dx && D.dx_elem != MOK_ELEM_F32)
+    return MOK_ERR_UNSUPPORTED;
   if (D.M > 0 && (!dy || (dw && !x) || (dx && !w) || !workspace)) return MOK_ERR_INVALID_ARG;
   if (D.M > 0 && D.act != MOK_ACT_NONE && !z) return MOK_ERR_INVALID_ARG;
   const size_t ye = elem_size(D.y_elem);

@@ -493,7 +493,7 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     const at::Tensor *dx0 = tensor_or_null(a[7], "dx"), *dw0 = tensor_or_null(a[8], "dw"),
                      *db0 = tensor_or_null(a[9], "dbias");
     const bool bias = PyObject_IsTrue(a[5]) == 1 || db0 != nullptr;
-    const bool acc = PyObject_IsTrue(a[10]) == 1;
+    const int64_t acc = integer(a[10]);
     const Call c(x, a[12]);
     mok_linear_desc D = linear_desc(c, x, w, act);
     dense(dy, "dy", c.device, {D.M, D.N});
@@ -503,8 +503,9 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
       dense(*z, "z", c.device, {D.M, D.N});
       type_is(*z, "z", dy.scalar_type());
     }
-    TORCH_CHECK_VALUE(!acc || (dx0 && dw0 && (!bias || db0)),
-                      "accumulate needs dx, dw and dbias to add into");
+    TORCH_CHECK_VALUE(!(acc & MOK_ADD_DX) || dx0, "accumulate needs dx to add into");
+    TORCH_CHECK_VALUE(!(acc & MOK_ADD_DW) || (dw0 && (!bias || db0)),
+                      "accumulate needs dw and dbias to add into");
     const at::ScalarType dt =
         dtype_or(a[6], dx0 ? dx0->scalar_type() : at::kBFloat16, "dx_dtype");
     TORCH_CHECK_VALUE(real(dt), "dx must not be ", dt);
@@ -521,7 +522,7 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     }
     D.y_elem = elem(dy.scalar_type());
     D.dx_elem = elem(dt);
-    D.accumulate = acc;
+    D.accumulate = static_cast<int32_t>(acc);
     size_t n = 0;
     check(mok_linear_workspace_size(&D, 1, &n), "mok_linear_workspace_size");
     const Scratch ws(c, tensor_or_null(a[11], "workspace"), n);

@@ -831,6 +831,7 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
   linear_layout(D, &W);
   char* b = static_cast<char*>(ws);
   const bool f32 = D.y_elem == MOK_ELEM_F32;
+  const bool add_dx = (D.accumulate & MOK_ADD_DX) != 0, add_dw = (D.accumulate & MOK_ADD_DW) != 0;
   const bool vec = D.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(z)) & 15) == 0;
   // a bf16 dy without an activation is dz already
   const bool direct = !f32 && D.act == MOK_ACT_NONE && vec;
@@ -875,11 +876,11 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     if (e != cudaSuccess) return e;
   }
   if (dbias) {
-    const cudaError_t e = launch_column_sum(part_bias, W.bias_rows, D.N, dbias, D.accumulate != 0, st);
+    const cudaError_t e = launch_column_sum(part_bias, W.bias_rows, D.N, dbias, add_dw, st);
     if (e != cudaSuccess) return e;
   }
   if (D.M == 0) {
-    if (dw && !D.accumulate) return cudaMemsetAsync(dw, 0, static_cast<size_t>(D.N) * D.K * 4, st);
+    if (dw && !add_dw) return cudaMemsetAsync(dw, 0, static_cast<size_t>(D.N) * D.K * 4, st);
     return cudaSuccess;
   }
   BfParts dz;
@@ -894,12 +895,12 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     float* part = reinterpret_cast<float*>(b + W.part_dw);
     if (sum && split && !dxf && parts == 2) d.n = 2;
     cudaError_t e = gemm_linear_dx(D.M, D.N, D.K, d, w, sum ? part : dx, sum || dxf,
-                                   !sum && D.accumulate != 0, W.dx_splits, status, st);
+                                   !sum && add_dx, W.dx_splits, status, st);
     if (e != cudaSuccess) return e;
     if (sum) {
       LinArgs f = {};
       f.y = dx;
-      f.res = D.accumulate ? dx : nullptr;  // (fp32)
+      f.res = add_dx ? dx : nullptr;  // (fp32)
       f.M = static_cast<int>(D.M);
       f.N = static_cast<int>(D.K);
       f.act = MOK_ACT_NONE;
@@ -912,7 +913,7 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     float* part = reinterpret_cast<float*>(b + W.part_dw);
     const bool sum = W.dw_splits > 1;
     cudaError_t e = gemm_linear_dw(D.M, D.N, D.K, dz, x, D.ld_x, sum ? part : dw,
-                                   !sum && D.accumulate != 0, W.dw_splits, status, st);
+                                   !sum && add_dw, W.dw_splits, status, st);
     if (e != cudaSuccess || !sum) return e;
     const long long n4 = D.N * D.K / 4;
     const long long stride4 = (D.N + 127) / 128 * 128 * D.K / 4;
@@ -922,7 +923,7 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     ProfScope prof("linear_dw_sum", st);
     e = launch_dependent(split_sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
                          reinterpret_cast<const float4*>(part), W.dw_splits, stride4, n4,
-                         reinterpret_cast<float4*>(dw), D.accumulate ? 1 : 0);
+                         reinterpret_cast<float4*>(dw), add_dw ? 1 : 0);
     count_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
   }
