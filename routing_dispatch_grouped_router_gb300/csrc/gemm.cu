@@ -2656,8 +2656,11 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
   if (pair)
     return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true>(
         name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
-  return launch<BN1, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT>(
-      name, ta, tb, tc, a, a.m_tiles * a.n_tiles * splits, st, tl, om);
+  // (the forward has its own kernels for one row tile)
+  if constexpr (A_MN || B_MN)
+    return launch<BN1, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT>(
+        name, ta, tb, tc, a, a.m_tiles * a.n_tiles * splits, st, tl, om);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t gemm_linear_fwd(int64_t M, int64_t N, int64_t K, int64_t ld_x, const void* x,

@@ -110,6 +110,18 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(sum / d + eps), to within an ulp: the hardware's approximation and one
+// Newton step with the residual 1 - v r^2 in twice the precision.  An error of
+// rstd shifts a whole row, and with it which E4M3 code its values round to.
+__device__ __forceinline__ float row_rstd(float sum, float d, float eps) {
+  const float v = __fdiv_rn(sum, d) + eps;
+  const float r = rsqrtf(v);
+  const float h = v * r, l = fmaf(v, r, -h);
+  const float e = fmaf(-h, r, 1.0f) - l * r;
+  // (v = 0 or infinite: r is infinite or 0 and e not a number)
+  return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Row `r` of an array with row stride ld, F32 or bf16 elements.
 template <bool F32>
 __device__ __forceinline__ const void* row_at(const void* base, long long r, long long ld) {
@@ -128,7 +140,7 @@ struct NormFwd {
   uint8_t *codes, *scales;
   long long rows, ld_x, ld_r, ld_s, ld_y;
   int d, nvec, w_f32;
-  float inv_d, eps;
+  float eps;
 };
 
 // MXFP8 of the vector's elements: the block's 32 columns are 4 threads'
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormF
     sum = (t & 31) < (tpr >> 5) ? red[t & 31] : 0.f;
     sum = warp_sum(sum);
   }
-  const float rstd = rsqrtf(fmaf(sum, a.inv_d, a.eps));
+  const float rstd = row_rstd(sum, static_cast<float>(a.d), a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int vi = t + i * tpr;
@@ -313,7 +325,6 @@ cudaError_t launch_add_rmsnorm(const mok_rmsnorm_desc& D, const void* x, const v
   a.d = static_cast<int>(D.d);
   a.nvec = (a.d + 7) / 8;
   a.w_f32 = D.weight_elem == MOK_ELEM_F32;
-  a.inv_d = 1.0f / static_cast<float>(a.d);
   a.eps = D.eps;
   const int xe = xf ? 4 : 2, se = sf ? 4 : 2;
   const bool vec = a.d % 8 == 0 && vec_rows(x, a.ld_x, xe) && vec_rows(res, a.ld_r, se) &&
@@ -409,7 +420,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(NormBwd a) {
       ss = warp_sum(in ? red[par][0][t & 31] : 0.f);
       gs = warp_sum(in ? red[par][1][t & 31] : 0.f);
     }
-    const float rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+    const float rstd = row_rstd(ss, static_cast<float>(a.d), a.eps);
     const float c = gs * rstd * rstd * a.inv_d;  // rstd mean(g n) = c; n c = s rstd c
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -539,7 +550,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
     const bool in = (t & 31) < nw;
     ss = warp_sum(in ? red[par][0][t & 31] : 0.f);
     gs = warp_sum(in ? red[par][1][t & 31] : 0.f);
-    const float rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+    const float rstd = row_rstd(ss, static_cast<float>(a.d), a.eps);
     const float c = gs * rstd * rstd * a.inv_d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
