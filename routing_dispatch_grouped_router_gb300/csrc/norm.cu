@@ -21,16 +21,73 @@ namespace {
 // Eight elements of a row held by one thread.  The rows' vectors v = 0 ..
 // ceil(d/8)-1 go round the threads of the row.  VEC: vector v is elements
 // 8v .. 8v+7 (one or two 16-byte accesses; 16-byte aligned rows, d a multiple
-// of 8).  Otherwise element j of vector v is 256 (v / 32) + 32 j + v % 32, so
-// that a warp's element accesses are consecutive whatever the alignment.
+// of 8).  Otherwise a warp's 32 vectors are 256 elements, of which lane l holds
+// pairs 64 j + 2l, + 1 (j = 0..3): a warp's accesses are then whole words that
+// follow one another, whatever the row's alignment.  bf16 rows that start in
+// the middle of a word are read and written in words too, each lane passing
+// one of its two elements to its neighbour (4099 x 2881 bf16 element by element:
+// 2.8 times the aligned form's time forward, 5 times backward).
 template <bool VEC>
 __device__ __forceinline__ int elem_of(int v, int j) {
-  return VEC ? 8 * v + j : 256 * (v >> 5) + 32 * j + (v & 31);
+  return VEC ? 8 * v + j : 256 * (v >> 5) + 64 * (j >> 1) + 2 * (v & 31) + (j & 1);
 }
 
-// A vector as it lies in memory (aligned bf16 stays packed), so that all of a
-// row's loads can be in flight before the first is used.  Plain loads: the
-// outputs may be the same memory as inputs.
+__device__ __forceinline__ uint32_t load_u16(const __nv_bfloat16* p) {
+  return *reinterpret_cast<const unsigned short*>(p);
+}
+__device__ __forceinline__ void store_u16(__nv_bfloat16* p, uint32_t v) {
+  *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(v);
+}
+__device__ __forceinline__ bool mid_word(const __nv_bfloat16* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 2) != 0;
+}
+
+// The pairs of vector v of a bf16 row (w[j]: elements i, i + 1 with i = 2 lane +
+// 64 j + the warp's first).  In a row that starts mid-word, a word holds the
+// second element of one pair and the first of the next: each lane gets the other
+// half of its word from its neighbour (lane 0 and lane 31 from the pairs before
+// and after), and only the warp's two ends are halfwords.  The halves are joined
+// by a funnel shift whose amount is 0 for aligned rows.  Whole warps call these.
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, int v, int d,
+                                            const uint32_t (&w)[4]) {
+  const int lane = threadIdx.x & 31, i0 = 256 * (v >> 5) + 2 * lane;
+  const bool mid = mid_word(p);
+  const int back = mid ? 1 : 0;
+  uint32_t u[4];  // the word before and at pair j
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t give = lane == 31 && j > 0 ? w[j - 1] : w[j];
+    u[j] = __funnelshift_l(__shfl_sync(0xffffffffu, give, (lane + 31) & 31), w[j], 16 * back);
+  }
+  if (i0 - 2 * lane + 256 <= d) {  // all of the warp's pairs lie in the row
+    if (mid && lane == 0) store_u16(p + i0, w[0]);
+    else *reinterpret_cast<uint32_t*>(p + i0 - back) = u[0];
+#pragma unroll
+    for (int j = 1; j < 4; ++j) *reinterpret_cast<uint32_t*>(p + i0 + 64 * j - back) = u[j];
+    if (mid && lane == 31) store_u16(p + i0 + 193, w[3] >> 16);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = i0 + 64 * j;
+    if (!mid) {
+      if (i + 1 < d) *reinterpret_cast<uint32_t*>(p + i) = w[j];
+      else if (i < d) store_u16(p + i, w[j]);
+    } else {
+      if (lane == 0 && j == 0) {
+        if (i < d) store_u16(p + i, w[j]);
+      } else if (i < d) {
+        *reinterpret_cast<uint32_t*>(p + i - 1) = u[j];
+      } else if (i == d) {
+        store_u16(p + i - 1, u[j]);
+      }
+    }
+  }
+}
+
+// A vector as it lies in memory (bf16 stays packed), so that all of a row's
+// loads can be in flight before the first is used.  Plain loads: the outputs
+// may be the same memory as inputs.  Without VEC whole warps call load and store.
 template <bool F32, bool VEC>
 struct Raw8 {
   float f[8];
@@ -41,13 +98,11 @@ struct Raw8 {
       f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
       f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     } else {
+      const float* p = static_cast<const float*>(row);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int i = elem_of<false>(v, j);
-        f[j] = 0.f;
-        if (i < d)
-          f[j] = F32 ? static_cast<const float*>(row)[i]
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i]);
+        f[j] = i < d ? p[i] : 0.f;
       }
     }
   }
@@ -72,6 +127,57 @@ struct Raw8<false, true> {
     o[4] = bf16lo(u.z); o[5] = bf16hi(u.z); o[6] = bf16lo(u.w); o[7] = bf16hi(u.w);
   }
 };
+// The words of store_pairs' layout as they lie in memory, and the warp's last
+// element; the lanes exchange halves in get, so that no load waits for a shuffle.
+template <>
+struct Raw8<false, false> {
+  uint32_t a[4], end;
+  int shift;  // 16: the row starts mid-word
+  __device__ __forceinline__ void load(const void* row, int v, int d) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(row);
+    const int lane = threadIdx.x & 31, first = 256 * (v >> 5), i0 = first + 2 * lane;
+    const bool mid = mid_word(p);
+    const int back = mid ? 1 : 0;
+    shift = 16 * back;
+    end = 0u;
+    if (first + 256 <= d) {  // all of the warp's pairs lie in the row
+      a[0] = mid && i0 == 0 ? load_u16(p) << 16 : *reinterpret_cast<const uint32_t*>(p + i0 - back);
+#pragma unroll
+      for (int j = 1; j < 4; ++j)
+        a[j] = *reinterpret_cast<const uint32_t*>(p + i0 + 64 * j - back);
+      if (mid && lane == 31) end = load_u16(p + i0 + 193);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 64 * j;
+      a[j] = 0u;
+      if (!mid) {
+        if (i + 1 < d) a[j] = *reinterpret_cast<const uint32_t*>(p + i);
+        else if (i < d) a[j] = load_u16(p + i);
+      } else {
+        if (i < d) a[j] = i > 0 ? *reinterpret_cast<const uint32_t*>(p + i - 1) : load_u16(p) << 16;
+        else if (i == d) a[j] = load_u16(p + i - 1);
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+    a[0] = a[1] = a[2] = a[3] = end = 0u;
+    shift = 0;
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t give = lane == 0 && j < 3 ? a[j < 3 ? j + 1 : 3] : a[j];
+      uint32_t n = __shfl_sync(0xffffffffu, give, (lane + 1) & 31);
+      if (j == 3 && lane == 31) n = end;
+      const uint32_t w = __funnelshift_r(a[j], n, shift);
+      o[2 * j] = bf16lo(w);
+      o[2 * j + 1] = bf16hi(w);
+    }
+  }
+};
 
 template <bool F32, bool VEC>
 __device__ __forceinline__ void load8(const void* row, int v, int d, float (&o)[8]) {
@@ -82,24 +188,27 @@ __device__ __forceinline__ void load8(const void* row, int v, int d, float (&o)[
 
 template <bool F32, bool VEC>
 __device__ __forceinline__ void store8(void* row, int v, int d, const float (&o)[8]) {
-  if (VEC) {
-    if (F32) {
+  if (F32) {
+    if (VEC) {
       float4* p = reinterpret_cast<float4*>(row) + 2 * v;
       p[0] = make_float4(o[0], o[1], o[2], o[3]);
       p[1] = make_float4(o[4], o[5], o[6], o[7]);
     } else {
-      reinterpret_cast<uint4*>(row)[v] =
-          make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                     pack_bf16x2(o[6], o[7]));
+      float* p = static_cast<float*>(row);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = elem_of<false>(v, j);
+        if (i < d) p[i] = o[j];
+      }
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = elem_of<false>(v, j);
-      if (i < d) {
-        if (F32) static_cast<float*>(row)[i] = o[j];
-        else static_cast<__nv_bfloat16*>(row)[i] = __float2bfloat16_rn(o[j]);
-      }
+    const uint4 u = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                               pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+    if (VEC) {
+      reinterpret_cast<uint4*>(row)[v] = u;
+    } else {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      store_pairs(static_cast<__nv_bfloat16*>(row), v, d, w);
     }
   }
 }
@@ -120,6 +229,53 @@ __device__ __forceinline__ float row_rstd(float sum, float d, float eps) {
   const float e = fmaf(-h, r, 1.0f) - l * r;
   // (v = 0 or infinite: r is infinite or 0 and e not a number)
   return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
+}
+
+// An unevaluated sum hi + lo of two fp32 values, lo far below hi.
+struct Pair {
+  float hi, lo;
+};
+// (the _rn forms: these must not be contracted into fused products)
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  Pair s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return s;  // (an infinite sum has a low part that is no number: row_rstd drops it)
+}
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = pair_add(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
+// row_rstd as a pair, from the sum of squares as one.
+__device__ __forceinline__ Pair row_rstd(Pair sum, float d, float eps) {
+  const float q = __fdiv_rn(sum.hi, d);
+  Pair v = two_sum(q, eps);
+  v.lo += (fmaf(-q, d, sum.hi) + sum.lo) / d;
+  const float r = rsqrtf(v.hi);
+  const float h = v.hi * r, l = fmaf(v.hi, r, -h) + v.lo * r;
+  const float e = fmaf(-h, r, 1.0f) - l * r;
+  if (!(fabsf(e) < 1.0f)) return {r, 0.f};  // the mean square is 0, infinite or NaN
+  return {r, 0.5f * r * e};
+}
+
+// s rstd w, rounded to odd: cut off, with the last bit set where anything was
+// cut.  A further rounding to fewer bits then gives what rounding the exact
+// value would.
+__device__ __forceinline__ float norm_to_odd(float s, Pair rstd, float w) {
+  const float q = __fmul_rn(s, rstd.hi);
+  const float ql = fmaf(s, rstd.lo, fmaf(s, rstd.hi, -q));
+  const float m = __fmul_rn(q, w);
+  const float ml = fmaf(ql, w, fmaf(q, w, -m));
+  const float n = __fadd_rz(m, ml);
+  const float rest = __fsub_rn(ml, __fsub_rn(n, m));
+  // (not where n is infinite: the rest is no number then)
+  return fabsf(rest) > 0.f ? __uint_as_float(__float_as_uint(n) | 1u) : n;
 }
 
 // Row `r` of an array with row stride ld, F32 or bf16 elements.
@@ -144,7 +300,7 @@ struct NormFwd {
 };
 
 // MXFP8 of the vector's elements: the block's 32 columns are 4 threads'
-// vectors (VEC) or one element of each lane of the warp.
+// vectors (VEC) or a pair of each of 16 lanes.
 template <bool VEC>
 __device__ __forceinline__ void mx_store(const NormFwd& a, long long r, int v, bool in,
                                          const float (&n)[8]) {
@@ -178,33 +334,41 @@ __device__ __forceinline__ void mx_store(const NormFwd& a, long long r, int v, b
       store8<false, true>(static_cast<__nv_bfloat16*>(a.values) + r * a.d, v, a.d, q);
     }
   } else {
+    // a block is a pair of each of 16 lanes
+    uint32_t vals[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float amax = fabsf(n[j]);
+    for (int j = 0; j < 8; j += 2) {
+      float amax = fmaxf(fabsf(n[j]), fabsf(n[j + 1]));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int i = elem_of<false>(v, j);
-      if (!in || i >= a.d) continue;
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int i = elem_of<false>(v, j);  // (d is a multiple of 32: i and i + 1 alike)
       const int shared = mx_shared_exp(amax);
-      const uint16_t p = cvt_e4m3x2(0.f, n[j] * exp2i(-shared));
-      if (a.codes) {
+      const float down = exp2i(-shared), up = exp2i(shared);
+      const uint16_t p = cvt_e4m3x2(n[j + 1] * down, n[j] * down);
+      if (a.codes && in && i < a.d) {
         a.codes[r * a.d + i] = static_cast<uint8_t>(p & 0xFFu);
-        if ((i & 31) == 0) a.scales[r * (a.d >> 5) + (i >> 5)] = static_cast<uint8_t>(shared + 127);
+        a.codes[r * a.d + i + 1] = static_cast<uint8_t>(p >> 8);
+        if ((i & 31) == 0)
+          a.scales[r * (a.d >> 5) + (i >> 5)] = static_cast<uint8_t>(shared + 127);
       }
-      if (a.values) {
-        float hi, lo;
-        e4m3x2_to_f32(p, &hi, &lo);
-        static_cast<__nv_bfloat16*>(a.values)[r * a.d + i] = __float2bfloat16_rn(lo * exp2i(shared));
-      }
+      float hi, lo;
+      e4m3x2_to_f32(p, &hi, &lo);
+      vals[j >> 1] = pack_bf16x2(lo * up, hi * up);
     }
+    if (a.values && in)  // (in: alike for the warp)
+      store_pairs(static_cast<__nv_bfloat16*>(a.values) + r * a.d, v, a.d, vals);
   }
 }
 
 // One row per threadIdx.y; blockDim.x threads of whole warps hold it, NV
-// vectors each.
+// vectors each.  MX: mean square and norm are formed in pairs of fp32 and the norm
+// rounded to odd, so that codes and values are the roundings of the exact norm;
+// a plain fp32 norm lands on the wrong side of an E4M3 boundary about once in a
+// million values, an eighth of the value each time (8192 x 7168: 96.5 us from
+// plain fp32, 102.8 us so).
 template <bool XF32, bool SF32, bool VEC, int NV, bool MX>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormFwd a) {
-  __shared__ float red[32];
+  __shared__ float red[3][32];
   grid_dep_launch();
   grid_dep_wait();
   const int t = threadIdx.x, tpr = blockDim.x;
@@ -223,7 +387,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormF
     }
   }
   float v[NV][8];
-  float sum = 0.f;
+  float sq[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int vi = t + i * tpr;
@@ -240,16 +404,32 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormF
     if (a.s && row_in && vi < a.nvec)
       store8<SF32, VEC>(row_at<SF32>(a.s, r, a.ld_s), vi, a.d, v[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+    for (int j = 0; j < 8; ++j) sq[j] = fmaf(v[i][j], v[i][j], sq[j]);
   }
-  sum = warp_sum(sum);
+  const float df = static_cast<float>(a.d);
+  float sum = warp_sum(((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7])));
+  Pair sum2 = {sq[0], 0.f};
+  if (MX) {
+#pragma unroll
+    for (int j = 1; j < 8; ++j) sum2 = pair_add(sum2, {sq[j], 0.f});
+    sum2 = warp_sum(sum2);
+  }
   if (tpr > 32) {  // one row per block
-    if ((t & 31) == 0) red[t >> 5] = sum;
+    if ((t & 31) == 0) {
+      red[0][t >> 5] = sum;
+      if (MX) {
+        red[1][t >> 5] = sum2.hi;
+        red[2][t >> 5] = sum2.lo;
+      }
+    }
     __syncthreads();
-    sum = (t & 31) < (tpr >> 5) ? red[t & 31] : 0.f;
-    sum = warp_sum(sum);
+    const bool in = (t & 31) < (tpr >> 5);
+    sum = warp_sum(in ? red[0][t & 31] : 0.f);
+    if (MX) sum2 = warp_sum(Pair{in ? red[1][t & 31] : 0.f, in ? red[2][t & 31] : 0.f});
   }
-  const float rstd = row_rstd(sum, static_cast<float>(a.d), a.eps);
+  const float rstd = row_rstd(sum, df, a.eps);
+  Pair rstd2 = {0.f, 0.f};
+  if (MX) rstd2 = row_rstd(sum2, df, a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int vi = t + i * tpr;
@@ -260,9 +440,16 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormF
       if (a.w_f32) load8<true, VEC>(a.w, vi, a.d, w);
       else load8<false, VEC>(a.w, vi, a.d, w);
     }
+    if (in && a.y) {
+      float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = in ? v[i][j] * rstd * w[j] : 0.f;
-    if (in && a.y) store8<false, VEC>(row_at<false>(a.y, r, a.ld_y), vi, a.d, v[i]);
+      for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rstd * w[j];
+      store8<false, VEC>(row_at<false>(a.y, r, a.ld_y), vi, a.d, y);
+    }
+    if (MX) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = in ? norm_to_odd(v[i][j], rstd2, w[j]) : 0.f;
+    }
     if (MX) mx_store<VEC>(a, r, vi, in, v[i]);
   }
 }
@@ -377,7 +564,7 @@ struct BwdRow {
 template <bool DYF32, bool SF32, bool VEC, int NV>
 __global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(NormBwd a) {
   __shared__ float red[2][2][16];  // [row parity][sum][warp]
-  __shared__ float s_dw[8][256];
+  __shared__ float s_dw[NV <= 2 ? 8 : 1][NV * 256];
   grid_dep_launch();
   grid_dep_wait();
   const int t = threadIdx.x, tpr = blockDim.x, nw = tpr >> 5;
@@ -442,15 +629,21 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(NormBwd a) {
   }
   if (!a.part) return;
   float* p = a.part + static_cast<long long>(blockIdx.x) * a.d;
-  if (blockDim.y > 1) {  // rows of one warp, NV = 1: the block's rows in order
+  if (blockDim.y > 1) {  // rows of one warp: the block's rows in order
+    if (NV <= 2) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s_dw[threadIdx.y][t * 8 + j] = dw[0][j];
-    __syncthreads();
-    const int i = threadIdx.y * 32 + t;  // vector i / 8, element i % 8
-    float v = 0.f;
-    for (int y = 0; y < 8; ++y) v += s_dw[y][i];
-    const int e = elem_of<VEC>(i >> 3, i & 7);
-    if ((i >> 3) < a.nvec && e < a.d) p[e] = v;
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_dw[threadIdx.y][(t + 32 * i) * 8 + j] = dw[i][j];
+      __syncthreads();
+      for (int i = threadIdx.y * 32 + t; i < NV * 256; i += 256) {  // vector i / 8
+        float v = 0.f;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) v += s_dw[y][i];
+        const int e = elem_of<VEC>(i >> 3, i & 7);
+        if ((i >> 3) < a.nvec && e < a.d) p[e] = v;
+      }
+    }
     return;
   }
 #pragma unroll
@@ -633,9 +826,9 @@ BwdShape bwd_shape(int64_t rows, int64_t d, bool vec, int64_t row_bytes) {
   BwdShape b;
   b.nv = nvec <= 32 ? 1 : (nvec <= 1024 ? 2 : 4);
   b.tpr = ((nvec + b.nv - 1) / b.nv + 31) / 32 * 32;
-  b.rpb = b.nv == 1 ? 8 : 1;
+  b.rpb = b.tpr == 32 ? 8 : 1;
   b.depth = 0;
-  int per_sm = 768 / (b.tpr * b.rpb);
+  int per_sm = (b.rpb > 1 ? 1536 : 768) / (b.tpr * b.rpb);
   if (vec && d >= kBulkMinD) {
     // a row's chain of barrier and reductions takes a block long enough for an
     // SM's share of the memory to move some 70 KB: enough blocks to cover it
