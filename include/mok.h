@@ -451,7 +451,8 @@ typedef struct mok_balance_desc {
  * -inf has no probability; a token without a finite logit has lse -inf and
  * adds to counts and N only.  A NaN or +inf logit is taken as -inf and, in a
  * token of the mask, sets MOK_ERR_DEVICE_NONFINITE; an index outside [0, E) is
- * skipped and sets MOK_ERR_DEVICE_INDEX.  Pointers aligned to their elements.
+ * skipped and sets MOK_ERR_DEVICE_INDEX.  Pointers aligned to their elements;
+ * workspace: see the size query (NULL where it says 0).
  * status: device int32 or NULL.  It is sticky: only ever set, by the first
  * error, and never cleared here; zero it once before its first use. */
 mok_status mok_router_balance_forward(const mok_balance_desc* desc, const float* logits,

@@ -97,9 +97,9 @@ __device__ __forceinline__ bool clean(float (&l)[N]) {
 }
 
 // Sums over the threads of a block: thread t holds float4 / int4 column
-// t % cols (a power of two) of slice t / cols, and z, n of its own.  On return
-// threads t < cols hold column t's sums, and every thread z's and n's.  A fixed
-// tree: lanes, then warps in order.
+// t % cols (a power of two, at most 128) of slice t / cols, and z, n of its own.
+// On return threads t < cols hold column t's sums, and threads t < 128 z's and
+// n's.  A fixed tree: lanes, then warps in order.
 template <int TH>
 __device__ __forceinline__ void block_columns(int cols, float4& p, int4& c, float& z, int& n,
                                               float4* s_f4, int4* s_i4, float* s_z, int* s_n) {
@@ -137,12 +137,9 @@ __device__ __forceinline__ void block_columns(int cols, float4& p, int4& c, floa
       c.x += k.x; c.y += k.y; c.z += k.z; c.w += k.w;
     }
   }
-  z = 0.f;
-  n = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    z += s_z[i];
-    n += s_n[i];
+  if (t < 128) {  // the threads that columns go to
+    z = group_sum<32>(lane < W ? s_z[lane] : 0.f);
+    n = __reduce_add_sync(0xffffffffu, lane < W ? s_n[lane] : 0);
   }
 }
 
@@ -448,7 +445,8 @@ int64_t balance_blocks(const mok_balance_desc& D) {
 }
 
 void balance_layout(const mok_balance_desc& D, BalanceWs* W) {
-  const size_t G = static_cast<size_t>(balance_blocks(D));
+  // (one block leaves no partials)
+  const size_t G = balance_blocks(D) > 1 ? static_cast<size_t>(balance_blocks(D)) : 0;
   auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const size_t e_pad = (static_cast<size_t>(D.E) + 3) / 4 * 4;
   W->part_prob = 0;

@@ -138,7 +138,7 @@ mok_status mok_router_balance_forward(const mok_balance_desc* desc, const float*
   mok_balance_desc D;
   mok_status st = balance_desc(desc, &D);
   if (st != MOK_OK) return st;
-  if (!loss || !counts || !prob || !n_valid || !workspace) return MOK_ERR_INVALID_ARG;
+  if (!loss || !counts || !prob || !n_valid) return MOK_ERR_INVALID_ARG;
   if (D.T > 0 && (!logits || !topk_idx || !lse)) return MOK_ERR_INVALID_ARG;
   if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
       !aligned(prob, 4) || !aligned(lse, 4) || !aligned(n_valid, 4) || !aligned(status, 4) ||
@@ -146,6 +146,7 @@ mok_status mok_router_balance_forward(const mok_balance_desc* desc, const float*
     return MOK_ERR_INVALID_ARG;
   BalanceWs W;
   balance_layout(D, &W);
+  if (W.total > 0 && !workspace) return MOK_ERR_INVALID_ARG;
   if (ws_bytes < W.total) return MOK_ERR_WORKSPACE;
   st = mok_check_device();
   if (st != MOK_OK) return st;

@@ -90,8 +90,10 @@ def test_balance_pointers_refused(lib):
     assert lib.mok_router_balance_workspace_size(balance(), n) == 0
     f = lib.mok_router_balance_forward
     assert f(balance(), None, A, None, A, A, A, A, A, A, 1 << 20, None, None) == 1
-    assert f(balance(), A, A, None, A, A, A, A, A, None, 1 << 20, None, None) == 1
-    assert f(balance(), A, A, None, A, A, A, A, A, A, n.value - 1, None, None) == 3
+    many = balance(T=1 << 16)
+    assert lib.mok_router_balance_workspace_size(many, n) == 0 and n.value > 0
+    assert f(many, A, A, None, A, A, A, A, A, None, 1 << 20, None, None) == 1
+    assert f(many, A, A, None, A, A, A, A, A, A, n.value - 1, None, None) == 3
     assert f(balance(), P(4098), A, None, A, A, A, A, A, A, 1 << 20, None, None) == 1
     b = lib.mok_router_balance_backward
     assert b(balance(), None, A, A, A, A, None, A, None) == 1
