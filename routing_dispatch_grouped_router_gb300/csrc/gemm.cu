@@ -731,60 +731,181 @@ __device__ __forceinline__ void linear_tile_wide(const GemmArgs& a, const Tile& 
   }
 }
 
+// Loads that no branch holds back (0 without the predicate), and elements.
+__device__ __forceinline__ uint4 load_if(const uint4* p, bool on) {
+  uint4 v;
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %5, 0;\n"
+      "mov.u32 %0, 0; mov.u32 %1, 0; mov.u32 %2, 0; mov.u32 %3, 0;\n"
+      "@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4]; }"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(static_cast<uint32_t>(on)));
+  return v;
+}
+__device__ __forceinline__ float load_if(const float* p, bool on) {
+  uint32_t v;
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %2, 0;\n mov.u32 %0, 0;\n @q ld.global.u32 %0, [%1]; }"
+      : "=&r"(v)
+      : "l"(p), "r"(static_cast<uint32_t>(on)));
+  return __uint_as_float(v);
+}
+__device__ __forceinline__ float load_if(const __nv_bfloat16* p, bool on) {
+  uint16_t v;
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %2, 0;\n mov.u16 %0, 0;\n @q ld.global.u16 %0, [%1]; }"
+      : "=&h"(v)
+      : "l"(p), "r"(static_cast<uint32_t>(on)));
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+__device__ __forceinline__ void store_as(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+// v + the elements of word u, rounded, as a word
+__device__ __forceinline__ uint4 add_word(const float (&v)[4], const uint4& u, float) {
+  return make_uint4(__float_as_uint(v[0] + __uint_as_float(u.x)),
+                    __float_as_uint(v[1] + __uint_as_float(u.y)),
+                    __float_as_uint(v[2] + __uint_as_float(u.z)),
+                    __float_as_uint(v[3] + __uint_as_float(u.w)));
+}
+__device__ __forceinline__ uint4 add_word(const float (&v)[8], const uint4& u, __nv_bfloat16) {
+  return make_uint4(pack_bf16x2(v[0] + bf16lo(u.x), v[1] + bf16hi(u.x)),
+                    pack_bf16x2(v[2] + bf16lo(u.y), v[3] + bf16hi(u.y)),
+                    pack_bf16x2(v[4] + bf16lo(u.z), v[5] + bf16hi(u.z)),
+                    pack_bf16x2(v[6] + bf16lo(u.w), v[7] + bf16hi(u.w)));
+}
+
+// C's rows where the TMA cannot take them (any row length, elements aligned to
+// themselves only): a warp's 32 rows, 32 columns at a time from the left, lane r
+// holding row r's values.  Through the staging buffer, so that the lanes of a row
+// write its aligned 16-byte words; the columns past the last whole word wait in
+// registers (`carry`) for the next 32, so that only the first and the last
+// elements of the warp's columns go one by one.
+// (14692 x 4914 x 88 bf16, relu, residual and z: 250 us; 548 with a column per
+// lane, 2 bytes each; floor 64.  8192 x 4913 x 1024, silu and residual: 148 us; 303;
+// 88 with 4912 columns through the TMA.  The next columns' residuals loaded ahead
+// took 140 us there, but 311 instead of 252 us in fp32: registers.)
+template <typename T>
+struct DirectRows {
+  static constexpr int V = 16 / sizeof(T);  // elements of a word
+  static constexpr int L = 32 / V;          // lanes of a row
+  static constexpr int R = 32 / L;          // rows at a time
+  static constexpr int kBatch = 4;          // of them whose residuals are in flight
+  static constexpr int kStride = 32 + V - 1;  // (odd: no bank conflicts)
+  float carry[V - 1];
+
+  // one by one: the columns col(row, e), e < V, of the 32 rows (-V: none)
+  template <typename F>
+  static __device__ __forceinline__ void edge(const float* stage, int lane, T* dst, const T* res,
+                                              long long ld, const F& col) {
+    float r[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int row = (lane + 32 * k) / V, c = col(row, (lane + 32 * k) % V);
+      r[k] = load_if(res + row * ld + c, res && c > -V);
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int row = (lane + 32 * k) / V, c = col(row, (lane + 32 * k) % V);
+      if (c > -V) store_as(dst + row * ld + c, stage[row * kStride + V - 1 + c] + r[k]);
+    }
+  }
+
+  // dst[r ld + c] = v + res[r ld + c], rows r < rows, columns c < w <= 32; first,
+  // last: of the warp's columns
+  __device__ __forceinline__ void put(uint8_t* buf, const float (&v)[32], int lane, T* dst,
+                                      const T* res, long long ld, int rows, int w, bool first,
+                                      bool last) {
+    const int j = lane & (L - 1), rr = lane / L;
+    // left(r): columns of row r's word 0 that lie left of column 0
+    const uint32_t a0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst) / sizeof(T));
+    const uint32_t step = static_cast<uint32_t>(ld);
+    const auto left = [&](int r) { return static_cast<int>((a0 + r * step) & (V - 1)); };
+    const bool words_of_res =
+        res && ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(res)) & 15) == 0;
+    float* stage = reinterpret_cast<float*>(buf);
+    __syncwarp();  // the last block has been read
+#pragma unroll
+    for (int c = 0; c < V - 1; ++c) {
+      if (!first) stage[lane * kStride + c] = carry[c];
+      carry[c] = v[32 - (V - 1) + c];
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c) stage[lane * kStride + V - 1 + c] = v[c];
+    __syncwarp();
+#pragma unroll
+    for (int b = 0; b < L / kBatch; ++b) {
+      uint4 rw[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = (b * kBatch + i) * R + rr, c = j * V - left(r);
+        const bool in = r < rows && (c >= 0 || !first) && c + V <= w;
+        rw[i] = load_if(reinterpret_cast<const uint4*>(res + r * ld + c), in && words_of_res);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = (b * kBatch + i) * R + rr, c = j * V - left(r);
+        const bool in = r < rows && (c >= 0 || !first) && c + V <= w;
+        const float* p = stage + r * kStride + V - 1 + c;
+        float t[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) t[e] = p[e];
+        if (res && !words_of_res) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) t[e] += load_if(res + r * ld + c + e, in);
+        }
+        const uint4 u = add_word(t, rw[i], T());
+        if (in) *reinterpret_cast<uint4*>(dst + r * ld + c) = u;
+      }
+    }
+    if (first)  // what word 0 has of these columns, where it is not whole
+      edge(stage, lane, dst, res, ld, [&](int r, int e) {
+        const int a = left(r), c = e - a;
+        return r < rows && a > 0 && c >= 0 && w + a >= V ? c : -V;
+      });
+    if (last)  // what lies past the last whole word
+      edge(stage, lane, dst, res, ld, [&](int r, int e) {
+        const int a = left(r), c = (w + a) / V * V - a + e;
+        return r < rows && c < w && (c >= 0 || !first) ? c : -V;
+      });
+  }
+};
+
+template <int EPI>
+struct DirectState {
+  using T = std::conditional_t<linear_f32(EPI), float, __nv_bfloat16>;
+  DirectRows<T> y, z;
+};
+
 // The dense product's epilogue of one 32-column chunk: v = C's values of this
 // lane's row, columns x ..; tl's split writes its partial at rows e * m_rows.
 template <int EPI>
 __device__ __forceinline__ void linear_chunk(const GemmArgs& a, const Tile& tl, int q, int lane,
                                              int x, float (&v)[32], uint8_t* stage_buf,
                                              uint32_t& nst, const CUtensorMap* tmC,
-                                             const CUtensorMap* tmH) {
+                                             const CUtensorMap* tmH, DirectState<EPI>& direct,
+                                             bool first, bool last) {
   const int y = tl.e * a.m_rows + tl.row0 + q * 32;
   const long long row = tl.row0 + q * 32 + lane;
   if constexpr (linear_direct(EPI)) {
-    // C's values through the staging buffer (fp32, the swizzled layout), so that
-    // lane i then holds column x + i of each row in turn
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<float4*>(stage_buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-          make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    __syncwarp();
-    const int col = x + lane;
-    if (col >= a.n_valid) return;
-    const float bias = a.bias ? a.bias[col] : 0.f;
+    using T = typename DirectState<EPI>::T;
     const int rows = a.m_valid - (tl.row0 + q * 32) < 32 ? a.m_valid - (tl.row0 + q * 32) : 32;
-    const long long o0 = static_cast<long long>(y) * a.n_valid + col;
-    // eight rows at a time, their residuals loaded before the stores, which
-    // would hold later loads back
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      float res[8];
+    const int w = a.n_valid - x < 32 ? a.n_valid - x : 32;
+    const long long o = static_cast<long long>(y) * a.n_valid + x;
+    if (a.bias) {
+      const float b = load_if(a.bias + x + lane, lane < w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const long long o = o0 + static_cast<long long>(r0 + i) * a.n_valid;
-        res[i] = 0.f;
-        if (a.res && r0 + i < rows)
-          res[i] = linear_f32(EPI) ? static_cast<const float*>(a.res)[o]
-                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[o]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i;
-        if (r >= rows) break;
-        const long long o = o0 + static_cast<long long>(r) * a.n_valid;
-        const float z = bias + *reinterpret_cast<const float*>(
-                                   stage_buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
-                                   (lane & 3) * 4);
-        const float t = act_value(z, a.act) + res[i];
-        if (linear_f32(EPI)) {
-          if (a.z) static_cast<float*>(a.z)[o] = z;
-          static_cast<float*>(a.out)[o] = t;
-        } else {
-          if (a.z) static_cast<__nv_bfloat16*>(a.z)[o] = __float2bfloat16_rn(z);
-          static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(t);
-        }
-      }
+      for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, b, j);
     }
+    if (a.z)
+      direct.z.put(stage_buf, v, lane, static_cast<T*>(a.z) + o, nullptr, a.n_valid, rows, w,
+                   first, last);
+    if (a.act != MOK_ACT_NONE) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], a.act);
+    }
+    direct.y.put(stage_buf, v, lane, static_cast<T*>(a.out) + o,
+                 a.res ? static_cast<const T*>(a.res) + o : nullptr, a.n_valid, rows, w, first,
+                 last);
     return;
   }
   if (a.bias) {
@@ -844,12 +965,14 @@ __device__ __forceinline__ void linear_tile(const GemmArgs& a, const Tile& tl, u
                                             const CUtensorMap* tmH) {
   if (tl.row0 + q * 32 >= a.m_valid) return;  // (a partial block is clipped by the TMA)
   const int col0 = tl.n_tile * BN + half * (BN / 2);
+  DirectState<EPI> direct;
 #pragma unroll 1
   for (int c = 0; c < BN / 2; c += 32) {
     if (col0 + c >= a.n_valid) break;
     float v[32];
     tmem_ld32(taddr + half * (BN / 2) + c, v);
-    linear_chunk<EPI>(a, tl, q, lane, col0 + c, v, stage_buf, nst, tmC, tmH);
+    linear_chunk<EPI>(a, tl, q, lane, col0 + c, v, stage_buf, nst, tmC, tmH, direct, c == 0,
+                      c + 32 == BN / 2 || col0 + c + 32 >= a.n_valid);
   }
 }
 
@@ -908,8 +1031,10 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& a, const Tile& tl,
       }
     }
   } else if constexpr (linear_epi(EPI)) {
-    if constexpr (DBUF) linear_tile_wide<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, tmC);
-    else linear_tile<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, nst, tmC, tmH);
+    if constexpr (DBUF && !linear_direct(EPI))
+      linear_tile_wide<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, tmC);
+    else
+      linear_tile<BN, EPI>(a, tl, taddr, q, lane, half, stage_buf, nst, tmC, tmH);
   } else if (EPI == EPI_F32_T || EPI == EPI_BF16_T) {
     // C^T through TMA: accumulator rows are output columns; C viewed as
     // [E * N, M] with group e's block at rows e*N
@@ -1313,7 +1438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ GemmArgs args, const __grid_constant__ OutMaps om) {
   using C = Cfg<BN, SPLIT, PAIR, staging_bytes<EPI, SPLIT, SCHED, DB>()>;
   constexpr bool kDbuf = DB;
-  constexpr bool kChunks = linear_f32(EPI) && !DB;
+  constexpr bool kChunks = linear_f32(EPI) && (!DB || linear_direct(EPI));
   static_assert(!DB || ((EPI == EPI_F32 || EPI == EPI_F32_T) && SCHED == SCHED_KGROUP) ||
                     (EPI == EPI_SWIGLU_BWD && PAIR) || linear_epi(EPI),
                 "DB: double-buffered staging of the fp32 weight gradients, the SwiGLU "
@@ -1772,13 +1897,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         if (!valid || tl.row0 + q * 32 >= args.m_valid) continue;
         const int col0 = tl.n_tile * BN + half * (BN / 2);
+        DirectState<EPI> direct;
 #pragma unroll
         for (int c = 0; c < BN / 2; c += 32) {
           if (col0 + c >= args.n_valid) continue;
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
-          linear_chunk<EPI>(args, tl, q, lane, col0 + c, v, stage_buf, nst, &tmC, &om.h);
+          linear_chunk<EPI>(args, tl, q, lane, col0 + c, v, stage_buf, nst, &tmC, &om.h, direct,
+                            c == 0, c + 32 == BN / 2 || col0 + c + 32 >= args.n_valid);
         }
         continue;
       }
@@ -2653,8 +2780,9 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
       return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true, true>(
           name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
   }
+  // (8 KB of staging for the direct stores)
   if (pair)
-    return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true>(
+    return launch<256, A_MN, B_MN, SCHED_DENSE, EPI, SPLIT, true, linear_direct(EPI)>(
         name, ta, tb, tc, a, (a.m_tiles + 1) / 2 * a.n_tiles * splits, st, tl, om);
   // (the forward has its own kernels for one row tile)
   if constexpr (A_MN || B_MN)

@@ -380,6 +380,28 @@ def test_linear_takes_any_alignment_of_its_epilogue(M):
           + r.to(F64).abs() * 2 * U32)
 
 
+@pytest.mark.parametrize("M,N", [(130, 1), (200, 5), (257, 13), (131, 39), (300, 129), (192, 270),
+                                 (400, 301)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_linear_rows_of_any_alignment(M, N, out):
+    """y, z and the residual at element offsets of their own in rows of odd
+    lengths: values, and nothing written around them."""
+    K = 200
+    for oy, oz, orr in ((0, 0, 0), (1, 1, 1), (3, 5, 2), (7, 0, 4)):
+        x, w, b = randn(54, M, K), randn(55, N, K, scale=1 / math.sqrt(K)), randn(56, N, dtype=F32)
+        bufs = [torch.full((M * N + 32,), 7.0, dtype=out, device="cuda") for _ in range(2)]
+        y, z = (t[8 + o:8 + o + M * N].view(M, N) for t, o in zip(bufs, (oy, oz)))
+        r = randn(57, M * N + 8, dtype=out)[orr:orr + M * N].view(M, N)
+        api.linear(x, w, b, act="silu", residual=r, y=y, z=z)
+        y0, z0, mag = ref.linear(x, w, b, "silu", r)
+        dz = mag * (2 * K + 8) * U32
+        close(z, z0, z0.abs() * 1.01 * ref.rounding(out) + dz + 1e-30)
+        close(y, y0, y0.abs() * 1.01 * ref.rounding(out) + 1.13 * dz + act_bound(z0)
+              + r.to(F64).abs() * 2 * U32 + 1e-30)
+        for t, o in zip(bufs, (oy, oz)):
+            assert (t[:8 + o] == 7).all() and (t[8 + o + M * N:] == 7).all()
+
+
 def test_linear_writes_its_own_elements_only():
     """Nothing before or behind y and z, at sizes that end inside a tile."""
     for M, N in ((1, 130), (70, 61), (130, 136), (300, 264)):
