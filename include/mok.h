@@ -510,7 +510,8 @@ mok_status mok_linear_forward(const mok_linear_desc* desc, const void* x, const 
  * the products as the sum of bf16 parts, three (all 24 bits) for an fp32
  * result and two for a bf16 dx, unless it is bf16 itself (act NONE and dy
  * bf16); fp32 accumulation, fixed order.
- * x, w, dx, dw 16-byte aligned.  workspace: see the size query. */
+ * x, w, dx, dw 16-byte aligned.  workspace: see the size query (NULL where it
+ * says 0). */
 mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, const void* x,
                                const void* w, const void* z, void* dx, float* dw, float* dbias,
                                void* workspace, size_t ws_bytes, int32_t* status, void* stream);

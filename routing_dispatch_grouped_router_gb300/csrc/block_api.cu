@@ -216,7 +216,7 @@ mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, cons
   if (st != MOK_OK) return st;
   if ((D.accumulate & MOK_ADD_DX) && dx && D.dx_elem != MOK_ELEM_F32)
     return MOK_ERR_UNSUPPORTED;
-  if (D.M > 0 && (!dy || (dw && !x) || (dx && !w) || !workspace)) return MOK_ERR_INVALID_ARG;
+  if (D.M > 0 && (!dy || (dw && !x) || (dx && !w))) return MOK_ERR_INVALID_ARG;
   if (D.M > 0 && D.act != MOK_ACT_NONE && !z) return MOK_ERR_INVALID_ARG;
   const size_t ye = elem_size(D.y_elem);
   if (!aligned(dy, ye) || !aligned(z, ye) || !aligned(x, 16) || !aligned(w, 16) ||
@@ -225,6 +225,7 @@ mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, cons
     return MOK_ERR_INVALID_ARG;
   LinearWs W;
   linear_layout(D, &W);
+  if (D.M > 0 && W.total > 0 && !workspace) return MOK_ERR_INVALID_ARG;
   if (D.M > 0 && ws_bytes < W.total) return MOK_ERR_WORKSPACE;
   st = mok_check_device();
   if (st != MOK_OK) return st;

@@ -506,8 +506,8 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   return cudaGetLastError();
 }
 
-// Split-K products: y = act(sum of the parts + bias) + residual, part s in rows
-// s * m_pad.. of `part` (row stride N rounded up to 4), added in order.
+// Split products: y = act(sum of the parts + bias) + residual, part s from float4
+// s * stride of `part` (row stride N rounded up to 4), added in order.
 template <bool F32>
 __global__ void __launch_bounds__(256) linear_finish_kernel(LinArgs a, const float* part,
                                                             int splits, long long stride) {
@@ -531,10 +531,10 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(LinArgs a, const flo
   }
 }
 
-cudaError_t launch_finish(const LinArgs& a, const float* part, int splits, bool f32,
+// (rows: of a part)
+cudaError_t launch_finish(const LinArgs& a, const float* part, int splits, int64_t rows, bool f32,
                           cudaStream_t st) {
-  const long long n4 = (a.N + 3) / 4, items = a.M * n4;
-  const long long stride = (static_cast<long long>(a.M) + 127) / 128 * 128 * n4;
+  const long long n4 = (a.N + 3) / 4, items = a.M * n4, stride = rows * n4;
   long long blocks = (items + 255) / 256;
   const long long cap = 8LL * num_sms_current_device();
   if (blocks > cap) blocks = cap;
@@ -550,17 +550,36 @@ cudaError_t launch_finish(const LinArgs& a, const float* part, int splits, bool 
 // Shapes for the persistent engine: more than one 128-row tile of tokens.
 bool engine_takes(const mok_linear_desc& D) { return D.M > 128; }
 
-// K splits of an engine product C [M, N], reduction K: as many as its 256 x 256
-// tiles leave CTA pairs for (76 of a GB300, whatever the device, so that sums
-// do not depend on it), at least four K blocks each.  A second kernel adds them.
-int engine_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), nkb = (K + 63) / 64;
-  int64_t ks = 76 / tiles;
-  if (ks > nkb / 4) ks = nkb / 4;
-  if (ks > 16) ks = 16;
-  if (ks < 2) return 1;
-  const int64_t kb = (nkb + ks - 1) / ks;
-  return static_cast<int>((nkb + kb - 1) / kb);  // no empty split
+// Splits of a reduction of nkb 64-value blocks, A in `parts`, over the CTAs (or
+// CTA pairs) that `tiles` of `slots` leave: those of the least time by what was
+// measured, 260 ns a block on the tensor cores, 1.5 us or more for an epilogue on
+// the tiles' SMs alone, 2 us for the kernel that adds the partial results of `elems`
+// values, and their bytes at 5 TB/s.  (12 tokens, N = 1968, K = 368, two parts: dx
+// 24.7 us unsplit, 12 so; 772 tokens, N = 9: dw 21 and 13; 226 x 2275 x 904, fp32:
+// 23.1 and 13.4; 8331 tokens, K = 200: two splits' bytes would cost dx 2 us more
+// than they save.)
+int best_splits(int64_t tiles, int64_t slots, int64_t nkb, int parts, int64_t elems,
+                int most) {
+  int best = 1;
+  int64_t least = nkb * parts * 260 + 1500;
+  for (int64_t ks = 2; ks <= slots / tiles && ks <= nkb && ks <= most; ++ks) {
+    const int64_t kb = (nkb + ks - 1) / ks;
+    const int64_t t = kb * parts * 260 + 2000 + (ks + 1) * elems * 4 / 5000;
+    if (t >= least || (nkb + kb - 1) / kb != ks) continue;  // (no empty split)
+    least = t;
+    best = static_cast<int>(ks);
+  }
+  return best;
+}
+
+// K splits of an engine product C [M, N], reduction K: the tiles' CTAs or CTA
+// pairs are those of a GB300 (152, 76), whatever the device, so that sums do not
+// depend on it.
+int engine_splits(int64_t M, int64_t N, int64_t K, int parts) {
+  const int64_t rows = M > 128 ? 256 : 128, cols = M > 128 || parts < 3 ? 256 : 128;
+  const int64_t tiles = ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
+  return best_splits(tiles, M > 128 ? 76 : 152, (K + 63) / 64, parts, M * N,
+                     16);
 }
 
 size_t part_bytes(int splits, int64_t M, int64_t N) {
@@ -571,7 +590,7 @@ size_t part_bytes(int splits, int64_t M, int64_t N) {
 }  // namespace
 
 size_t linear_fwd_bytes(const mok_linear_desc& D) {
-  return engine_takes(D) ? part_bytes(engine_splits(D.M, D.N, D.K), D.M, D.N) : 0;
+  return engine_takes(D) ? part_bytes(engine_splits(D.M, D.N, D.K, 1), D.M, D.N) : 0;
 }
 
 cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w,
@@ -593,7 +612,7 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
                          reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(z);
   a.vec = D.N % 4 == 0 && (bits & 15) == 0;
   if (engine_takes(D)) {
-    const int splits = engine_splits(D.M, D.N, D.K);
+    const int splits = engine_splits(D.M, D.N, D.K, 1);
     const bool direct = D.N % 8 != 0 || (bits & 15) != 0;
     if (splits == 1)
       return gemm_linear_fwd(D.M, D.N, D.K, D.ld_x, x, w, bias, res, D.act, y, z, f32, direct,
@@ -602,7 +621,7 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
     const cudaError_t e =
         gemm_linear_part(D.M, D.N, D.K, D.ld_x, x, w, part, splits, status, st);
     if (e != cudaSuccess) return e;
-    return launch_finish(a, part, splits, f32, st);
+    return launch_finish(a, part, splits, (D.M + 127) / 128 * 128, f32, st);
   }
   // few tokens: on the CUDA cores while their products (M N K) do not take
   // longer than the tensor-core kernel's setup (measured even at 6e7: M = 4,
@@ -779,6 +798,7 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float4* part, int 
   grid_dep_wait();
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n4; i += gridDim.x * 256LL) {
     float4 v = part[i];
+#pragma unroll 8
     for (int s = 1; s < n; ++s) {
       const float4 p = part[s * stride4 + i];
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
@@ -791,24 +811,175 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float4* part, int 
   }
 }
 
-// K splits of the weight gradient (over the tokens): as many as its tiles
-// leave SMs for, at least eight 64-token blocks each.
+// The parts of dz that a product with a result of fp32 (or bf16) takes.  A bf16
+// dy without an activation is dz; else an fp32 result takes all 24 bits in three
+// parts (16 bits of two parts leave it 2.4e-6 off, the fp32 sums 5e-7), a bf16
+// result two.
+int dz_parts(const mok_linear_desc& D, bool f32) {
+  return D.y_elem != MOK_ELEM_F32 && D.act == MOK_ACT_NONE ? 1 : (f32 ? 3 : 2);
+}
+
+// ... of the weight gradient (over the tokens).
 int dw_splits(const mok_linear_desc& D) {
   const int64_t mt = (D.N + 127) / 128;
   const int64_t tiles = (mt + 1) / 2 * ((D.K + 255) / 256);
-  const int64_t slots = mt > 1 ? 76 : 152;  // whatever the device: the sums do not depend on it
-  const int64_t nkb = (D.M + 63) / 64;
-  int64_t ks = slots / tiles;
-  if (ks > nkb / 8) ks = nkb / 8;
-  if (ks < 1) return 1;
-  const int64_t kb = (nkb + ks - 1) / ks;
-  return static_cast<int>((nkb + kb - 1) / kb);  // no empty split
+  return best_splits(tiles, mt > 1 ? 76 : 152, (D.M + 63) / 64, dz_parts(D, true), D.N * D.K,
+                     32);
 }
+
+// Up to kFewTokens tokens, on the CUDA cores: dz, dbias, dx and dw in one pass
+// over w and dw, whose bytes bound it.  A block takes 128 columns of K (a lane
+// four) and a slice of the rows n, which its warps share: per row a lane has
+// dz[m][n] (fp32, shared memory) for dw[n] = sum_m dz[m][n] x[m], stored at
+// once, and for its sums dx[m] += dz[m][n] w[n].  The warps' sums are added in
+// order; where there are several slices, a second kernel adds theirs.  (One token,
+// N = 2048, K = 7168: 17.3 us, floor 13.0; N = 6351, K = 6072: two tokens 47 us,
+// eight 66, 72 by the tensor cores in six launches; floor 34; one token, N = 37,
+// K = 2520: 2.6 and 13.  At eight tokens the products on the CUDA cores show.)
+constexpr int kFewDz = 512;  // rows whose dz a block holds
+struct FewBwd {
+  const void *dy, *z;
+  const __nv_bfloat16 *x, *w;
+  void* dx;      // (NULL: not wanted; so dw and dbias)
+  float *dw, *dbias;
+  float* part;   // [slices, M, K], several slices
+  long long ld_x;
+  int M, N, K, rows, act;  // rows: of a slice
+  bool dx_f32, add_dx;
+};
+
+template <int MT, bool F32, bool ADD>
+__global__ void __launch_bounds__(kFewThreads, 2) linear_bwd_few_kernel(FewBwd a) {
+  constexpr int U = ADD ? 4 : 8;  // rows of a warp in flight
+  constexpr int kWarps = kFewThreads / 32;
+  union Shared {
+    float dz[kFewDz][MT];
+    float4 dx[kWarps][MT][32];
+  };
+  __shared__ __align__(16) Shared s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = (blockIdx.x * 32 + lane) * 4;
+  const bool in = c < a.K;
+  const int n0 = blockIdx.y * a.rows, n1 = n0 + a.rows < a.N ? n0 + a.rows : a.N;
+  grid_dep_launch();
+  grid_dep_wait();
+  float xf[MT][4], acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xf[m][j] = acc[m][j] = 0.f;
+    if (in && a.dw && m < a.M) load4<false>(a.x, m * a.ld_x + c, xf[m]);
+  }
+  for (int t0 = n0; t0 < n1; t0 += kFewDz) {
+    const int cnt = n1 - t0 < kFewDz ? n1 - t0 : kFewDz;
+    __syncthreads();  // the rows before have been used
+    for (int i = threadIdx.x; i < cnt; i += kFewThreads) {
+      float d[MT], sum = 0.f;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const long long o = static_cast<long long>(m) * a.N + t0 + i;
+        d[m] = m < a.M ? load1<F32>(a.dy, o) : 0.f;
+        if (a.act != MOK_ACT_NONE && m < a.M) d[m] *= act_slope(load1<F32>(a.z, o), a.act);
+        sum += d[m];
+      }
+#pragma unroll
+      for (int m = 0; m < MT; m += 2)
+        *reinterpret_cast<float2*>(&s.dz[i][m]) = make_float2(d[m], d[m + 1]);
+      if (a.dbias && blockIdx.x == 0) a.dbias[t0 + i] = ADD ? a.dbias[t0 + i] + sum : sum;
+    }
+    __syncthreads();
+    if (!in || (!a.dx && !a.dw)) continue;
+    for (int i = warp; i < cnt; i += U * kWarps) {
+      uint2 wv[U];
+      float4 old[ADD ? U : 1];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = i + u * kWarps;
+        const long long o = static_cast<long long>(t0 + row) * a.K + c;
+        wv[u] = make_uint2(0u, 0u);
+        if (a.dx && row < cnt) wv[u] = *reinterpret_cast<const uint2*>(a.w + o);
+        if (ADD && a.dw && row < cnt) old[u] = *reinterpret_cast<const float4*>(a.dw + o);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = i + u * kWarps;
+        if (row >= cnt) break;
+        const float wf[4] = {bf16lo(wv[u].x), bf16hi(wv[u].x), bf16lo(wv[u].y), bf16hi(wv[u].y)};
+        float v[4] = {0.f, 0.f, 0.f, 0.f}, dz[MT];
+#pragma unroll
+        for (int m = 0; m < MT; m += 2) {
+          const float2 t = *reinterpret_cast<const float2*>(&s.dz[row][m]);
+          dz[m] = t.x;
+          dz[m + 1] = t.y;
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float d = dz[m];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[j] = fmaf(d, xf[m][j], v[j]);
+            acc[m][j] = fmaf(d, wf[j], acc[m][j]);
+          }
+        }
+        if (ADD) {
+          const float4 t = old[ADD ? u : 0];
+          v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;
+        }
+        if (a.dw) store4<true>(a.dw, static_cast<long long>(t0 + row) * a.K + c, v);
+      }
+    }
+  }
+  if (!a.dx) return;
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    s.dx[warp][m][lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+  __syncthreads();
+  for (int m = warp; m < a.M; m += kWarps) {
+    if (!in) break;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) {
+      const float4 t = s.dx[q][m][lane];
+      v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;
+    }
+    const long long o = static_cast<long long>(m) * a.K + c;
+    if (gridDim.y > 1) {
+      store4<true>(a.part, (static_cast<long long>(blockIdx.y) * a.M) * a.K + o, v);
+    } else if (a.dx_f32) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      if (a.add_dx) load4<true>(a.dx, o, t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += t[j];
+      store4<true>(a.dx, o, v);
+    } else {
+      store4<false>(a.dx, o, v);
+    }
+  }
+}
+
+// Rows of a slice: two blocks per SM (of a GB300, whatever the device), at
+// least eight rows per warp.
+int64_t few_rows(const mok_linear_desc& D) {
+  const int64_t cols = (D.K + 127) / 128;
+  int64_t slices = 304 / cols;
+  if (slices < 1) slices = 1;
+  const int64_t rows = ((D.N + slices - 1) / slices + 7) / 8 * 8;
+  return rows < 64 ? 64 : rows;
+}
+
+bool few_bwd(const mok_linear_desc& D) { return D.M <= kFewTokens; }
 
 }  // namespace
 
 void linear_layout(const mok_linear_desc& D, LinearWs* W) {
   auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  if (few_bwd(D)) {
+    *W = LinearWs{};
+    const int64_t slices = (D.N + few_rows(D) - 1) / few_rows(D);
+    W->total = slices > 1 ? al(static_cast<size_t>(slices) * D.M * D.K * 4) : 0;
+    return;
+  }
   W->n_pad = (D.N + 63) / 64 * 64;
   W->bias_rows = (D.M + kDzRows - 1) / kDzRows;
   W->dw_splits = dw_splits(D);
@@ -817,12 +988,65 @@ void linear_layout(const mok_linear_desc& D, LinearWs* W) {
   W->part_bias = 3 * al(dz);
   W->part_dw = W->part_bias + al(static_cast<size_t>(W->bias_rows) * D.N * 4);
   // partial products of dx, then of dw: one region
-  W->dx_splits = D.M > 128 ? engine_splits(D.M, D.K, W->n_pad) : 1;
+  W->dx_splits = engine_splits(D.M, D.K, W->n_pad, dz_parts(D, D.dx_elem == MOK_ELEM_F32));
   const size_t rows = static_cast<size_t>((D.N + 127) / 128 * 128);
   const size_t a = part_bytes(W->dx_splits, D.M, D.K);
   const size_t b = W->dw_splits > 1 ? W->dw_splits * rows * D.K * 4 : 0;
   W->total = W->part_dw + al(a > b ? a : b);
 }
+
+namespace {
+
+cudaError_t launch_few_bwd(const mok_linear_desc& D, const void* dy, const void* x, const void* w,
+                           const void* z, void* dx, float* dw, float* dbias, float* part,
+                           cudaStream_t st) {
+  FewBwd a;
+  a.dy = dy; a.z = z;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.w = static_cast<const __nv_bfloat16*>(w);
+  a.dx = dx; a.dw = dw; a.dbias = dbias; a.part = part;
+  a.ld_x = D.ld_x;
+  a.M = static_cast<int>(D.M); a.N = static_cast<int>(D.N); a.K = static_cast<int>(D.K);
+  a.rows = static_cast<int>(few_rows(D));
+  a.act = D.act;
+  a.dx_f32 = D.dx_elem == MOK_ELEM_F32;
+  a.add_dx = (D.accumulate & MOK_ADD_DX) != 0;
+  const int64_t slices = (D.N + a.rows - 1) / a.rows;
+  const int64_t cols = dx || dw ? (D.K + 127) / 128 : 1;
+  cudaError_t e = cudaSuccess;
+  {
+    ProfScope prof("linear_bwd_few", st);
+    auto run = [&](auto MT, auto F) {
+      constexpr int mt = decltype(MT)::value;
+      constexpr bool f32 = decltype(F)::value;
+      e = launch_dependent((D.accumulate & MOK_ADD_DW) ? linear_bwd_few_kernel<mt, f32, true>
+                                                       : linear_bwd_few_kernel<mt, f32, false>,
+                           dim3(static_cast<unsigned>(cols), static_cast<unsigned>(slices)),
+                           dim3(kFewThreads), 0, st, a);
+    };
+    auto by_tokens = [&](auto F) {
+      using std::integral_constant;
+      if (D.M <= 2) run(integral_constant<int, 2>(), F);
+      else if (D.M <= 4) run(integral_constant<int, 4>(), F);
+      else run(integral_constant<int, kFewTokens>(), F);
+    };
+    if (D.y_elem == MOK_ELEM_F32) by_tokens(std::true_type());
+    else by_tokens(std::false_type());
+    count_launch();
+  }
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess || slices == 1 || !dx) return e;
+  LinArgs f = {};
+  f.y = dx;
+  f.res = a.add_dx ? dx : nullptr;  // (fp32)
+  f.M = a.M;
+  f.N = a.K;
+  f.act = MOK_ACT_NONE;
+  f.vec = 1;
+  return launch_finish(f, part, static_cast<int>(slices), D.M, a.dx_f32, st);
+}
+
+}  // namespace
 
 cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const void* x,
                               const void* w, const void* z, void* dx, float* dw, float* dbias,
@@ -835,12 +1059,11 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
   const bool vec = D.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(z)) & 15) == 0;
   // a bf16 dy without an activation is dz already
   const bool direct = !f32 && D.act == MOK_ACT_NONE && vec;
-  // an fp32 result takes all 24 bits of dz in three parts (16 bits of two
-  // parts leave it 2.4e-6 off, the fp32 sums 5e-7), a bf16 result two
   const bool dxf = D.dx_elem == MOK_ELEM_F32;
-  const bool split = f32 || D.act != MOK_ACT_NONE;
-  const int parts = direct ? 0 : (!split ? 1 : (dw || dxf ? 3 : 2));
+  const int parts = direct ? 0 : dz_parts(D, dw || dxf);
   const bool products = D.M > 0 && (dx || dw);
+  if (D.M > 0 && few_bwd(D))
+    return launch_few_bwd(D, dy, x, w, z, dx, dw, dbias, static_cast<float*>(ws), st);
   float* part_bias = reinterpret_cast<float*>(b + W.part_bias);
   if (D.M > 0 && ((products && !direct) || dbias)) {
     DzArgs a;
@@ -884,16 +1107,15 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     return cudaSuccess;
   }
   BfParts dz;
-  dz.n = split ? 3 : 1;
+  dz.n = dz_parts(D, true);
   dz.ld = direct ? D.N : W.n_pad;
   for (int p = 0; p < 3; ++p) dz.part[p] = b + W.dz[p];
   if (direct) dz.part[0] = dy;
   if (dx) {
     BfParts d = dz;
-    if (split && !dxf) d.n = 2;
+    d.n = dz_parts(D, dxf);
     const bool sum = W.dx_splits > 1;
     float* part = reinterpret_cast<float*>(b + W.part_dw);
-    if (sum && split && !dxf && parts == 2) d.n = 2;
     cudaError_t e = gemm_linear_dx(D.M, D.N, D.K, d, w, sum ? part : dx, sum || dxf,
                                    !sum && add_dx, W.dx_splits, status, st);
     if (e != cudaSuccess) return e;
@@ -905,7 +1127,7 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
       f.N = static_cast<int>(D.K);
       f.act = MOK_ACT_NONE;
       f.vec = 1;
-      e = launch_finish(f, part, W.dx_splits, dxf, st);
+      e = launch_finish(f, part, W.dx_splits, (D.M + 127) / 128 * 128, dxf, st);
       if (e != cudaSuccess) return e;
     }
   }

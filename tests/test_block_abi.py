@@ -125,7 +125,9 @@ def test_linear_pointers_refused(lib):
     assert b(linear(), None, A, A, None, A, A, A, A, 1 << 30, None, None) == 1
     assert b(linear(act=2), A, A, A, None, A, A, A, A, 1 << 30, None, None) == 1   # no z
     assert b(linear(accumulate=1), A, A, A, None, A, A, A, A, 1 << 30, None, None) == 2  # bf16 dx
-    assert b(linear(), A, A, A, None, A, A, A, A, 16, None, None) == 3
+    d = linear(M=40)
+    assert b(d, A, A, A, None, A, A, A, None, 1 << 30, None, None) == 1
+    assert b(d, A, A, A, None, A, A, A, A, 16, None, None) == 3
 
 
 def test_python_refusals_without_a_gpu(lib):

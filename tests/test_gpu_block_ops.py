@@ -2,6 +2,7 @@
 residual addition with RMS norm, the router's auxiliary losses, the dense
 product; each with its gradient, at the sizes, types, strides and masks where
 it can go wrong.  Bounds are derived in _block_ref.py."""
+import ctypes
 import math
 
 import pytest
@@ -470,6 +471,46 @@ def test_linear_backward(M, N, K, act, dyt, dxt, bias):
     assert api.device_status(api.operator_status()) == 0
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 7, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 8), (40, 136), (513, 264), (1300, 1032), (2050, 40008)])
+def test_linear_backward_of_few_tokens(M, N, K):
+    """Slices of N and their sum, accumulation, and each gradient without the others."""
+    x, w = randn(90, M, K, pad=8), randn(91, N, K, scale=1 / math.sqrt(K))
+    dy, z = randn(92, M, N, dtype=F32), randn(93, M, N, dtype=F32)
+    dx, dw, db = api.linear_backward(dy, x, w, z, act="silu", bias=True, dx_dtype=F32)
+    (dx0, dw0, db0), (mx, mw, mb) = ref.linear_backward(dy, x, w, z, "silu")
+    dza = dy.to(F64).abs() * 64 * U32
+    close(dx, dx0, mx * (2 * 3 * N * U32 + U32) + dza @ w.to(F64).abs() + 1e-30)
+    close(dw, dw0, mw * (2 * 3 * M + 16) * U32 + dza.T @ x.to(F64).abs() + 1e-30)
+    close(db, db0, mb * (2 * M + 16) * U32 + dza.sum(0) + 1e-30)
+    again = [t.clone() for t in (dx, dw, db)]
+    api.linear_backward(dy, x, w, z, act="silu", dx=again[0], dw=again[1], dbias=again[2],
+                        accumulate=True)
+    assert all(torch.equal(a + a, b) for a, b in zip((dx, dw, db), again))
+
+
+@pytest.mark.parametrize("M,K", [(5, 136), (5, 40008), (40, 520)])
+def test_linear_gradients_alone(M, K):
+    """Through the C entry: any of dx, dw and dbias may be NULL."""
+    N = 1300
+    x, w = randn(94, M, K), randn(95, N, K)
+    dy = randn(96, M, N)
+    want = api.linear_backward(dy, x, w, bias=True)
+    d = _lib.LinearDesc(M=M, N=N, K=K)
+    n = ctypes.c_size_t()
+    f = _lib.load()
+    assert f.mok_linear_workspace_size(d, 1, n) == 0
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    for i in range(3):
+        got = torch.zeros_like(want[i])
+        out = [got.data_ptr() if i == j else None for j in range(3)]
+        stream = torch.cuda.current_stream().cuda_stream
+        assert f.mok_linear_backward(d, dy.data_ptr(), x.data_ptr(), w.data_ptr(), None, *out,
+                                     ws.data_ptr() if n.value else None, n.value, None,
+                                     stream) == 0
+        assert torch.equal(got, want[i])
+
+
 def test_linear_backward_accumulates_and_repeats():
     for M, N, K in ((40, 60, 136), (3000, 264, 512), (9000, 64, 256)):
         x, w, dy = randn(80, M, K), randn(81, N, K), randn(82, M, N, dtype=F32)
@@ -618,7 +659,7 @@ def test_refusals():
         (1, lambda: api.linear(x[:, 1:57], randn(99, 8, 56))),
         (2, lambda: api.linear_backward(randn(99, 4, 8), x, randn(99, 8, 64), accumulate=True,
                                         dx=torch.zeros_like(x), dw=torch.zeros(8, 64, device="cuda"))),
-        (3, lambda: api.linear_backward(randn(99, 4, 8), x, randn(99, 8, 64),
+        (3, lambda: api.linear_backward(randn(99, 40, 8), randn(99, 40, 64), randn(99, 8, 64),
                                         workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))),
     ]
     for code, call in refused:
