@@ -533,6 +533,7 @@ struct NormBwd {
   float* part;  // [gridDim.x, d] partial weight gradients (NULL: not computed)
   long long rows, ld_dy, ld_s, ld_ds, ld_dx;
   int d, nvec, w_f32;
+  int ld8;  // SHIFT: elements from one row to the next, mod 8
   float inv_d, eps;
 };
 
@@ -662,16 +663,42 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_kernel(NormBwd a) {
 // copy), issued a row or more ahead, so that the reductions and barriers of one
 // row do not interrupt the stream of loads.  A slot is filled again after the
 // next row's barrier, which every thread reaches only when done with it.
+//
+// SHIFT: rows of any length in aligned tensors.  Row r begins r ld8 elements (mod
+// 8) past a multiple of eight, in all of them alike; a block's rows are a multiple
+// of eight apart, so all of its rows begin at the same h.  A thread's eight columns
+// are 8 v - h .. + 7: aligned words everywhere, and fixed columns for its weights
+// and their gradients.  The copies take whole 16-byte words (a few elements of the
+// rows next to it with them), except past the end of the last row.
+// (13142 x 2373 bf16: 55 us, 148 by word loads; floor 37.  8192 x 4095 fp32: 88 and
+// 111; floor 79.)
 constexpr int kBulkMinD = 1024;
-template <bool DYF32, bool SF32, int NV>
-__global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, int depth) {
+constexpr int kShiftMinD = 512;
+template <bool F32>
+__device__ __forceinline__ void bulk_row(uint8_t* dst, const void* base, long long r, long long ld,
+                                         int h, uint32_t bytes, uint32_t whole, uint64_t* bar) {
+  constexpr int es = F32 ? 4 : 2;
+  const char* src = static_cast<const char*>(row_at<F32>(base, r, ld)) - h * es;
+  bulk_load(dst, src, whole, bar);
+  for (uint32_t i = whole; i < bytes; i += es) {  // (the last row's last elements)
+    if (F32) *reinterpret_cast<float*>(dst + i) = *reinterpret_cast<const float*>(src + i);
+    else *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
+  }
+}
+
+// (launch bounds: the registers that 768 threads on an SM leave, see bwd_shape)
+template <bool DYF32, bool SF32, int NV, bool SHIFT>
+__global__ void __launch_bounds__(NV == 2 ? 768 : 512)
+    add_rmsnorm_bwd_bulk_kernel(NormBwd a, int depth) {
   extern __shared__ __align__(128) uint8_t s_rows[];
   __shared__ __align__(8) uint64_t full[kBulkMaxDepth];
   __shared__ float red[2][2][16];
   __shared__ int s_abort;
   grid_dep_launch();
   const int t = threadIdx.x, tpr = blockDim.x, nw = tpr >> 5;
-  const uint32_t s_bytes = a.d * (SF32 ? 4 : 2), y_bytes = a.d * (DYF32 ? 4 : 2);
+  const int h = SHIFT ? (blockIdx.x * a.ld8) & 7 : 0;
+  const int nvec = SHIFT ? (a.d + h + 7) >> 3 : a.nvec;
+  const uint32_t s_bytes = nvec * (SF32 ? 32 : 16), y_bytes = nvec * (DYF32 ? 32 : 16);
   const uint32_t row_bytes = s_bytes + y_bytes + (a.ds ? s_bytes : 0);
   if (t == 0) {
     for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
@@ -683,10 +710,36 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
   volatile int* vabort = &s_abort;
   auto fill = [&](int slot, long long r) {  // thread 0
     uint8_t* p = s_rows + slot * row_bytes;
+    if (SHIFT && r == a.rows - 1) {
+      const uint32_t se = (a.d + h) * (SF32 ? 4 : 2), ye = (a.d + h) * (DYF32 ? 4 : 2);
+      const uint32_t sw = se & ~15u, yw = ye & ~15u;
+      bulk_row<SF32>(p, a.s, r, a.ld_s, h, se, sw, &full[slot]);
+      bulk_row<DYF32>(p + s_bytes, a.dy, r, a.ld_dy, h, ye, yw, &full[slot]);
+      if (a.ds) bulk_row<SF32>(p + s_bytes + y_bytes, a.ds, r, a.ld_ds, h, se, sw, &full[slot]);
+      mbar_arrive_expect_tx(&full[slot], sw + yw + (a.ds ? sw : 0));
+      return;
+    }
     mbar_arrive_expect_tx(&full[slot], row_bytes);
-    bulk_load(p, row_at<SF32>(a.s, r, a.ld_s), s_bytes, &full[slot]);
-    bulk_load(p + s_bytes, row_at<DYF32>(a.dy, r, a.ld_dy), y_bytes, &full[slot]);
-    if (a.ds) bulk_load(p + s_bytes + y_bytes, row_at<SF32>(a.ds, r, a.ld_ds), s_bytes, &full[slot]);
+    bulk_row<SF32>(p, a.s, r, a.ld_s, h, s_bytes, s_bytes, &full[slot]);
+    bulk_row<DYF32>(p + s_bytes, a.dy, r, a.ld_dy, h, y_bytes, y_bytes, &full[slot]);
+    if (a.ds)
+      bulk_row<SF32>(p + s_bytes + y_bytes, a.ds, r, a.ld_ds, h, s_bytes, s_bytes, &full[slot]);
+  };
+  // SHIFT: which elements of this thread's vectors are the rows' own
+  uint32_t own[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    own[i] = 0xffu;
+    if (!SHIFT) continue;
+    const int e = 8 * (t + i * tpr) - h;  // element 0's column
+    if (e < 0) own[i] &= 0xffu << -e;
+    if (e + 8 > a.d) own[i] &= e < a.d ? 0xffu >> (e + 8 - a.d) : 0u;
+  }
+  auto mask = [&](uint32_t m, float (&v)[8]) {
+    if (SHIFT && m != 0xffu) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (m >> j & 1u) ? v[j] : 0.f;
+    }
   };
   const long long step = gridDim.x;
   int filled = 0;  // thread 0: rows requested
@@ -699,9 +752,20 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
     const int vi = t + i * tpr;
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = w[i][j] = 0.f;
-    if (vi < a.nvec) {
-      if (a.w_f32) load8<true, true>(a.w, vi, a.d, w[i]);
-      else load8<false, true>(a.w, vi, a.d, w[i]);
+    if (vi < nvec) {
+      if (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = 8 * vi - h + j;
+          if (own[i] >> j & 1u)
+            w[i][j] = a.w_f32 ? static_cast<const float*>(a.w)[e]
+                              : __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[e]);
+        }
+      } else if (a.w_f32) {
+        load8<true, true>(a.w, vi, a.d, w[i]);
+      } else {
+        load8<false, true>(a.w, vi, a.d, w[i]);
+      }
     }
   }
   int it = 0;
@@ -716,10 +780,12 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vi = t + i * tpr;
-      if (vi < a.nvec) {
+      if (vi < nvec) {
         float s[8], dy[8];
         load8<SF32, true>(p, vi, a.d, s);
         load8<DYF32, true>(p + s_bytes, vi, a.d, dy);
+        mask(own[i], s);
+        mask(own[i], dy);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           ss = fmaf(s[j], s[j], ss);
@@ -748,7 +814,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vi = t + i * tpr;
-      if (vi >= a.nvec) continue;
+      if (vi >= nvec) continue;
       float s[8], dy[8], o[8];
       load8<SF32, true>(p, vi, a.d, s);
       load8<DYF32, true>(p + s_bytes, vi, a.d, dy);
@@ -758,12 +824,24 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = 0.f;
       }
+      mask(own[i], s);
+      mask(own[i], dy);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         o[j] = rstd * (dy[j] * w[i][j] - s[j] * c) + o[j];
         dw[i][j] = fmaf(dy[j], s[j] * rstd, dw[i][j]);
       }
-      store8<SF32, true>(row_at<SF32>(a.dx, r, a.ld_dx), vi, a.d, o);
+      char* out = static_cast<char*>(row_at<SF32>(a.dx, r, a.ld_dx)) - h * (SF32 ? 4 : 2);
+      if (SHIFT && own[i] != 0xffu) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (!(own[i] >> j & 1u)) continue;
+          if (SF32) reinterpret_cast<float*>(out)[8 * vi + j] = o[j];
+          else reinterpret_cast<__nv_bfloat16*>(out)[8 * vi + j] = __float2bfloat16_rn(o[j]);
+        }
+      } else {
+        store8<SF32, true>(out, vi, a.d, o);
+      }
     }
   }
   if (*vabort) {
@@ -772,10 +850,25 @@ __global__ void __launch_bounds__(512) add_rmsnorm_bwd_bulk_kernel(NormBwd a, in
   }
   if (!a.part) return;
   float* out = a.part + static_cast<long long>(blockIdx.x) * a.d;
+  if (SHIFT) {  // through the ring's memory, for whole sectors
+    float* s_dw = reinterpret_cast<float*>(s_rows);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vi = t + i * tpr;
+      if (vi >= nvec) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (own[i] >> j & 1u) s_dw[8 * vi - h + j] = dw[i][j];
+    }
+    __syncthreads();
+    for (int e = t; e < a.d; e += blockDim.x) out[e] = s_dw[e];
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int vi = t + i * tpr;
-    if (vi < a.nvec) store8<true, true>(out, vi, a.d, dw[i]);
+    if (vi < nvec) store8<true, true>(out, vi, a.d, dw[i]);
   }
 }
 
@@ -821,15 +914,25 @@ struct BwdShape {
   int64_t blocks;
 };
 constexpr int kBulkSmem = 216 * 1024;  // of an SM's shared memory, for all its blocks
-BwdShape bwd_shape(int64_t rows, int64_t d, bool vec, int64_t row_bytes) {
-  const int nvec = static_cast<int>(vec ? d / 8 : (d + 255) / 256 * 32);
+// How a row's elements are taken: words at any alignment by register loads,
+// aligned vectors, or aligned vectors of rows at a common shift.
+enum class Rows { kAny, kVec, kShift };
+int64_t bwd_row_bytes(int64_t d, int64_t per_elem, Rows how) {
+  return how == Rows::kShift ? (d + 14) / 8 * 8 * per_elem : d * per_elem;
+}
+BwdShape bwd_shape(int64_t rows, int64_t d, Rows how, int64_t row_bytes) {
+  const bool bulk = how == Rows::kShift || (how == Rows::kVec && d >= kBulkMinD);
+  const int nvec = static_cast<int>(how == Rows::kVec     ? d / 8
+                                    : how == Rows::kShift ? (d + 14) / 8
+                                                          : (d + 255) / 256 * 32);
   BwdShape b;
   b.nv = nvec <= 32 ? 1 : (nvec <= 1024 ? 2 : 4);
   b.tpr = ((nvec + b.nv - 1) / b.nv + 31) / 32 * 32;
   b.rpb = b.tpr == 32 ? 8 : 1;
+  if (how == Rows::kShift) b.rpb = 1;
   b.depth = 0;
   int per_sm = (b.rpb > 1 ? 1536 : 768) / (b.tpr * b.rpb);
-  if (vec && d >= kBulkMinD) {
+  if (bulk) {
     // a row's chain of barrier and reductions takes a block long enough for an
     // SM's share of the memory to move some 70 KB: enough blocks to cover it
     // (4099 x 2880 bf16: 29.7 us with two, 24.5 with three, 23.8 with four or
@@ -841,41 +944,59 @@ BwdShape bwd_shape(int64_t rows, int64_t d, bool vec, int64_t row_bytes) {
     while (per_sm > 1 && per_sm * 2 * row_bytes > kBulkSmem) --per_sm;
   }
   per_sm = per_sm < 1 ? 1 : (per_sm > 16 ? 16 : per_sm);
-  if (vec && d >= kBulkMinD) {
+  if (bulk) {
     b.depth = static_cast<int>(kBulkSmem / per_sm / row_bytes);
     if (b.depth > kBulkMaxDepth) b.depth = kBulkMaxDepth;
   }
   const int64_t need = (rows + b.rpb - 1) / b.rpb;
-  b.blocks = need < 152 * per_sm ? need : 152 * per_sm;
+  b.blocks = need < 152 * per_sm ? need : 152 * per_sm;  // (kShift: a multiple of eight)
   return b;
 }
 
-template <bool DYF32, bool SF32, int NV>
+template <bool DYF32, bool SF32, int NV, bool SHIFT>
 cudaError_t bulk_launch(const NormBwd& a, const BwdShape& b, int64_t row_bytes, cudaStream_t st) {
-  auto kern = add_rmsnorm_bwd_bulk_kernel<DYF32, SF32, NV>;
+  auto kern = add_rmsnorm_bwd_bulk_kernel<DYF32, SF32, NV, SHIFT>;
   const int smem = static_cast<int>(b.depth * row_bytes);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(static_cast<unsigned>(b.blocks)), dim3(b.tpr), smem, st, a,
                           b.depth);
 }
 
-template <bool DYF32, bool SF32, bool VEC>
+template <bool DYF32, bool SF32, Rows HOW>
 cudaError_t bwd_launch(const NormBwd& a, int64_t row_bytes, cudaStream_t st) {
-  const BwdShape b = bwd_shape(a.rows, a.d, VEC, row_bytes);
+  const BwdShape b = bwd_shape(a.rows, a.d, HOW, row_bytes);
   ProfScope prof("add_rmsnorm_bwd", st);
   count_launch();
-  if constexpr (VEC) {
+  constexpr bool kShift = HOW == Rows::kShift;
+  if constexpr (HOW != Rows::kAny) {
     // (with at least two rows in the ring: the next one's copy is under way)
     if (b.depth >= 2)
-      return b.nv == 2 ? bulk_launch<DYF32, SF32, 2>(a, b, row_bytes, st)
-                       : bulk_launch<DYF32, SF32, 4>(a, b, row_bytes, st);
+      return b.nv == 2 ? bulk_launch<DYF32, SF32, 2, kShift>(a, b, row_bytes, st)
+                       : bulk_launch<DYF32, SF32, 4, kShift>(a, b, row_bytes, st);
   }
-  auto kern = b.nv == 1 ? add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 1>
-                        : (b.nv == 2 ? add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 2>
-                                     : add_rmsnorm_bwd_kernel<DYF32, SF32, VEC, 4>);
-  return launch_dependent(kern, dim3(static_cast<unsigned>(b.blocks)), dim3(b.tpr, b.rpb), 0, st,
-                          a);
+  if constexpr (kShift) {
+    return cudaErrorInvalidValue;  // (not chosen: see shift_rows)
+  } else {
+    constexpr bool kVec = HOW == Rows::kVec;
+    auto kern = b.nv == 1 ? add_rmsnorm_bwd_kernel<DYF32, SF32, kVec, 1>
+                          : (b.nv == 2 ? add_rmsnorm_bwd_kernel<DYF32, SF32, kVec, 2>
+                                       : add_rmsnorm_bwd_kernel<DYF32, SF32, kVec, 4>);
+    return launch_dependent(kern, dim3(static_cast<unsigned>(b.blocks)), dim3(b.tpr, b.rpb), 0, st,
+                            a);
+  }
+}
+
+// Whether rows of this length are taken at a common shift where the tensors'
+// alignment allows it: more of them than blocks, so that the ring has a row ahead
+// (499 x 1109: 10.2 us so, 8.8 by word loads; 3988 x 660: 16 and 19).
+bool shift_rows(int64_t rows, int64_t d, int64_t row_bytes) {
+  if (d < kShiftMinD || (d + 14) / 8 > 4 * 512) return false;
+  const BwdShape b = bwd_shape(rows, d, Rows::kShift, row_bytes);
+  return b.depth >= 2 && rows > b.blocks;
 }
 
 }  // namespace
@@ -883,12 +1004,16 @@ cudaError_t bwd_launch(const NormBwd& a, int64_t row_bytes, cudaStream_t st) {
 int64_t norm_bwd_blocks(const mok_rmsnorm_desc& D) {
   // the most that any alignment of the pointers leads to
   const int64_t se = D.s_elem == MOK_ELEM_F32 ? 4 : 2, ye = D.x_elem == MOK_ELEM_F32 ? 4 : 2;
-  int64_t most = bwd_shape(D.rows, D.d, false, 0).blocks;
-  if (D.d % 8 == 0)
-    for (int skip = 0; skip < 2; ++skip) {
-      const int64_t b = bwd_shape(D.rows, D.d, true, D.d * (se * (1 + skip) + ye)).blocks;
-      if (b > most) most = b;
-    }
+  int64_t most = bwd_shape(D.rows, D.d, Rows::kAny, 0).blocks;
+  for (int skip = 0; skip < 2; ++skip) {
+    const int64_t per_elem = se * (1 + skip) + ye;
+    int64_t b = 0, n = bwd_row_bytes(D.d, per_elem, Rows::kShift);
+    if (shift_rows(D.rows, D.d, n)) b = bwd_shape(D.rows, D.d, Rows::kShift, n).blocks;
+    if (b > most) most = b;
+    if (D.d % 8 != 0) continue;
+    b = bwd_shape(D.rows, D.d, Rows::kVec, D.d * per_elem).blocks;
+    if (b > most) most = b;
+  }
   return most;
 }
 
@@ -913,20 +1038,30 @@ cudaError_t launch_add_rmsnorm_bwd(const mok_rmsnorm_desc& D, const void* dy, co
     const int ye = yf ? 4 : 2, se = sf ? 4 : 2;
     const bool vec = a.d % 8 == 0 && vec_rows(dy, a.ld_dy, ye) && vec_rows(s, a.ld_s, se) &&
                      vec_rows(ds, a.ld_ds, se) && vec_rows(dx, a.ld_dx, se) && vec_rows(w, 0, 4);
-    if (!vec) a.nvec = (a.d + 255) / 256 * 32;
-    const int64_t row_bytes = D.d * (se * (ds ? 2 : 1) + ye);
-    grid = bwd_shape(D.rows, D.d, vec, row_bytes).blocks;
-    if (yf) {
-      if (sf) e = vec ? bwd_launch<true, true, true>(a, row_bytes, st)
-                      : bwd_launch<true, true, false>(a, row_bytes, st);
-      else e = vec ? bwd_launch<true, false, true>(a, row_bytes, st)
-                   : bwd_launch<true, false, false>(a, row_bytes, st);
-    } else {
-      if (sf) e = vec ? bwd_launch<false, true, true>(a, row_bytes, st)
-                      : bwd_launch<false, true, false>(a, row_bytes, st);
-      else e = vec ? bwd_launch<false, false, true>(a, row_bytes, st)
-                   : bwd_launch<false, false, false>(a, row_bytes, st);
-    }
+    // every tensor's rows begin alike: aligned bases, lengths that agree mod 8
+    // (fp32 alone: mod 4)
+    const int64_t step = !yf ? a.ld_dy : a.ld_s;
+    auto alike = [&](const void* p, int64_t ld, bool f) {
+      return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld - step) % (f ? 4 : 8) == 0);
+    };
+    const int64_t per_elem = se * (ds ? 2 : 1) + ye;
+    Rows how = vec ? Rows::kVec : Rows::kAny;
+    if (!vec && alike(dy, a.ld_dy, yf) && alike(s, a.ld_s, sf) && alike(ds, a.ld_ds, sf) &&
+        alike(dx, a.ld_dx, sf) &&
+        shift_rows(D.rows, D.d, bwd_row_bytes(D.d, per_elem, Rows::kShift)))
+      how = Rows::kShift;
+    if (how == Rows::kAny) a.nvec = (a.d + 255) / 256 * 32;
+    a.ld8 = static_cast<int>(step & 7);
+    const int64_t row_bytes = bwd_row_bytes(D.d, per_elem, how);
+    grid = bwd_shape(D.rows, D.d, how, row_bytes).blocks;
+    auto run = [&](auto Y, auto S) {
+      constexpr bool y = decltype(Y)::value, f = decltype(S)::value;
+      if (how == Rows::kVec) return bwd_launch<y, f, Rows::kVec>(a, row_bytes, st);
+      if (how == Rows::kShift) return bwd_launch<y, f, Rows::kShift>(a, row_bytes, st);
+      return bwd_launch<y, f, Rows::kAny>(a, row_bytes, st);
+    };
+    if (yf) e = sf ? run(std::true_type(), std::true_type()) : run(std::true_type(), std::false_type());
+    else e = sf ? run(std::false_type(), std::true_type()) : run(std::false_type(), std::false_type());
   }
   if (e != cudaSuccess || !dweight) return e;
   return launch_column_sum(part, grid, D.d, dweight, D.accumulate != 0, st);

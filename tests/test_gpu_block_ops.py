@@ -150,6 +150,38 @@ def test_add_rmsnorm_backward(rows, d, yt, st, wt, skip, pad):
     close(dw, dw0, magw * (2 * rows + 2 * d + 32) * U32)
 
 
+@pytest.mark.parametrize("rows,d", [(1, 513), (40, 515), (9, 16376), (1300, 2373), (2600, 1001),
+                                    (3000, 644), (7, 16381), (1217, 4094)])
+@pytest.mark.parametrize("yt,st,skip", [(BF16, BF16, True), (F32, BF16, False), (BF16, F32, True),
+                                        (F32, F32, True)])
+@pytest.mark.parametrize("lds", [(0, 0, 0, 0), (8, 0, 16, 24), (4, 0, 0, 4), (1, 1, 1, 1),
+                                 (0, 3, 0, 0)])
+def test_add_rmsnorm_backward_rows_at_a_shift(rows, d, yt, st, skip, lds):
+    """Rows whose beginnings are alike in every tensor, or not; NaN between the rows
+    of the inputs and nothing written between those of dx."""
+    def strided(seed, pad, dtype, scale=1.0):
+        t = torch.full((rows, d + pad), math.nan, dtype=dtype, device="cuda")
+        t[:, :d] = randn(seed, rows, d, dtype=dtype, scale=scale)
+        return t[:, :d]
+    dy, s = strided(21, lds[0], yt), strided(22, lds[1], st, 3.0)
+    ds = strided(23, lds[2], st) if skip else None
+    w = randn(24, d, dtype=F32)
+    buf = torch.full((rows, d + lds[3]), 7.0, dtype=st, device="cuda")
+    dx, dw = api.add_rmsnorm_backward(dy, s, w, ds, eps=1e-5, dx=buf[:, :d])
+    assert (buf[:, d:] == 7).all()
+    dx0, dw0 = ref.add_rmsnorm_backward(dy, s, w, ds, 1e-5)
+    v = s.to(F64)
+    rstd = (v.pow(2).mean(1, keepdim=True) + 1e-5).rsqrt()
+    gw = (dy.to(F64) * w.to(F64)).abs()
+    mag = rstd * (gw + (v * rstd).abs() * (gw * (v * rstd).abs()).mean(1, keepdim=True))
+    if ds is not None:
+        mag = mag + ds.to(F64).abs()
+    close(dx, dx0, dx0.abs() * 1.01 * ref.rounding(st) + mag * (4 * d + 32) * U32)
+    magw = (dy.to(F64) * v * rstd).abs().sum(0)
+    close(dw, dw0, magw * (2 * rows + 2 * d + 32) * U32)
+    assert torch.equal(dw, api.add_rmsnorm_backward(dy, s, w, ds, eps=1e-5, dx=buf[:, :d])[1])
+
+
 def test_add_rmsnorm_backward_accumulates_and_repeats():
     dy, s, ds = randn(25, 1000, 2880), randn(26, 1000, 2880), randn(27, 1000, 2880)
     w = randn(28, 2880, dtype=F32)
