@@ -404,16 +404,18 @@ typedef struct mok_rmsnorm_desc {
  * and the pointer s may be NULL.  s: the sum in fp32, rounded once to s_elem;
  * the norm reads s as it is stored, so that the backward, which gets the
  * stored s, differentiates the very function that ran.  s may equal residual
- * or x (same strides).  Statistics in fp32.
+ * or x (same strides).  Statistics in fp32, for values and codes in pairs of
+ * fp32 (some 48 bits).
  * Outputs, each optional but one of y, values, codes needed:
  *   y       bf16 [rows,d] (stride ld_y): the norm rounded once
  *   values  bf16 [rows,d] contiguous: the values of its MXFP8 form
  *   codes, scales  uint8 [rows,d] E4M3 codes and [rows,d/32] E8M0 bytes, both
  *           or neither: the MXFP8 form by mok_mx_quantize's rule (along rows),
- *           of the fp32 norm; what mok_gemm_mxfp8 takes
+ *           of the norm before any rounding; what mok_gemm_mxfp8 takes
  * d a multiple of 32 for values and codes.  Any pointer aligned to its
  * element and any row stride >= d is taken; 16-byte aligned rows with d a
- * multiple of 8 run at full width. */
+ * multiple of 8 run at full width (backward: also rows of other lengths in
+ * 16-byte aligned tensors whose strides agree modulo 8). */
 mok_status mok_add_rmsnorm_forward(const mok_rmsnorm_desc* desc, const void* x,
                                    const void* residual, const void* weight, void* s, void* y,
                                    void* values, uint8_t* codes, uint8_t* scales, void* stream);

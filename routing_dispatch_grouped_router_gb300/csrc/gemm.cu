@@ -2730,7 +2730,12 @@ cudaError_t launch_router_logits(const Dims& D, const void* x, const void* w_rou
 
 // ---------------------------------------------------- the dense product --
 
+// K blocks (times the parts of A) up to which a plain epilogue is the wide one, 64
+// fp32 or 128 bf16 columns at a time: dx of a router, 16384 x 4096 from 128 experts
+// (two blocks of three parts), 76 us in chunks of 32 columns and 61 so.  With more
+// the products cover the stores, and the wide form's staging costs a stage.
 constexpr int kWideKb = 8;
+
 
 // fp32 or bf16 C or z in 32 x 32 blocks; wide: bf16 in 32 x 64 ones
 static bool make_lin_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, bool f32,
