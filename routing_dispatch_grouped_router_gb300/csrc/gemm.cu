@@ -2731,10 +2731,11 @@ cudaError_t launch_router_logits(const Dims& D, const void* x, const void* w_rou
 // ---------------------------------------------------- the dense product --
 
 // K blocks (times the parts of A) up to which a plain epilogue is the wide one, 64
-// fp32 or 128 bf16 columns at a time: dx of a router, 16384 x 4096 from 128 experts
-// (two blocks of three parts), 76 us in chunks of 32 columns and 61 so.  With more
-// the products cover the stores, and the wide form's staging costs a stage.
-constexpr int kWideKb = 8;
+// fp32 or 128 bf16 columns at a time.  8192 x 7168, chunks of 32 columns and wide:
+// fp32 of one block 51.0 and 46.3 us, of eight 66.7 and 64.3; bf16 of one block
+// 33.1 and 30.3, of four 41.1 and 38.5, of eight 47.5 and 50.1, of twelve 56.9 and
+// 64.2.  (dx of a router, 16384 x 4096 fp32 from 128 experts: 70 and 60.)
+constexpr int wide_blocks(bool f32) { return f32 ? 8 : 4; }
 
 
 // fp32 or bf16 C or z in 32 x 32 blocks; wide: bf16 in 32 x 64 ones
@@ -2773,7 +2774,7 @@ static cudaError_t dense_linear(const char* name, const CUtensorMap& ta, const v
   const bool plain = !a.bias && !a.res && a.act == MOK_ACT_NONE && !a.store_z &&
                      !linear_direct(EPI);
   // short K: the stores set the pace (and an fp32 result is one accumulation)
-  const bool wide = pair && plain && a.num_kb * parts <= kWideKb &&
+  const bool wide = pair && plain && a.num_kb * parts <= wide_blocks(EPI == EPI_LIN_F32) &&
                     (EPI != EPI_LIN_F32 || a.num_kb <= a.chunk_kb);
   CUtensorMap tc = ta;
   if (!linear_direct(EPI) &&
