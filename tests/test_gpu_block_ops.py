@@ -53,6 +53,30 @@ def test_add_rmsnorm(rows, d, xt, st, wt, pad):
     close(y, y0, y0.abs() * (1.01 * U16 + (2 * d + 16) * U32) + 1e-30)
 
 
+@pytest.mark.parametrize("rows,d", [(1, 65), (40, 67), (9, 16376), (700, 2373), (3000, 130),
+                                    (7, 16381), (1217, 4094), (8, 1001)])
+@pytest.mark.parametrize("xt,st,wt", [(BF16, BF16, F32), (F32, BF16, BF16), (BF16, F32, F32),
+                                      (F32, F32, BF16)])
+@pytest.mark.parametrize("lds", [(0, 0, 0, 0), (8, 0, 16, 24), (4, 0, 0, 4), (1, 1, 1, 1),
+                                 (0, 3, 0, 0)])
+def test_add_rmsnorm_strided_rows(rows, d, xt, st, wt, lds):
+    """Strides of their own: NaN between the rows of the inputs, and nothing written
+    between those of s and y."""
+    def strided(seed, pad, dtype):
+        t = torch.full((rows, d + pad), math.nan, dtype=dtype, device="cuda")
+        t[:, :d] = randn(seed, rows, d, dtype=dtype)
+        return t[:, :d]
+    x, r = strided(1, lds[0], xt), strided(2, lds[1], st)
+    w = randn(3, d, dtype=wt)
+    sb = torch.full((rows, d + lds[2]), 7.0, dtype=st, device="cuda")
+    yb = torch.full((rows, d + lds[3]), 7.0, dtype=BF16, device="cuda")
+    s, y = api.add_rmsnorm(x, w, r, eps=1e-5, s=sb[:, :d], y=yb[:, :d])
+    assert (sb[:, d:] == 7).all() and (yb[:, d:] == 7).all()
+    s0, y0 = ref.add_rmsnorm(x, w, r, 1e-5)
+    assert torch.equal(s, s0)
+    close(y, y0, y0.abs() * (1.01 * U16 + (2 * d + 16) * U32) + 1e-30)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_rmsnorm_without_residual(dtype):
     x = randn(4, 37, 2048, dtype=dtype)
