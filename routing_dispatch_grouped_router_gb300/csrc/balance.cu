@@ -11,8 +11,8 @@
 // stay in registers, then shared memory, then per-block partials that a second
 // kernel (launched while the first drains) adds in block order: no
 // floating-point atomics.  (256 tokens of 8 experts: 4.7 us, one launch; 16384 of
-// 128: 11.5 us, of which the sum 4, floor 1.3; the backward of 8192 of 384: 8.1 us,
-// 3.1 TB/s of logits and gradients, which L2 mostly holds; floor 3.7.)
+// 128: 11.5 us, of which the sum 4, floor 1.3; the backward of 8192 of 384: 8.5 us,
+// 3.0 TB/s of logits and gradients, which L2 mostly holds; floor 3.7.)
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -385,14 +385,22 @@ __global__ void __launch_bounds__(kBwdThreads, 4) balance_bwd_kernel(BalBwd a, i
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       clean(l[u]);
+      // P = exp(l - lse) / its sum over the row: lse's rounding (1e-3 at 1e4; from
+      // 1e8 on all of log E) shifts every term of a row alike, and without the
+      // division the row would not sum to 1
       some[u] = some[u] && lse[u] > -INFINITY;
-      float dot = 0.f;
+      float sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 0; i < 4 * NJ; ++i) {
         l[u][i] = some[u] ? expf(l[u][i] - lse[u]) : 0.f;
+        sum += l[u][i];
         dot = fmaf(f[i], l[u][i], dot);
       }
-      dot = group_sum<L>(dot);
+      sum = group_sum<L>(sum);  // (about 1: the quick division's 2 ulp, and no spills)
+      const float inv = sum > 0.f ? __fdividef(1.0f, sum) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NJ; ++i) l[u][i] *= inv;
+      dot = group_sum<L>(dot) * inv;
       const float c = some[u] ? Z * lse[u] - dot : 0.f;
       float* row = a.dlogits + (base + u * step + grp) * a.ld;
 #pragma unroll

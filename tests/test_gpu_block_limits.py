@@ -1,0 +1,80 @@
+"""The operators around the layer where a first form of them went wrong: logits
+far from zero.
+Bounds as in _block_ref.py, and as derived at each test."""
+import math
+
+import pytest
+import torch
+
+import _block_ref as ref
+from _block_ref import F64, U32
+from routing_dispatch_grouped_router_gb300 import api
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def randn(seed, *shape, dtype=BF16, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def within(got, want, bound):
+    """|got - want| <= bound everywhere; the largest excess otherwise."""
+    d = (got.to(F64) - want).abs() - bound
+    assert torch.isfinite(got).all()
+    assert d.max().item() <= 0, (d.max().item(), (got.to(F64) - want).abs().max().item())
+
+
+# ---------------------------------------------------------- router_balance --
+
+@pytest.mark.parametrize("T,E,k", [(60, 40, 4), (33, 8, 2), (50, 130, 8), (9, 512, 8), (40, 17, 1),
+                                   (21, 300, 3)])
+@pytest.mark.parametrize("offset", [0.0, 1e4, -1e4, 3e6, -1e8, -3e37])
+def test_balance_gradient_of_rows_far_from_zero(T, E, k, offset):
+    """A row's softmax does not change with an offset of all its logits, however
+    large its lse: every other row of the batch is moved far away."""
+    l = randn(1000 + T, T, E, dtype=F32)
+    l[::2] += offset
+    idx = torch.topk(l, k, 1).indices.to(torch.int32)
+    check_gradient(l, idx, None, 0.5, 1e-3)
+
+
+def check_gradient(l, idx, mask, a, b):
+    T, E = l.shape
+    u = torch.tensor([1.25, -0.75], device="cuda")
+    _, counts, prob, lse, n = api.router_balance(l, idx, mask, balance_coef=a, z_coef=b)
+    dl = api.router_balance_backward(u, l, lse, counts, n, idx.shape[1], mask, balance_coef=a,
+                                     z_coef=b)
+    _, counts0, prob0, lse0, n0, p, m, f, some = ref.router_balance(l, idx, mask, a, b)
+    assert torch.equal(counts, counts0)
+    x = torch.where(some[:, None], l.to(F64), torch.zeros_like(l, dtype=F64))
+    # softmax: E positive terms; an exponential of l - max (one rounding of an
+    # argument that matters down to -104), for each row by itself
+    far = (x - x.amax(1, keepdim=True)).abs().clamp(max=104.0).amax(1, keepdim=True)
+    soft = (2 * E + 4 * far + 64) * U32
+    within(prob, prob0, prob0 * (soft.amax() + 2 * T * U32) + 1e-30)
+    dl0 = ref.router_balance_backward(u, l, idx, mask, a, b)
+    z0 = torch.where(some, lse0, torch.zeros_like(lse0)).abs()[:, None]
+    mag = p * (1.25 * a * E * (f + (p @ f)[:, None] + 1.0 / E) + 0.75 * 2 * b * z0) / max(n0, 1)
+    within(dl, dl0, mag * (2 * soft + (4 * E + 64) * U32) + 1e-30)
+    return dl
+
+
+def test_balance_gradient_of_rows_of_the_lowest_value():
+    """Rows masked with the type's lowest value, whole or in part, with and
+    without the z loss in the gradient."""
+    low = torch.finfo(F32).min
+    l = randn(1100, 64, 40, dtype=F32)
+    l[3] = low
+    l[5, :36] = low
+    l[8] = low / 2
+    l[9, 1:] = -math.inf
+    l[11] = -math.inf
+    idx = torch.topk(l, 4, 1).indices.to(torch.int32)
+    for b in (0.0, 1e-3):
+        dl = check_gradient(l, idx, None, 0.5, b)
+        assert (dl[11] == 0).all()
+    mask = torch.ones(64, dtype=torch.uint8, device="cuda")
+    mask[5:9] = 0
+    assert (check_gradient(l, idx, mask, 0.5, 0.0)[5:9] == 0).all()
