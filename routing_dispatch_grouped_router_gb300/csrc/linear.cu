@@ -721,15 +721,19 @@ struct Dz8<false, true> {
 // dz = dy act'(z) as the sum of bf16 parts (each the rounding of what those
 // before it leave), and its column sums over the block's rows.  A block takes
 // kDzRows rows by 8 * `lanes` columns, a lane 8 columns of every 256/lanes-th
-// row, in batches of four rows whose loads are in flight together.
+// row, in batches of four rows whose loads are in flight together.  The blocks of
+// a grid of one dimension go round the `cols` column blocks first (two million
+// tokens are more row blocks than a second dimension holds).
 template <bool F32, bool VEC, int ACT>
-__global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
+__global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes, int cols) {
   __shared__ float s_sum[256 * 9];
   grid_dep_launch();
   grid_dep_wait();
   const int l = threadIdx.x & (lanes - 1), row0 = threadIdx.x / lanes, rows = 256 / lanes;
-  const int c = (blockIdx.x * lanes + l) * 8;
-  const long long r0 = static_cast<long long>(blockIdx.y) * kDzRows;
+  const int col_block = blockIdx.x % cols;
+  const long long row_block = blockIdx.x / cols;
+  const int c = (col_block * lanes + l) * 8;
+  const long long r0 = row_block * kDzRows;
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
@@ -784,11 +788,11 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a, int lanes) {
   for (int j = 0; j < 8; ++j) s_sum[(row0 * lanes + l) * 9 + j] = sum[j];
   __syncthreads();
   for (int i = threadIdx.x; i < lanes * 8; i += 256) {
-    const int col = blockIdx.x * lanes * 8 + i;
+    const int col = col_block * lanes * 8 + i;
     if (col >= a.N) break;
     float t = 0.f;
     for (int r = 0; r < rows; ++r) t += s_sum[(r * lanes + (i >> 3)) * 9 + (i & 7)];
-    a.part[static_cast<long long>(blockIdx.y) * a.N + col] = t;
+    a.part[row_block * a.N + col] = t;
   }
 }
 
@@ -1079,14 +1083,14 @@ cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const vo
     a.n_pad = static_cast<int>(W.n_pad);
     // lanes of a row: 8 columns each, up to a warp
     const int lanes = W.n_pad >= 256 ? 32 : (W.n_pad > 64 ? 16 : 8);
-    const dim3 grid(static_cast<unsigned>((W.n_pad + lanes * 8 - 1) / (lanes * 8)),
-                    static_cast<unsigned>(W.bias_rows));
+    const int64_t cols = (W.n_pad + lanes * 8 - 1) / (lanes * 8);
+    const dim3 grid(static_cast<unsigned>(cols * W.bias_rows));
     ProfScope prof("linear_dz", st);
     cudaError_t e = cudaSuccess;
     auto run = [&](auto F, auto V, auto A) {
       e = launch_dependent(
           linear_dz_kernel<decltype(F)::value, decltype(V)::value, decltype(A)::value>, grid,
-          dim3(256), 0, st, a, lanes);
+          dim3(256), 0, st, a, lanes, static_cast<int>(cols));
     };
     auto by_act = [&](auto F, auto V) {
       if (D.act == MOK_ACT_NONE) run(F, V, std::integral_constant<int, MOK_ACT_NONE>());

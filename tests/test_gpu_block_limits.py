@@ -1,5 +1,5 @@
 """The operators around the layer where a first form of them went wrong: logits
-far from zero.
+far from zero, tensors of more rows than one grid dimension holds.
 Bounds as in _block_ref.py, and as derived at each test."""
 import math
 
@@ -78,3 +78,24 @@ def test_balance_gradient_of_rows_of_the_lowest_value():
     mask = torch.ones(64, dtype=torch.uint8, device="cuda")
     mask[5:9] = 0
     assert (check_gradient(l, idx, mask, 0.5, 0.0)[5:9] == 0).all()
+
+
+# ----------------------------------------------------------------- linear --
+
+@pytest.mark.parametrize("act,dyt,bias", [("none", F32, True), ("silu", BF16, False)])
+def test_linear_backward_of_two_million_tokens(act, dyt, bias):
+    """More than 65535 blocks of 32 rows: dz, its column sums and products."""
+    M, N, K = 65535 * 32 + 33, 8, 8
+    x, w = randn(1200, M, K), randn(1201, N, K)
+    dy, z = randn(1202, M, N, dtype=dyt), randn(1203, M, N, dtype=dyt)
+    dx, dw, db = api.linear_backward(dy, x, w, z, act=act, bias=bias, dx_dtype=F32)
+    assert api.device_status(api.operator_status()) == 0
+    (dx0, dw0, db0), (mx, mw, mb) = ref.linear_backward(dy, x, w, z, act)
+    dza = dy.to(F64).abs() * (0.0 if act == "none" else 64 * U32)
+    within(dx, dx0, mx * (6 * N + 1) * U32 + dza @ w.to(F64).abs() + 1e-30)
+    # 36 products to an accumulation, then sums in fp32 over the chunks of a split
+    # and over the splits: errors that do not line up, so well below M U32
+    rms = lambda t: t.pow(2).mean().sqrt().item()  # noqa: E731
+    assert rms(dw.to(F64) - dw0) <= 1e-4 * rms(dw0)
+    if bias:
+        assert rms(db.to(F64) - db0) <= 1e-4 * rms(db0)
