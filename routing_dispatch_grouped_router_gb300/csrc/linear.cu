@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kFewThreads)
   }
 }
 
-// grid (K splits = the cluster, feature tiles, token tiles)
+// grid (feature tiles x K splits, a tile's splits being its cluster; token tiles)
 template <int BN, bool F32, int KS>
 __global__ void __launch_bounds__(kLinThreads)
     linear_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(kLinThreads)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int ks = KS;  // = gridDim.x, the cluster
-  const int split = blockIdx.x;
-  const int n0 = blockIdx.y * 128, m0 = blockIdx.z * BN;
+  constexpr int ks = KS;  // the cluster
+  const int split = blockIdx.x % ks;
+  const int n0 = blockIdx.x / ks * 128, m0 = blockIdx.y * BN;
   const int kb0 = static_cast<int>(static_cast<long long>(args.nkb) * split / ks);
   const int kb1 = static_cast<int>(static_cast<long long>(args.nkb) * (split + 1) / ks);
 
@@ -471,7 +471,6 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
       !make_tensor_map_2d(&tx, bf, 2, x, D.K, D.M, D.ld_x, 64, BN, sw))
     return cudaErrorInvalidValue;
   const int64_t nt = (D.N + 127) / 128, mt = (D.M + BN - 1) / BN;
-  if (nt > 65535 || mt > 65535) return cudaErrorInvalidConfiguration;
   // K splits: a power of two, as many as the CTAs that fit at once leave room
   // for, at least four 64-value blocks each
   const int64_t slots = 2LL * num_sms_current_device();
@@ -492,8 +491,7 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(ks), static_cast<unsigned>(nt),
-                     static_cast<unsigned>(mt));
+  cfg.gridDim = dim3(static_cast<unsigned>(ks * nt), static_cast<unsigned>(mt));
   cfg.blockDim = dim3(kLinThreads, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = st;

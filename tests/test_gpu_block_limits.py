@@ -1,13 +1,13 @@
 """The operators around the layer where a first form of them went wrong: logits
-far from zero, tensors of more rows than one grid dimension holds.
-Bounds as in _block_ref.py, and as derived at each test."""
+far from zero, tensors of more rows or features than one grid dimension
+holds.  Bounds as in _block_ref.py, and as derived at each test."""
 import math
 
 import pytest
 import torch
 
 import _block_ref as ref
-from _block_ref import F64, U32
+from _block_ref import F64, U16, U32
 from routing_dispatch_grouped_router_gb300 import api
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +99,16 @@ def test_linear_backward_of_two_million_tokens(act, dyt, bias):
     assert rms(dw.to(F64) - dw0) <= 1e-4 * rms(dw0)
     if bias:
         assert rms(db.to(F64) - db0) <= 1e-4 * rms(db0)
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 100])
+def test_linear_of_more_features_than_a_grid_dimension(M):
+    """N beyond 65535 tiles of 128 features, few tokens."""
+    N, K = 65535 * 128 + 130, 8
+    x, w = randn(1300, M, K), randn(1301, N, K)
+    y = api.linear(x, w)
+    assert api.device_status(api.operator_status()) == 0
+    for n0 in (0, 65534 * 128, N - 200):
+        n1 = min(n0 + 300, N)
+        y0, _, mag = ref.linear(x, w[n0:n1], None, "none", None)
+        within(y[:, n0:n1], y0, y0.abs() * 1.01 * U16 + mag * (2 * K + 8) * U32 + 1e-30)
