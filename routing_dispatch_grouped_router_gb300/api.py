@@ -200,9 +200,16 @@ def _ops():
 
 def operator_status(device=None):
     """The device int32 that the operators below report into (sticky: the
-    first error stays; read it with `device_status`, zero it to go on)."""
-    index = torch.cuda.current_device() if device is None else torch.device("cuda", device).index \
-        if isinstance(device, int) else torch.device(device).index
+    first error stays; read it with `device_status`, zero it to go on).  device:
+    an index, a CUDA device or its name; the current one where it says none."""
+    index = device
+    if device is not None and not isinstance(device, int):
+        d = torch.device(device)
+        if d.type != "cuda":
+            raise ValueError(f"the operators run on a CUDA device, not on {d}")
+        index = d.index
+    if index is None:
+        index = torch.cuda.current_device()
     word = _status_words.get(index)
     if word is None:
         word = torch.zeros(64, dtype=torch.int32, device=torch.device("cuda", index))

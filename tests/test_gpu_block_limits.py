@@ -112,3 +112,15 @@ def test_linear_of_more_features_than_a_grid_dimension(M):
         n1 = min(n0 + 300, N)
         y0, _, mag = ref.linear(x, w[n0:n1], None, "none", None)
         within(y[:, n0:n1], y0, y0.abs() * 1.01 * U16 + mag * (2 * K + 8) * U32 + 1e-30)
+
+
+# ------------------------------------------------------- status, arguments --
+
+def test_operator_status_is_one_word_however_the_device_is_named():
+    word = api.operator_status()
+    i = torch.cuda.current_device()
+    for name in ("cuda", f"cuda:{i}", i, torch.device("cuda"), torch.device("cuda", i)):
+        assert api.operator_status(name).data_ptr() == word.data_ptr()
+    for name in ("cpu", torch.device("cpu")):
+        with pytest.raises(ValueError):
+            api.operator_status(name)
