@@ -76,6 +76,13 @@ int64_t integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
+// (a tensor of several elements, for one, has no truth value)
+bool flag(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) PyErr_Clear();
+  TORCH_CHECK_VALUE(v >= 0, name, " must be true or false");
+  return v != 0;
+}
 
 // The stream of a call on the GPU of `t`, which must be the current one.
 struct Call {
@@ -286,7 +293,7 @@ PyObject* py_add_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     const at::Tensor& w = tensor(a[2], "weight");
     const at::Tensor* ds = tensor_or_null(a[3], "ds");
     const at::Tensor *dx0 = tensor_or_null(a[5], "dx"), *dw0 = tensor_or_null(a[6], "dweight");
-    const bool acc = PyObject_IsTrue(a[7]) == 1;
+    const bool acc = flag(a[7], "accumulate");
     const Call c(dy, a[9]);
     mok_rmsnorm_desc D = {};
     D.ld_x = matrix(dy, "dy", c.device);
@@ -448,7 +455,7 @@ PyObject* py_linear(PyObject*, PyObject* const* a, Py_ssize_t) {
     const at::Tensor* bias = tensor_or_null(a[2], "bias");
     const at::Tensor* res = tensor_or_null(a[4], "residual");
     const at::Tensor *y0 = tensor_or_null(a[6], "y"), *z0 = tensor_or_null(a[7], "z");
-    const bool keep = PyObject_IsTrue(a[8]) == 1;
+    const bool keep = flag(a[8], "keep_z");
     const Call c(x, a[10]);
     mok_linear_desc D = linear_desc(c, x, w, integer(a[3]));
     const at::ScalarType dt =
@@ -492,7 +499,7 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     const at::Tensor* z = act == MOK_ACT_NONE ? nullptr : tensor_or_null(a[3], "z");
     const at::Tensor *dx0 = tensor_or_null(a[7], "dx"), *dw0 = tensor_or_null(a[8], "dw"),
                      *db0 = tensor_or_null(a[9], "dbias");
-    const bool bias = PyObject_IsTrue(a[5]) == 1 || db0 != nullptr;
+    const bool bias = flag(a[5], "bias") || db0 != nullptr;
     const int64_t acc = integer(a[10]);
     const Call c(x, a[12]);
     mok_linear_desc D = linear_desc(c, x, w, act);

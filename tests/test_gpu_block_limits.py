@@ -124,3 +124,17 @@ def test_operator_status_is_one_word_however_the_device_is_named():
     for name in ("cpu", torch.device("cpu")):
         with pytest.raises(ValueError):
             api.operator_status(name)
+
+
+def test_arguments_without_a_truth_value():
+    """A tensor of several elements for a flag raises ValueError, and no call is made."""
+    x, w, b = randn(1500, 4, 64), randn(1501, 8, 64), torch.zeros(8, device="cuda")
+    ones, dy = torch.ones(64, device="cuda"), randn(1502, 4, 8)
+    dw = torch.zeros(64, device="cuda")
+    for call in (lambda: api.linear(x, w, keep_z=b),
+                 lambda: api.linear_backward(dy, x, w, bias=b),
+                 lambda: api.add_rmsnorm_backward(x, x, ones, dweight=dw, accumulate=b)):
+        with pytest.raises(ValueError):
+            call()
+    torch.cuda.synchronize()
+    assert (dw == 0).all()
