@@ -960,7 +960,10 @@ template <bool DYF32, bool SF32, int NV, bool SHIFT>
 cudaError_t bulk_launch(const NormBwd& a, const BwdShape& b, int64_t row_bytes, cudaStream_t st) {
   auto kern = add_rmsnorm_bwd_bulk_kernel<DYF32, SF32, NV, SHIFT>;
   const int smem = static_cast<int>(b.depth * row_bytes);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit is the kernel's, not the call's: the most that any call takes, so
+  // that no host thread lowers it between another's setting and launch)
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);

@@ -1,14 +1,17 @@
 """The operators around the layer where a first form of them went wrong: logits
-far from zero, tensors of more rows or features than one grid dimension
-holds.  Bounds as in _block_ref.py, and as derived at each test."""
+far from zero, tensors of more rows or features than one grid dimension holds,
+calls from several host threads.  Bounds as in _block_ref.py, and as derived at
+each test."""
+import ctypes
 import math
+import threading
 
 import pytest
 import torch
 
 import _block_ref as ref
 from _block_ref import F64, U16, U32
-from routing_dispatch_grouped_router_gb300 import api
+from routing_dispatch_grouped_router_gb300 import _lib, api
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -138,3 +141,44 @@ def test_arguments_without_a_truth_value():
             call()
     torch.cuda.synchronize()
     assert (dw == 0).all()
+
+
+# ------------------------------------------------------------ host threads --
+
+def test_norm_backward_from_several_host_threads():
+    """The C entry from three threads at once, each with a width and a stream of its
+    own: no call fails, and every result is the call's alone."""
+    lib = _lib.load()
+    fail, result = [], {}
+    jobs = {}
+    for i, d in enumerate((1024, 7168, 2048)):
+        dy, s, w = randn(1400 + i, 64, d), randn(1410 + i, 64, d), randn(1420 + i, d, dtype=F32)
+        dx0, dw0 = api.add_rmsnorm_backward(dy, s, w)
+        desc = _lib.RmsnormDesc(rows=64, d=d, eps=1e-6, weight_elem=1)
+        n = ctypes.c_size_t()
+        assert lib.mok_add_rmsnorm_workspace_size(desc, n) == 0
+        ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+        jobs[d] = (desc, dy, s, w, torch.zeros_like(dx0), torch.zeros_like(dw0), ws, dx0, dw0,
+                   torch.cuda.Stream())
+    torch.cuda.synchronize()
+    go = threading.Barrier(len(jobs))
+
+    def work(d):
+        desc, dy, s, w, dx, dw, ws, _, _, st = jobs[d]
+        go.wait()
+        for _ in range(4000):
+            rc = lib.mok_add_rmsnorm_backward(
+                desc, dy.data_ptr(), s.data_ptr(), w.data_ptr(), None, dx.data_ptr(),
+                dw.data_ptr(), ws.data_ptr(), ws.numel(), None, st.cuda_stream)
+            if rc != 0:
+                fail.append((d, rc))
+
+    threads = [threading.Thread(target=work, args=(d,)) for d in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not fail, (len(fail), fail[:4])
+    for d, (_, _, _, _, dx, dw, _, dx0, dw0, _) in jobs.items():
+        assert torch.equal(dx, dx0) and torch.equal(dw, dw0), d
