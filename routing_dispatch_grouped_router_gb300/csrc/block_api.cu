@@ -13,7 +13,13 @@ namespace {
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool elem_ok(int32_t e) { return e == MOK_ELEM_BF16 || e == MOK_ELEM_F32; }
 size_t elem_size(int32_t e) { return e == MOK_ELEM_F32 ? 4 : 2; }
-mok_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA; }
+// (a refused launch also stays as the thread's last error, which the next call of
+// another library would take for its own)
+mok_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOK_OK;
+  cudaGetLastError();
+  return MOK_ERR_CUDA;
+}
 
 // A row stride: 0 stands for `cols`; less than a row is wrong.
 bool stride(int64_t* ld, int64_t cols) {

@@ -182,3 +182,35 @@ def test_norm_backward_from_several_host_threads():
     assert not fail, (len(fail), fail[:4])
     for d, (_, _, _, _, dx, dw, _, dx0, dw0, _) in jobs.items():
         assert torch.equal(dx, dx0) and torch.equal(dw, dw0), d
+
+
+def test_a_refused_launch_leaves_no_pending_error():
+    """A call that the runtime refuses (here: its stream's capture has been
+    invalidated) says so in its status; the runtime's error does not wait for the
+    next call of the process."""
+    lib = _lib.load()
+    stream = ctypes.c_void_p()
+    assert lib.cudaStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
+    x, w = randn(1510, 4, 64), torch.ones(64, device="cuda")
+    y = torch.empty_like(x)
+    wl, out = randn(1511, 8, 64), torch.empty(4, 8, dtype=BF16, device="cuda")
+    torch.cuda.synchronize()
+    try:
+        assert lib.cudaStreamBeginCapture(stream, 2) == 0  # relaxed: this stream alone
+        assert lib.cudaStreamSynchronize(stream) != 0      # not allowed in a capture: ends it
+        lib.cudaGetLastError()
+        norm = _lib.RmsnormDesc(rows=4, d=64, eps=1e-6, weight_elem=1)
+        assert lib.mok_add_rmsnorm_forward(norm, x.data_ptr(), None, w.data_ptr(), None,
+                                           y.data_ptr(), None, None, None, stream) == 4
+        assert lib.cudaPeekAtLastError() == 0
+        lin = _lib.LinearDesc(M=4, N=8, K=64)
+        assert lib.mok_linear_forward(lin, x.data_ptr(), wl.data_ptr(), None, None, out.data_ptr(),
+                                      None, None, 0, None, stream) == 4
+        assert lib.cudaPeekAtLastError() == 0
+    finally:
+        graph = ctypes.c_void_p()
+        lib.cudaStreamEndCapture(stream, ctypes.byref(graph))
+        lib.cudaStreamDestroy(stream)
+        lib.cudaGetLastError()
+    torch.cuda.synchronize()
+    assert torch.equal(api.add_rmsnorm(x, w)[1], api.add_rmsnorm(x, w)[1])
