@@ -404,8 +404,8 @@ typedef struct mok_rmsnorm_desc {
  * and the pointer s may be NULL.  s: the sum in fp32, rounded once to s_elem;
  * the norm reads s as it is stored, so that the backward, which gets the
  * stored s, differentiates the very function that ran.  s may equal residual
- * or x (same strides).  Statistics in fp32, for values and codes in pairs of
- * fp32 (some 48 bits).
+ * or x (same strides).  Statistics in fp32; for values and codes statistics
+ * and norm in pairs of fp32, to within 2^-42 of the norm.
  * Outputs, each optional but one of y, values, codes needed:
  *   y       bf16 [rows,d] (stride ld_y): the norm rounded once
  *   values  bf16 [rows,d] contiguous: the values of its MXFP8 form

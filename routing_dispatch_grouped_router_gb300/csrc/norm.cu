@@ -7,7 +7,7 @@
 //
 // Bound by HBM bytes: a row is read once, kept in registers across the row
 // reductions and written once.  (8192 x 7168 to MXFP8, fp32 into a bf16 stream:
-// 102 us, 6.4 TB/s; backward of 16384 x 4096 fp32: 161.5 us, 6.7 TB/s; a copy runs
+// 106 us, 6.1 TB/s; backward of 16384 x 4096 fp32: 161.5 us, 6.7 TB/s; a copy runs
 // at 6.8.  4099 x 2880 bf16 backward: 22.7 us, floor 13.9, a third of it the ramp
 // of a few rows per block and the column sums' kernel.)
 #include <cuda_bf16.h>
@@ -248,6 +248,34 @@ __device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
   s.lo += a.lo + b.lo;
   return s;  // (an infinite sum has a low part that is no number: row_rstd drops it)
 }
+// The sum of a thread's squares as a pair.  The sum starts at a power of two that
+// no square exceeds, so that hi - s is exact at every step and the second fused
+// product gives what the step rounded away, the square's own low bits with it; it
+// is taken off in the end, exactly.  (A general error-free addition takes twice the
+// instructions: 8192 x 7168 109.9 us so.)  plain: their sum in fp32, for squares
+// near or past the end of its range.
+template <int N>
+__device__ __forceinline__ Pair sum_squares(const float (&v)[N][8], float plain) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
+  top = __fmul_rn(top, top);
+  if (!(top < 0x1p120f)) return {plain, 0.f};
+  const float c = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + 0x00800000u);
+  Pair s = {c, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float hi = __fmaf_rn(v[i][j], v[i][j], s.hi);
+      s.lo = __fadd_rn(s.lo, __fmaf_rn(v[i][j], v[i][j], __fsub_rn(s.hi, hi)));
+      s.hi = hi;
+    }
+  s.hi = __fsub_rn(s.hi, c);
+  return s;  // (a NaN is not in `top`, but in both sums)
+}
 __device__ __forceinline__ Pair warp_sum(Pair v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
@@ -260,6 +288,9 @@ __device__ __forceinline__ Pair row_rstd(Pair sum, float d, float eps) {
   const float q = __fdiv_rn(sum.hi, d);
   Pair v = two_sum(q, eps);
   v.lo += (fmaf(-q, d, sum.hi) + sum.lo) / d;
+  // the low parts of many terms may add up: hi once more the nearest value, so
+  // that the Newton step starts from rsqrtf's error alone (no number: see above)
+  if (fabsf(v.lo) < INFINITY) v = two_sum(v.hi, v.lo);
   const float r = rsqrtf(v.hi);
   const float h = v.hi * r, l = fmaf(v.hi, r, -h) + v.lo * r;
   const float e = fmaf(-h, r, 1.0f) - l * r;
@@ -365,10 +396,10 @@ __device__ __forceinline__ void mx_store(const NormFwd& a, long long r, int v, b
 
 // One row per threadIdx.y; blockDim.x threads of whole warps hold it, NV
 // vectors each.  MX: mean square and norm are formed in pairs of fp32 and the norm
-// rounded to odd, so that codes and values are the roundings of the exact norm;
-// a plain fp32 norm lands on the wrong side of an E4M3 boundary about once in a
-// million values, an eighth of the value each time (8192 x 7168: 96.5 us from
-// plain fp32, 102.8 us so).
+// rounded to odd: codes and values are the roundings of the norm to within 2^-42 of
+// it, the exact one's unless it lies that near a boundary.  A plain fp32 norm lands
+// on the wrong side of an E4M3 boundary about once in a million values, an eighth of
+// the value each time (8192 x 7168: 96.5 us from plain fp32, 105.9 us so).
 template <bool XF32, bool SF32, bool VEC, int NV, bool MX>
 __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormFwd a) {
   __shared__ float red[3][32];
@@ -410,13 +441,10 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) add_rmsnorm_kernel(NormF
     for (int j = 0; j < 8; ++j) sq[j] = fmaf(v[i][j], v[i][j], sq[j]);
   }
   const float df = static_cast<float>(a.d);
-  float sum = warp_sum(((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7])));
-  Pair sum2 = {sq[0], 0.f};
-  if (MX) {
-#pragma unroll
-    for (int j = 1; j < 8; ++j) sum2 = pair_add(sum2, {sq[j], 0.f});
-    sum2 = warp_sum(sum2);
-  }
+  float sum = ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
+  Pair sum2 = {0.f, 0.f};
+  if (MX) sum2 = warp_sum(sum_squares<NV>(v, sum));
+  sum = warp_sum(sum);
   if (tpr > 32) {  // one row per block
     if ((t & 31) == 0) {
       red[0][t >> 5] = sum;

@@ -1,7 +1,7 @@
 """The operators around the layer where a first form of them went wrong: logits
 far from zero, tensors of more rows or features than one grid dimension holds,
-calls from several host threads.  Bounds as in _block_ref.py, and as derived at
-each test."""
+norms beside a rounding boundary of E4M3, calls from several host threads.  Bounds
+as in _block_ref.py, and as derived at each test."""
 import ctypes
 import math
 import threading
@@ -214,3 +214,59 @@ def test_a_refused_launch_leaves_no_pending_error():
         lib.cudaGetLastError()
     torch.cuda.synchronize()
     assert torch.equal(api.add_rmsnorm(x, w)[1], api.add_rmsnorm(x, w)[1])
+
+
+# ------------------------------------------------------- precision of MXFP8 --
+
+# The MXFP8 form of the norm: mean square, reciprocal root and products in pairs
+# of fp32.  The root's Newton step leaves 3/8 of the square of rsqrtf's error
+# (2 ulp: 2^-22.4 relative, so 2^-46), each product and sum some 2^-46: in all below
+# 2^-42.  Codes and scales are those of the exact norm wherever no boundary of
+# theirs lies that near.
+MX_ERR = 2.0 ** -42
+
+
+def check_mx(x, w, eps, residual=None):
+    values = torch.empty(x.shape, dtype=BF16, device="cuda")
+    _, codes, scales = api.add_rmsnorm_mx(x, w, residual, eps=eps, values=values)
+    y0 = ref.add_rmsnorm(x, w, residual, eps)[1]
+    (lo, slo), (hi, shi) = (ref.mx_values(y0 * (1 + e)) for e in (-MX_ERR, MX_ERR))
+    sure, ssure = lo == hi, slo == shi
+    assert sure.double().mean().item() > 0.999 and ssure.double().mean().item() > 0.99
+    assert torch.equal(values.to(F64)[sure], lo[sure])
+    assert torch.equal(scales[ssure], slo[ssure])
+    assert torch.equal(values.to(F64), ref.decode(codes, scales))
+
+
+@pytest.mark.parametrize("d", [32, 96, 2880, 4096, 16384])
+@pytest.mark.parametrize("rows", [1, 700])
+def test_mx_codes_of_norms_beside_a_rounding_boundary(rows, d):
+    """Rows of one magnitude c: every square has the same rounding error in fp32.
+    eps puts the norm 1e-10 above or below the middle of two codes."""
+    b = 1.0625  # between the codes of 1 and 1.125
+    w1 = torch.nextafter(torch.tensor(b), torch.tensor(2.0)).item()
+    w = torch.full((d,), w1, device="cuda")
+    g = w1 / b - 1
+    sign = torch.where(randn(1600, rows, d, dtype=F32) < 0, -1.0, 1.0)
+    for c in (1.2345678, 0.7654321, 3.3333333, 1.1, 0.01234567):
+        c = torch.tensor(c, dtype=F32).item()
+        for delta in (1e-10, -1e-10):
+            eps = c * c * (((1 + g) / (1 + delta)) ** 2 - 1)
+            eps = torch.tensor(eps, dtype=F32).item()
+            x = sign * c
+            y0 = ref.add_rmsnorm(x, w, None, eps)[1].abs()
+            assert ((y0 / b - 1).abs() > MX_ERR).all() and ((y0 > b) == (delta > 0)).all()
+            check_mx(x, w, eps)
+
+
+@pytest.mark.parametrize("xt,st", [(F32, None), (BF16, F32), (F32, BF16), (BF16, BF16)])
+def test_mx_codes_are_the_exact_norm_s(xt, st):
+    """Eight million values of random rows, of which an fp32 norm rounds some eight
+    the other way; a part of them in rows of odd strides."""
+    x = randn(1700, 2048, 4096, dtype=xt)
+    r = None if st is None else randn(1701, 2048, 4096, dtype=st, scale=3.0)
+    w = 1 + randn(1702, 4096, dtype=F32, scale=0.1)
+    check_mx(x, w, 1e-6, r)
+    y = torch.empty(700, 4097, dtype=xt, device="cuda")[:, :4096]
+    y.copy_(x[:700])
+    check_mx(y, w, 1e-6, None if r is None else r[:700])
