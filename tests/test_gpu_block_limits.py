@@ -270,3 +270,30 @@ def test_mx_codes_are_the_exact_norm_s(xt, st):
     y = torch.empty(700, 4097, dtype=xt, device="cuda")[:, :4096]
     y.copy_(x[:700])
     check_mx(y, w, 1e-6, None if r is None else r[:700])
+
+
+# ------------------------------------------- precision of weight gradients --
+
+@pytest.mark.parametrize("M,N,K", [(16384, 128, 512), (4096, 256, 512), (12000, 130, 256),
+                                   (9000, 64, 512), (600, 40, 1032)])
+@pytest.mark.parametrize("act,dyt", [("none", F32), ("silu", BF16)])
+def test_linear_backward_keeps_fp32_accuracy_over_many_tokens(M, N, K, act, dyt):
+    """dw and an fp32 dx take all 24 bits of dz and few MMAs per accumulation.  A
+    truncating MMA costs a sum up to 1.7e-8 of it, 36 of them 6e-7 (half of that
+    on average, and less as the chunks' sums join: a chunk's error is relative to
+    the chunk); the sums in fp32 beside it some 3e-7, the slope's exponential up to
+    3e-7: in all 1.5e-6.  Two parts of dz alone would leave 2^-17 / sqrt(12) = 2.2e-6."""
+    x, w = randn(1800, M, K), randn(1801, N, K, scale=1 / math.sqrt(K))
+    dy, z = randn(1802, M, N, dtype=dyt), randn(1803, M, N, dtype=dyt)
+    dx, dw, _ = api.linear_backward(dy, x, w, z, act=act, dx_dtype=F32)
+    (dx0, dw0, _), _ = ref.linear_backward(dy, x, w, z, act)
+
+    def err(got, want):
+        return ((got.to(F64) - want).pow(2).mean().sqrt() / want.pow(2).mean().sqrt()).item()
+
+    assert err(dx, dx0) <= 1.5e-6 and err(dw, dw0) <= 1.5e-6, (err(dx, dx0), err(dw, dw0))
+    # the bound tells two parts from three: two, in an exact product, are beyond it
+    dz = dy.to(F64) if act == "none" else dy.to(F64) * ref.act(z.to(F64), act)[1]
+    one = dz.to(BF16).to(F64)
+    two = one + (dz - one).to(BF16).to(F64)
+    assert err(two.T @ x.to(F64), dw0) > 1.5e-6 and err(two @ w.to(F64), dx0) > 1.5e-6
