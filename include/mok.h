@@ -517,7 +517,9 @@ mok_status mok_linear_forward(const mok_linear_desc* desc, const void* x, const 
 mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, const void* x,
                                const void* w, const void* z, void* dx, float* dw, float* dbias,
                                void* workspace, size_t ws_bytes, int32_t* status, void* stream);
-/* Bytes of scratch of the forward (backward = 0; may be 0) or the backward (1). */
+/* Bytes of scratch of the forward (backward = 0; may be 0), of the backward
+ * (1), or of the backward of a dy that is 16-byte aligned (2): less for a bf16
+ * dy without an activation, of which no copy is then kept. */
 mok_status mok_linear_workspace_size(const mok_linear_desc* desc, int backward, size_t* bytes);
 
 /* Waits for `stream`, then reads the device status word at the start of

@@ -209,7 +209,7 @@ mok_status mok_linear_workspace_size(const mok_linear_desc* desc, int backward, 
     return MOK_OK;
   }
   LinearWs W;
-  linear_layout(D, &W);
+  linear_layout(D, backward == 2 && linear_dz_is_dy(D, nullptr), &W);
   *bytes = W.total;
   return MOK_OK;
 }
@@ -230,7 +230,7 @@ mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, cons
       !aligned(status, 4))
     return MOK_ERR_INVALID_ARG;
   LinearWs W;
-  linear_layout(D, &W);
+  linear_layout(D, linear_dz_is_dy(D, dy), &W);
   if (D.M > 0 && W.total > 0 && !workspace) return MOK_ERR_INVALID_ARG;
   if (D.M > 0 && ws_bytes < W.total) return MOK_ERR_WORKSPACE;
   st = mok_check_device();

@@ -531,7 +531,8 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
     D.dx_elem = elem(dt);
     D.accumulate = static_cast<int32_t>(acc);
     size_t n = 0;
-    check(mok_linear_workspace_size(&D, 1, &n), "mok_linear_workspace_size");
+    const bool aligned = (reinterpret_cast<uintptr_t>(addr(dy)) & 15) == 0;
+    check(mok_linear_workspace_size(&D, aligned ? 2 : 1, &n), "mok_linear_workspace_size");
     const Scratch ws(c, tensor_or_null(a[11], "workspace"), n);
     check(mok_linear_backward(&D, addr(dy), addr(x), addr(w), addr(z), addr(dx),
                               static_cast<float*>(addr(dw)), static_cast<float*>(addr(db)), ws.p,

@@ -976,7 +976,12 @@ bool few_bwd(const mok_linear_desc& D) { return D.M <= kFewTokens; }
 
 }  // namespace
 
-void linear_layout(const mok_linear_desc& D, LinearWs* W) {
+bool linear_dz_is_dy(const mok_linear_desc& D, const void* dy) {
+  return D.y_elem != MOK_ELEM_F32 && D.act == MOK_ACT_NONE && D.N % 8 == 0 &&
+         (reinterpret_cast<uintptr_t>(dy) & 15) == 0;
+}
+
+void linear_layout(const mok_linear_desc& D, bool dz_is_dy, LinearWs* W) {
   auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   if (few_bwd(D)) {
     *W = LinearWs{};
@@ -987,9 +992,11 @@ void linear_layout(const mok_linear_desc& D, LinearWs* W) {
   W->n_pad = (D.N + 63) / 64 * 64;
   W->bias_rows = (D.M + kDzRows - 1) / kDzRows;
   W->dw_splits = dw_splits(D);
-  const size_t dz = static_cast<size_t>(D.M) * W->n_pad * 2;
-  for (int p = 0; p < 3; ++p) W->dz[p] = p * al(dz);
-  W->part_bias = 3 * al(dz);
+  // dz in as many parts as a product takes
+  const size_t dz = al(static_cast<size_t>(D.M) * W->n_pad * 2);
+  const int parts = dz_is_dy ? 0 : dz_parts(D, true);
+  for (int p = 0; p < 3; ++p) W->dz[p] = p < parts ? p * dz : 0;
+  W->part_bias = parts * dz;
   W->part_dw = W->part_bias + al(static_cast<size_t>(W->bias_rows) * D.N * 4);
   // partial products of dx, then of dw: one region
   W->dx_splits = engine_splits(D.M, D.K, W->n_pad, dz_parts(D, D.dx_elem == MOK_ELEM_F32));
@@ -1055,14 +1062,14 @@ cudaError_t launch_few_bwd(const mok_linear_desc& D, const void* dy, const void*
 cudaError_t launch_linear_bwd(const mok_linear_desc& D, const void* dy, const void* x,
                               const void* w, const void* z, void* dx, float* dw, float* dbias,
                               void* ws, int* status, cudaStream_t st) {
+  // a bf16 dy without an activation is dz already
+  const bool direct = linear_dz_is_dy(D, dy);
   LinearWs W;
-  linear_layout(D, &W);
+  linear_layout(D, direct, &W);
   char* b = static_cast<char*>(ws);
   const bool f32 = D.y_elem == MOK_ELEM_F32;
   const bool add_dx = (D.accumulate & MOK_ADD_DX) != 0, add_dw = (D.accumulate & MOK_ADD_DW) != 0;
   const bool vec = D.N % 8 == 0 && ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-  // a bf16 dy without an activation is dz already
-  const bool direct = !f32 && D.act == MOK_ACT_NONE && vec;
   const bool dxf = D.dx_elem == MOK_ELEM_F32;
   const int parts = direct ? 0 : dz_parts(D, dw || dxf);
   const bool products = D.M > 0 && (dx || dw);

@@ -298,7 +298,10 @@ struct LinearWs {
   int dw_splits;      // partial weight gradients (1: none)
   int dx_splits;      // partial products of dx (1: none)
 };
-void linear_layout(const mok_linear_desc& D, LinearWs* W);
+// Whether dz is dy itself, in place (a bf16 dy in 16-byte aligned rows, no
+// activation): the backward then keeps no copy of it.
+bool linear_dz_is_dy(const mok_linear_desc& D, const void* dy);
+void linear_layout(const mok_linear_desc& D, bool dz_is_dy, LinearWs* W);
 cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w,
                           const float* bias, const void* res, void* y, void* z, void* ws,
                           int* status, cudaStream_t st);

@@ -297,3 +297,28 @@ def test_linear_backward_keeps_fp32_accuracy_over_many_tokens(M, N, K, act, dyt)
     one = dz.to(BF16).to(F64)
     two = one + (dz - one).to(BF16).to(F64)
     assert err(two.T @ x.to(F64), dw0) > 1.5e-6 and err(two @ w.to(F64), dx0) > 1.5e-6
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 64, 136), (700, 264, 520), (3000, 1024, 256)])
+@pytest.mark.parametrize("offset", [0, 1, 4])
+def test_linear_backward_of_a_plain_dy_in_the_stated_scratch(M, N, K, offset):
+    """A bf16 dy without an activation, at an offset of its own, through the C entry
+    in exactly the scratch that the size query states for it; less is refused."""
+    x, w = randn(1900, M, K), randn(1901, N, K, scale=1 / math.sqrt(K))
+    dy = randn(1902, M * N + 8)[offset:offset + M * N].view(M, N)
+    dx, dw, db = (torch.empty(s, device="cuda") for s in ((M, K), (N, K), (N,)))
+    d = _lib.LinearDesc(M=M, N=N, K=K, dx_elem=1)
+    n, lib = ctypes.c_size_t(), _lib.load()
+    assert lib.mok_linear_workspace_size(d, 1 if offset else 2, n) == 0
+    buf = torch.full((n.value + 256,), 91, dtype=torch.uint8, device="cuda")
+    ptrs = [t.data_ptr() for t in (dy, x, w)] + [None] + [t.data_ptr() for t in (dx, dw, db, buf)]
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.mok_linear_backward(d, *ptrs, n.value - 1, None, stream) == 3
+    assert lib.mok_linear_backward(d, *ptrs, n.value, None, stream) == 0
+    assert (buf[n.value:] == 91).all()
+    (dx0, dw0, db0), (mx, mw, mb) = ref.linear_backward(dy, x, w, None, "none")
+    within(dx, dx0, mx * (2 * N + 2) * U32 + 1e-30)
+    within(dw, dw0, mw * (2 * M + 16) * U32 + 1e-30)
+    within(db, db0, mb * (2 * M + 16) * U32 + 1e-30)
+    for got, want in zip(api.linear_backward(dy, x, w, bias=True, dx_dtype=F32), (dx, dw, db)):
+        assert torch.equal(got, want)
