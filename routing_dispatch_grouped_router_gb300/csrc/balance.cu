@@ -30,9 +30,8 @@ namespace {
 constexpr int kManyThreads = 1024;
 constexpr int kFewThreads = 256;
 constexpr int kBwdThreads = 256;
-// Blocks of the forward (one per SM of a GB300, whatever the device, so that
-// the sums do not depend on it).
-constexpr int kFwdBlocks = 152;
+// Blocks of the forward.
+constexpr int kFwdBlocks = kGb300Sms;
 
 struct BalArgs {
   const float* logits;

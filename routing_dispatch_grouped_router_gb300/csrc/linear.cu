@@ -473,7 +473,7 @@ cudaError_t run_linear(const mok_linear_desc& D, const void* x, const void* w, c
   const int64_t nt = (D.N + 127) / 128, mt = (D.M + BN - 1) / BN;
   // K splits: a power of two, as many as the CTAs that fit at once leave room
   // for, at least four 64-value blocks each
-  const int64_t slots = 2LL * num_sms_current_device();
+  constexpr int64_t slots = 2 * kGb300Sms;
   int ks = 1;
   while (ks < kMaxSplits && nt * mt * ks * 2 <= slots && a.nkb >= ks * 8) ks *= 2;
   auto kern = ks == 1   ? linear_kernel<BN, F32, 1>
@@ -576,7 +576,7 @@ int best_splits(int64_t tiles, int64_t slots, int64_t nkb, int parts, int64_t el
 int engine_splits(int64_t M, int64_t N, int64_t K, int parts) {
   const int64_t rows = M > 128 ? 256 : 128, cols = M > 128 || parts < 3 ? 256 : 128;
   const int64_t tiles = ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
-  return best_splits(tiles, M > 128 ? 76 : 152, (K + 63) / 64, parts, M * N,
+  return best_splits(tiles, M > 128 ? kGb300Sms / 2 : kGb300Sms, (K + 63) / 64, parts, M * N,
                      16);
 }
 
@@ -640,7 +640,7 @@ cudaError_t launch_linear(const mok_linear_desc& D, const void* x, const void* w
     };
     auto run = [&](auto MT, auto F) {
       using std::integral_constant;
-      const int64_t many = 2LL * num_sms_current_device();
+      constexpr int64_t many = 2 * kGb300Sms;
       if (K <= 2048 && D.N >= 16 * many) launch(MT, integral_constant<int, 2>(), F);
       else if (K <= 4096 && D.N >= 8 * many) launch(MT, integral_constant<int, 4>(), F);
       else launch(MT, integral_constant<int, 8>(), F);
@@ -827,7 +827,7 @@ int dz_parts(const mok_linear_desc& D, bool f32) {
 int dw_splits(const mok_linear_desc& D) {
   const int64_t mt = (D.N + 127) / 128;
   const int64_t tiles = (mt + 1) / 2 * ((D.K + 255) / 256);
-  return best_splits(tiles, mt > 1 ? 76 : 152, (D.M + 63) / 64, dz_parts(D, true), D.N * D.K,
+  return best_splits(tiles, mt > 1 ? kGb300Sms / 2 : kGb300Sms, (D.M + 63) / 64, dz_parts(D, true), D.N * D.K,
                      32);
 }
 
@@ -966,7 +966,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_bwd_few_kernel(FewBwd a
 // least eight rows per warp.
 int64_t few_rows(const mok_linear_desc& D) {
   const int64_t cols = (D.K + 127) / 128;
-  int64_t slices = 304 / cols;
+  int64_t slices = 2 * kGb300Sms / cols;
   if (slices < 1) slices = 1;
   const int64_t rows = ((D.N + slices - 1) / slices + 7) / 8 * 8;
   return rows < 64 ? 64 : rows;

@@ -93,6 +93,9 @@ void bwd_layout(const Dims& D, BwdWs* W);
 void stage_layout(const Dims& D, StageWs* W);
 
 int num_sms_current_device();
+// SMs of a GB300.  Splits and block counts that decide the order of a sum go by
+// this and not by what the device shows, so that results do not depend on it.
+constexpr int kGb300Sms = 152;
 mok_status mok_check_device();  // MOK_OK when the current device is sm_103
 
 // ------------------------------------------------------------------ kernels --

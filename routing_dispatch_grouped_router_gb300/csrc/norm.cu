@@ -492,7 +492,7 @@ namespace {
 // thread where that fits, so that a row's loads are all in flight at once.
 // Many rows: up to max_nv, so that several rows share an SM.
 void norm_shape(long long rows, int nvec, int max_nv, int* tpr, int* nv) {
-  int n = rows >= 4LL * num_sms_current_device() ? max_nv : 1;
+  int n = rows >= 4LL * kGb300Sms ? max_nv : 1;
   if (nvec > 1024) n = 4;
   while (n > 1 && nvec <= 32 * (n / 2)) n /= 2;
   const int th = (nvec + n - 1) / n;
@@ -980,7 +980,7 @@ BwdShape bwd_shape(int64_t rows, int64_t d, Rows how, int64_t row_bytes) {
     if (b.depth > kBulkMaxDepth) b.depth = kBulkMaxDepth;
   }
   const int64_t need = (rows + b.rpb - 1) / b.rpb;
-  b.blocks = need < 152 * per_sm ? need : 152 * per_sm;  // (kShift: a multiple of eight)
+  b.blocks = need < kGb300Sms * per_sm ? need : kGb300Sms * per_sm;  // (kShift: a multiple of eight)
   return b;
 }
 
