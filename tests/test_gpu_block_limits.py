@@ -11,7 +11,7 @@ import torch
 
 import _block_ref as ref
 from _block_ref import F64, U16, U32
-from routing_dispatch_grouped_router_gb300 import _lib, api
+from routing_dispatch_grouped_router_gb300 import _lib, api, block
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -322,3 +322,45 @@ def test_linear_backward_of_a_plain_dy_in_the_stated_scratch(M, N, K, offset):
     within(db, db0, mb * (2 * M + 16) * U32 + 1e-30)
     for got, want in zip(api.linear_backward(dy, x, w, bias=True, dx_dtype=F32), (dx, dw, db)):
         assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------ the MoE block --
+
+@pytest.mark.parametrize("dtype", [api.BF16, api.MXFP8, api.NVFP4])
+def test_block_is_its_calls_in_every_type_of_the_layer(dtype):
+    """MoEBlock gives, bit for bit, what its operators and a layer of that type give
+    called one by one."""
+    T, d, E, I, k, F = 200, 256, 8, 256, 2, 264
+    w = {"norm": 1 + randn(2000, d, dtype=F32, scale=0.1), "w_router": randn(2001, E, d, scale=d ** -0.5),
+         "w_gate_up": randn(2002, E, 2 * I, d, scale=d ** -0.5),
+         "w_down": randn(2003, E, d, I, scale=I ** -0.5), "w_up": randn(2004, F, d, scale=d ** -0.5),
+         "b_up": randn(2005, F, dtype=F32, scale=0.1), "w_out": randn(2006, d, F, scale=F ** -0.5),
+         "b_out": randn(2007, d, dtype=F32, scale=0.1)}
+    x, r, dout = randn(2008, T, d, dtype=F32), randn(2009, T, d), randn(2010, T, d)
+    dloss = torch.tensor([1.5, 0.5], device="cuda")
+    blk = block.MoEBlock(T, d, E, I, k, act="gelu", dtype=dtype)
+    out, s, loss, counts = blk.forward(x, r, w)
+    dx, g = blk.backward(dout, None, dloss, w)
+    assert blk.status() == 0
+
+    layer = api.MoELayer(T, d, E, I, k, dtype=dtype)
+    s0, n = api.add_rmsnorm(x, w["norm"], r, eps=blk.eps)
+    routed = layer.forward(n, w["w_router"], None, w["w_gate_up"], w["w_down"])
+    logits = api.linear(n, w["w_router"], out_dtype=F32)
+    idx = layer.saved_tensor("topk_idx", torch.int32, (T, k))
+    loss0, counts0, _, lse, nv = api.router_balance(logits, idx, **blk.coefs)
+    h, z = api.linear(n, w["w_up"], w["b_up"], act="gelu", keep_z=True)
+    out0 = api.linear(h, w["w_out"], w["b_out"], residual=routed, out_dtype=F32)
+    for got, want in ((out, out0), (s, s0), (loss, loss0), (counts, counts0)):
+        assert torch.equal(got, want)
+    dn, wr, wgu, wd = layer.backward(dout, n, w["w_router"], None, w["w_gate_up"], w["w_down"])
+    dh, wo, bo = api.linear_backward(dout, h, w["w_out"], bias=True)
+    _, wu, bu = api.linear_backward(dh, n, w["w_up"], z, act="gelu", bias=True, dx=dn,
+                                    accumulate="dx")
+    dl = api.router_balance_backward(dloss, logits, lse, counts, nv, k, **blk.coefs)
+    api.linear_backward(dl, n, w["w_router"], dx=dn, dw=wr, accumulate=True)
+    dx0, wn = api.add_rmsnorm_backward(dn, s, w["norm"], eps=blk.eps)
+    assert torch.equal(dx, dx0)
+    for name, want in (("norm", wn), ("w_router", wr), ("w_gate_up", wgu), ("w_down", wd),
+                       ("w_up", wu), ("b_up", bu), ("w_out", wo), ("b_out", bo)):
+        assert torch.equal(g[name], want), name
