@@ -522,6 +522,102 @@ mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, cons
  * dy without an activation, of which no copy is then kept. */
 mok_status mok_linear_workspace_size(const mok_linear_desc* desc, int backward, size_t* bytes);
 
+/* Dropout and the residual's addition:
+ *   y = residual + (u >= round(p 2^32) ? x / (1 - p) : 0)
+ * u of the element in row i and column j is word n mod 4, n = i d + j, of
+ * Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
+ * 2011) at the counter (n / 4 in 64 bits, step, site) under the key seed.  A
+ * function of rng, site and the element's place alone, whatever strides, types
+ * or launches: no mask is stored, the backward draws it again.  rng: device
+ * int64 [2], the seed and the step (its low 32 bits count); a program draws new
+ * numbers by writing another step there, also between replays of a graph.
+ * site tells the calls of a step apart. */
+typedef struct mok_dropout_desc {
+  int64_t rows, d;       /* 0 <= rows < 2^31, 1 <= d < 2^31 */
+  int64_t ld_x;          /* row stride of x (forward), dy (backward) */
+  int64_t ld_res;        /* of residual */
+  int64_t ld_y;          /* of y (forward), dx (backward) */
+  double p;              /* 0 <= p <= 1; 1 drops every element */
+  int32_t x_elem;        /* mok_elem of x (forward), dy (backward) */
+  int32_t y_elem;        /* of residual and y (forward), of dx (backward) */
+  uint32_t site;
+  uint32_t reserved;     /* 0 */
+} mok_dropout_desc;
+
+/* x [rows,d], residual [rows,d] or NULL, y [rows,d]: the sum in fp32, rounded
+ * once.  What is dropped does not reach y (not even a NaN).  y may equal x or
+ * residual (of the same type and stride).  Pointers aligned to their elements;
+ * 16-byte aligned tensors, contiguous or with rows of whole 16-byte words, run
+ * at full width. */
+mok_status mok_dropout_forward(const mok_dropout_desc* desc, const void* x, const void* residual,
+                               const int64_t* rng, void* y, void* stream);
+/* dx = u >= round(p 2^32) ? dy / (1 - p) : 0.  dx may equal dy.  (The gradient
+ * of residual is dy itself.) */
+mok_status mok_dropout_backward(const mok_dropout_desc* desc, const void* dy, const int64_t* rng,
+                                void* dx, void* stream);
+
+typedef enum mok_gate {
+  MOK_GATE_NONE = 0,
+  MOK_GATE_CHANNEL = 1, /* [d]: one per column */
+  MOK_GATE_TOKEN = 2    /* [rows]: one per row */
+} mok_gate;
+
+typedef struct mok_post_pre_desc {
+  int64_t rows, d;       /* 0 <= rows < 2^31, 1 <= d <= 16384 */
+  int64_t ld_x;          /* row stride of x */
+  int64_t ld_res;        /* of residual (forward), ds (backward) */
+  int64_t ld_s;          /* of s */
+  int64_t ld_y;          /* of y (forward), dy (backward) */
+  int64_t ld_dx, ld_dr;  /* backward: of dx, dresidual */
+  float eps;             /* added to both mean squares; >= 0 */
+  float residual_scale;
+  int32_t x_elem;        /* mok_elem of x */
+  int32_t s_elem;        /* of the residual stream: residual, s, ds, dresidual */
+  int32_t weight_elem;   /* of post_weight and pre_weight */
+  int32_t gate_elem;     /* of gate */
+  int32_t gate;          /* mok_gate */
+  int32_t y_elem;        /* backward: of dy */
+  int32_t dx_elem;       /* backward: of dx */
+  int32_t accumulate;    /* backward: add into dpost, dpre and dgate */
+} mok_post_pre_desc;
+
+/* The norms after and before a block with its gate and the residual's scale:
+ *   s = residual_scale residual + gate post_weight x / sqrt(mean(x^2) + eps)
+ *   y = pre_weight s / sqrt(mean(s^2) + eps)
+ * x [rows,d] is a block's output, residual [rows,d] the stream that went into
+ * it; s is the stream that goes on (the sum in fp32, rounded once to s_elem) and
+ * y bf16 what the next block reads.  The second norm reads s as it is stored,
+ * so that the backward differentiates the very function that ran.  gate:
+ * [d], [rows] or NULL, as desc->gate says.  s may equal residual, or x of the
+ * same type (same strides).  Any pointer aligned to its element and any row
+ * stride >= d is taken; 16-byte aligned rows with d a multiple of 8 run at full
+ * width. */
+mok_status mok_post_pre_rmsnorm_forward(const mok_post_pre_desc* desc, const void* x,
+                                        const void* residual, const void* post_weight,
+                                        const void* pre_weight, const void* gate, void* s,
+                                        void* y, void* stream);
+
+/* Backward, from dy [rows,d] of y and ds [rows,d] (s_elem; NULL: none) that
+ * reaches s by other ways.  With n, m the normalised x and s:
+ *   g = dy pre_weight,  t = (g - m mean(g m)) / sqrt(mean(s^2) + eps) + ds
+ *   q = t gate post_weight,  dx = (q - n mean(q n)) / sqrt(mean(x^2) + eps)
+ *   dresidual = residual_scale t
+ *   dpost [d] (+)= sum over rows of t gate n,  dpre [d] (+)= sum of dy m,
+ *   dgate (+)= sum of t post_weight n over the rows ([d]) or columns ([rows])
+ * dx (dx_elem) and dresidual (s_elem) [rows,d]; dpost, dpre, dgate fp32, each
+ * optional (NULL), summed in a fixed order.  dresidual may equal ds, dx may
+ * equal x or dy of its type (same strides).  workspace: see the size query
+ * (needed for dpost, dpre or a channel's dgate).  status: as in
+ * mok_router_balance_forward; a bounded wait that gave up sets
+ * MOK_ERR_DEVICE_TIMEOUT. */
+mok_status mok_post_pre_rmsnorm_backward(const mok_post_pre_desc* desc, const void* dy,
+                                         const void* x, const void* s, const void* post_weight,
+                                         const void* pre_weight, const void* gate,
+                                         const void* ds, void* dx, void* dresidual, float* dpost,
+                                         float* dpre, float* dgate, void* workspace,
+                                         size_t ws_bytes, int32_t* status, void* stream);
+mok_status mok_post_pre_rmsnorm_workspace_size(const mok_post_pre_desc* desc, size_t* bytes);
+
 /* Waits for `stream`, then reads the device status word at the start of
  * `buf` (the `saved` buffer of forward/backward, or the workspace of the
  * other entry points) into *code (a mok_status; MOK_OK = no device error). */

@@ -49,6 +49,21 @@ class LinearDesc(ctypes.Structure):
                 ("accumulate", c_int32)]
 
 
+class DropoutDesc(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("d", c_int64), ("ld_x", c_int64), ("ld_res", c_int64),
+                ("ld_y", c_int64), ("p", ctypes.c_double), ("x_elem", c_int32),
+                ("y_elem", c_int32), ("site", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class PostPreDesc(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("d", c_int64), ("ld_x", c_int64), ("ld_res", c_int64),
+                ("ld_s", c_int64), ("ld_y", c_int64), ("ld_dx", c_int64), ("ld_dr", c_int64),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("x_elem", c_int32), ("s_elem", c_int32), ("weight_elem", c_int32),
+                ("gate_elem", c_int32), ("gate", c_int32), ("y_elem", c_int32),
+                ("dx_elem", c_int32), ("accumulate", c_int32)]
+
+
 # name -> (restype, argtypes)
 _SIGS = {
     "mok_moe_workspace_size": (c_int32, [ctypes.POINTER(MoeDesc), ctypes.POINTER(c_size_t),
@@ -97,6 +112,13 @@ _SIGS = {
                             + [c_size_t, c_void_p, c_void_p]),
     "mok_linear_workspace_size": (c_int32, [ctypes.POINTER(LinearDesc), c_int32,
                                             ctypes.POINTER(c_size_t)]),
+    "mok_dropout_forward": (c_int32, [ctypes.POINTER(DropoutDesc)] + [c_void_p] * 5),
+    "mok_dropout_backward": (c_int32, [ctypes.POINTER(DropoutDesc)] + [c_void_p] * 4),
+    "mok_post_pre_rmsnorm_forward": (c_int32, [ctypes.POINTER(PostPreDesc)] + [c_void_p] * 8),
+    "mok_post_pre_rmsnorm_backward": (c_int32, [ctypes.POINTER(PostPreDesc)] + [c_void_p] * 13
+                                      + [c_size_t, c_void_p, c_void_p]),
+    "mok_post_pre_rmsnorm_workspace_size": (c_int32, [ctypes.POINTER(PostPreDesc),
+                                                      ctypes.POINTER(c_size_t)]),
     "mok_selftest_bounded_wait": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_fill_zero": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_get_device_status": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(c_int32)]),

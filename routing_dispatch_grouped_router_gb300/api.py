@@ -293,6 +293,48 @@ def linear_backward(dy, x, w, z=None, *, act="none", bias=False, dx_dtype=None, 
                                   workspace, stream)
 
 
+def dropout(x, p, rng, site=0, *, residual=None, out_dtype=None, y=None, stream=None):
+    """y = residual + dropout(x) with kept elements over 1 - p (see
+    mok_dropout_forward).  rng: int64 [2] on the GPU, the seed and the step (its
+    low 32 bits count); what is dropped goes by them, `site` (a number that tells
+    the calls of a step apart) and the element's place alone, so that no mask is
+    kept.  x bf16 or fp32 [rows, d], rows may be strided; y of out_dtype (the
+    residual's type, else that of x)."""
+    return _ops().dropout(x, p, rng, site, residual, out_dtype, y, stream)
+
+
+def dropout_backward(dy, p, rng, site=0, *, dx_dtype=None, dx=None, stream=None):
+    """The gradient of x of `dropout` from dy and what the forward had for p, rng
+    (with the same values) and site; that of the residual is dy itself.  dx of
+    dx_dtype (the type of dy)."""
+    return _ops().dropout_backward(dy, p, rng, site, dx_dtype, dx, stream)
+
+
+def post_pre_rmsnorm(x, residual, post_weight, pre_weight, gate=None, *, residual_scale=1.0,
+                     eps=1e-6, s=None, y=None, stream=None):
+    """s = residual_scale * residual + gate * RMSNorm(x) * post_weight and y =
+    RMSNorm(s) * pre_weight (see mok_post_pre_rmsnorm_forward): (s, y), s in the
+    residual's type, y bf16.  x is a block's output, residual the stream that went
+    into it.  gate: None, [d] (per channel) or [rows, 1] (per token).  All bf16 or
+    fp32, the two weights alike; rows may be strided."""
+    return _ops().post_pre_rmsnorm(x, residual, post_weight, pre_weight, gate, residual_scale, eps,
+                                   s, y, stream)
+
+
+def post_pre_rmsnorm_backward(dy, x, s, post_weight, pre_weight, gate=None, ds=None, *,
+                              residual_scale=1.0, eps=1e-6, dx_dtype=None, dx=None,
+                              dresidual=None, dpost=None, dpre=None, dgate=None,
+                              accumulate=False, workspace=None, stream=None):
+    """Gradients of `post_pre_rmsnorm` from dy, the stored s and ds, the gradient
+    that reaches s by other ways (see mok_post_pre_rmsnorm_backward): (dx,
+    dresidual, dpost, dpre, dgate), dx of dx_dtype (the type of x), dresidual of
+    the type of s, the others fp32 (dgate None without a gate) and added into with
+    `accumulate`."""
+    return _ops().post_pre_rmsnorm_backward(dy, x, s, post_weight, pre_weight, gate, ds,
+                                            residual_scale, eps, dx_dtype, dx, dresidual, dpost,
+                                            dpre, dgate, accumulate, workspace, stream)
+
+
 def device_status(buf, stream=None) -> int:
     """Synchronises the stream and returns the device status word of `buf`."""
     lib = _lib.load()

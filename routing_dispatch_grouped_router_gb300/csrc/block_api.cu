@@ -1,6 +1,6 @@
 // C ABI of the operators around the layer (declared in include/mok.h): the
-// residual addition with RMS norm, the router's auxiliary losses and the dense
-// product.  Argument checks and the order of kernels; nothing is enqueued
+// residual addition with RMS norm, the router's auxiliary losses, the dense
+// product, dropout and the norms after and before a block.  Argument checks and the order of kernels; nothing is enqueued
 // before every argument has been checked.
 #include <cuda_runtime.h>
 
@@ -62,6 +62,47 @@ mok_status linear_desc(const mok_linear_desc* desc, mok_linear_desc* D) {
   if (D->accumulate & ~(MOK_ADD_DX | MOK_ADD_DW)) return MOK_ERR_UNSUPPORTED;
   if (!stride(&D->ld_x, D->K)) return MOK_ERR_INVALID_ARG;
   if (D->ld_x % 8) return MOK_ERR_UNSUPPORTED;
+  return MOK_OK;
+}
+
+mok_status dropout_desc(const mok_dropout_desc* desc, mok_dropout_desc* D) {
+  if (!desc) return MOK_ERR_INVALID_ARG;
+  *D = *desc;
+  if (D->rows < 0 || D->d <= 0 || !(D->p >= 0.0 && D->p <= 1.0)) return MOK_ERR_INVALID_ARG;
+  if (D->rows >= (1LL << 31) || D->d >= (1LL << 31)) return MOK_ERR_UNSUPPORTED;
+  if (!elem_ok(D->x_elem) || !elem_ok(D->y_elem) || D->reserved != 0) return MOK_ERR_UNSUPPORTED;
+  if (!stride(&D->ld_x, D->d) || !stride(&D->ld_res, D->d) || !stride(&D->ld_y, D->d))
+    return MOK_ERR_INVALID_ARG;
+  return MOK_OK;
+}
+
+mok_status dropout(const mok_dropout_desc* desc, const void* x, const void* residual,
+                   const int64_t* rng, void* y, void* stream) {
+  mok_dropout_desc D;
+  mok_status st = dropout_desc(desc, &D);
+  if (st != MOK_OK) return st;
+  if (!rng || (D.rows > 0 && (!x || !y))) return MOK_ERR_INVALID_ARG;
+  const size_t ye = elem_size(D.y_elem);
+  if (!aligned(x, elem_size(D.x_elem)) || !aligned(residual, ye) || !aligned(y, ye) ||
+      !aligned(rng, 8))
+    return MOK_ERR_INVALID_ARG;
+  st = mok_check_device();
+  if (st != MOK_OK) return st;
+  return cuda_status(launch_dropout(D, x, residual, rng, y, static_cast<cudaStream_t>(stream)));
+}
+
+mok_status post_pre_desc(const mok_post_pre_desc* desc, mok_post_pre_desc* D) {
+  if (!desc) return MOK_ERR_INVALID_ARG;
+  *D = *desc;
+  if (D->rows < 0 || D->d <= 0 || !(D->eps >= 0.f)) return MOK_ERR_INVALID_ARG;
+  if (D->rows >= (1LL << 31) || D->d > 16384) return MOK_ERR_UNSUPPORTED;
+  if (!elem_ok(D->x_elem) || !elem_ok(D->s_elem) || !elem_ok(D->weight_elem) ||
+      !elem_ok(D->gate_elem) || !elem_ok(D->y_elem) || !elem_ok(D->dx_elem))
+    return MOK_ERR_UNSUPPORTED;
+  if (D->gate < MOK_GATE_NONE || D->gate > MOK_GATE_TOKEN) return MOK_ERR_UNSUPPORTED;
+  if (!stride(&D->ld_x, D->d) || !stride(&D->ld_res, D->d) || !stride(&D->ld_s, D->d) ||
+      !stride(&D->ld_y, D->d) || !stride(&D->ld_dx, D->d) || !stride(&D->ld_dr, D->d))
+    return MOK_ERR_INVALID_ARG;
   return MOK_OK;
 }
 
@@ -237,6 +278,80 @@ mok_status mok_linear_backward(const mok_linear_desc* desc, const void* dy, cons
   if (st != MOK_OK) return st;
   return cuda_status(launch_linear_bwd(D, dy, x, w, z, dx, dw, dbias, workspace, status,
                                        static_cast<cudaStream_t>(stream)));
+}
+
+mok_status mok_dropout_forward(const mok_dropout_desc* desc, const void* x, const void* residual,
+                               const int64_t* rng, void* y, void* stream) {
+  return dropout(desc, x, residual, rng, y, stream);
+}
+
+mok_status mok_dropout_backward(const mok_dropout_desc* desc, const void* dy, const int64_t* rng,
+                                void* dx, void* stream) {
+  return dropout(desc, dy, nullptr, rng, dx, stream);
+}
+
+mok_status mok_post_pre_rmsnorm_forward(const mok_post_pre_desc* desc, const void* x,
+                                        const void* residual, const void* post_weight,
+                                        const void* pre_weight, const void* gate, void* s,
+                                        void* y, void* stream) {
+  mok_post_pre_desc D;
+  mok_status st = post_pre_desc(desc, &D);
+  if (st != MOK_OK) return st;
+  if (!post_weight || !pre_weight || (D.rows > 0 && (!x || !residual || !s || !y)))
+    return MOK_ERR_INVALID_ARG;
+  if ((gate != nullptr) != (D.gate != MOK_GATE_NONE) && D.rows > 0) return MOK_ERR_INVALID_ARG;
+  const size_t se = elem_size(D.s_elem), we = elem_size(D.weight_elem);
+  if (!aligned(x, elem_size(D.x_elem)) || !aligned(residual, se) || !aligned(s, se) ||
+      !aligned(y, 2) || !aligned(post_weight, we) || !aligned(pre_weight, we) ||
+      !aligned(gate, elem_size(D.gate_elem)))
+    return MOK_ERR_INVALID_ARG;
+  st = mok_check_device();
+  if (st != MOK_OK) return st;
+  return cuda_status(launch_post_pre(D, x, residual, post_weight, pre_weight, gate, s, y,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+mok_status mok_post_pre_rmsnorm_workspace_size(const mok_post_pre_desc* desc, size_t* bytes) {
+  mok_post_pre_desc D;
+  const mok_status st = post_pre_desc(desc, &D);
+  if (st != MOK_OK) return st;
+  if (!bytes) return MOK_ERR_INVALID_ARG;
+  *bytes = static_cast<size_t>(post_pre_bwd_blocks(D)) * static_cast<size_t>(D.d) * 8;
+  return MOK_OK;
+}
+
+mok_status mok_post_pre_rmsnorm_backward(const mok_post_pre_desc* desc, const void* dy,
+                                         const void* x, const void* s, const void* post_weight,
+                                         const void* pre_weight, const void* gate,
+                                         const void* ds, void* dx, void* dresidual, float* dpost,
+                                         float* dpre, float* dgate, void* workspace,
+                                         size_t ws_bytes, int32_t* status, void* stream) {
+  mok_post_pre_desc D;
+  mok_status st = post_pre_desc(desc, &D);
+  if (st != MOK_OK) return st;
+  if (!post_weight || !pre_weight || (D.rows > 0 && (!dy || !x || !s || !dx || !dresidual)))
+    return MOK_ERR_INVALID_ARG;
+  if ((gate != nullptr) != (D.gate != MOK_GATE_NONE) && D.rows > 0) return MOK_ERR_INVALID_ARG;
+  if (dgate && D.gate == MOK_GATE_NONE) return MOK_ERR_INVALID_ARG;
+  const size_t se = elem_size(D.s_elem), we = elem_size(D.weight_elem);
+  if (!aligned(dy, elem_size(D.y_elem)) || !aligned(x, elem_size(D.x_elem)) || !aligned(s, se) ||
+      !aligned(ds, se) || !aligned(dresidual, se) || !aligned(dx, elem_size(D.dx_elem)) ||
+      !aligned(post_weight, we) || !aligned(pre_weight, we) ||
+      !aligned(gate, elem_size(D.gate_elem)) || !aligned(dpost, 4) || !aligned(dpre, 4) ||
+      !aligned(dgate, 4) || !aligned(status, 4))
+    return MOK_ERR_INVALID_ARG;
+  if (D.rows > 0 && (dpost || dpre || (dgate && D.gate == MOK_GATE_CHANNEL))) {
+    if (!workspace || !aligned(workspace, 16)) return MOK_ERR_INVALID_ARG;
+    size_t need = 0;
+    mok_post_pre_rmsnorm_workspace_size(&D, &need);
+    if (ws_bytes < need) return MOK_ERR_WORKSPACE;
+  }
+  st = mok_check_device();
+  if (st != MOK_OK) return st;
+  return cuda_status(launch_post_pre_bwd(D, dy, x, s, post_weight, pre_weight, gate, ds, dx,
+                                         dresidual, dpost, dpre, dgate,
+                                         static_cast<float*>(workspace), status,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

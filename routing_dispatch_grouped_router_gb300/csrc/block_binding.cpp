@@ -542,6 +542,191 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
   });
 }
 
+// ---------------------------------------------------------------- dropout --
+
+// x, rng, p, site and the output of a call in either direction
+mok_dropout_desc dropout_desc(const Call& c, const at::Tensor& x, const char* name,
+                              const at::Tensor& rng, double p, int64_t site) {
+  mok_dropout_desc D = {};
+  D.ld_x = matrix(x, name, c.device);
+  type_real(x, name);
+  D.rows = x.size(0);
+  D.d = x.size(1);
+  dense(rng, "rng", c.device, {2});
+  type_is(rng, "rng", at::kLong);
+  TORCH_CHECK_VALUE(p >= 0.0 && p <= 1.0, "p must be from 0 to 1, got ", p);
+  TORCH_CHECK_VALUE(site >= 0 && site < (1LL << 32), "site must be a 32-bit number, got ", site);
+  D.p = p;
+  D.site = static_cast<uint32_t>(site);
+  D.x_elem = elem(x.scalar_type());
+  return D;
+}
+
+// (x, p, rng, site, residual, out_dtype, y, stream) -> y
+PyObject* py_dropout(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&] {
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::Tensor& rng = tensor(a[2], "rng");
+    const at::Tensor *res = tensor_or_null(a[4], "residual"), *y0 = tensor_or_null(a[6], "y");
+    const Call c(x, a[7]);
+    mok_dropout_desc D = dropout_desc(c, x, "x", rng, number(a[1]), integer(a[3]));
+    const at::ScalarType dt = dtype_or(
+        a[5], y0 ? y0->scalar_type() : (res ? *res : x).scalar_type(), "out_dtype");
+    TORCH_CHECK_VALUE(real(dt), "y must not be ", dt);
+    if (res) {
+      D.ld_res = matrix(*res, "residual", c.device, D.rows, D.d);
+      type_is(*res, "residual", dt);
+    }
+    at::Tensor y = y0 ? *y0 : c.empty({D.rows, D.d}, dt);
+    D.ld_y = matrix(y, "y", c.device, D.rows, D.d);
+    type_is(y, "y", dt);
+    D.y_elem = elem(dt);
+    check(mok_dropout_forward(&D, addr(x), addr(res), static_cast<int64_t*>(addr(rng)), addr(y),
+                              c.raw),
+          "mok_dropout_forward");
+    return wrap(y);
+  });
+}
+
+// (dy, p, rng, site, dx_dtype, dx, stream) -> dx
+PyObject* py_dropout_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&] {
+    const at::Tensor& dy = tensor(a[0], "dy");
+    const at::Tensor& rng = tensor(a[2], "rng");
+    const at::Tensor* dx0 = tensor_or_null(a[5], "dx");
+    const Call c(dy, a[6]);
+    mok_dropout_desc D = dropout_desc(c, dy, "dy", rng, number(a[1]), integer(a[3]));
+    const at::ScalarType dt = dtype_or(a[4], (dx0 ? *dx0 : dy).scalar_type(), "dx_dtype");
+    TORCH_CHECK_VALUE(real(dt), "dx must not be ", dt);
+    at::Tensor dx = dx0 ? *dx0 : c.empty({D.rows, D.d}, dt);
+    D.ld_y = matrix(dx, "dx", c.device, D.rows, D.d);
+    type_is(dx, "dx", dt);
+    D.y_elem = elem(dt);
+    check(mok_dropout_backward(&D, addr(dy), static_cast<int64_t*>(addr(rng)), addr(dx), c.raw),
+          "mok_dropout_backward");
+    return wrap(dx);
+  });
+}
+
+// -------------------------------------------------------- post_pre_rmsnorm --
+
+// x, the weights, the gate ([d]: per channel, [rows, 1]: per token) and the scales
+mok_post_pre_desc post_pre_desc(const Call& c, const at::Tensor& x, const at::Tensor& post,
+                                const at::Tensor& pre, const at::Tensor* gate, double alpha,
+                                double eps) {
+  mok_post_pre_desc D = {};
+  D.ld_x = matrix(x, "x", c.device);
+  type_real(x, "x");
+  D.rows = x.size(0);
+  D.d = x.size(1);
+  dense(post, "post_weight", c.device, {D.d});
+  type_real(post, "post_weight");
+  dense(pre, "pre_weight", c.device, {D.d});
+  type_is(pre, "pre_weight", post.scalar_type());
+  if (gate) {
+    if (gate->dim() == 1) dense(*gate, "gate", c.device, {D.d});
+    else dense(*gate, "gate", c.device, {D.rows, 1});
+    type_real(*gate, "gate");
+    D.gate = gate->dim() == 1 ? MOK_GATE_CHANNEL : MOK_GATE_TOKEN;
+    D.gate_elem = elem(gate->scalar_type());
+  }
+  D.residual_scale = static_cast<float>(alpha);
+  D.eps = static_cast<float>(eps);
+  D.x_elem = D.dx_elem = elem(x.scalar_type());
+  D.weight_elem = elem(post.scalar_type());
+  return D;
+}
+
+// (x, residual, post_weight, pre_weight, gate, residual_scale, eps, s, y, stream) -> (s, y)
+PyObject* py_post_pre_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&] {
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::Tensor& res = tensor(a[1], "residual");
+    const at::Tensor& post = tensor(a[2], "post_weight");
+    const at::Tensor& pre = tensor(a[3], "pre_weight");
+    const at::Tensor* gate = tensor_or_null(a[4], "gate");
+    const at::Tensor *s0 = tensor_or_null(a[7], "s"), *y0 = tensor_or_null(a[8], "y");
+    const Call c(x, a[9]);
+    mok_post_pre_desc D = post_pre_desc(c, x, post, pre, gate, number(a[5]), number(a[6]));
+    D.ld_res = matrix(res, "residual", c.device, D.rows, D.d);
+    type_real(res, "residual");
+    at::Tensor s = s0 ? *s0 : c.empty({D.rows, D.d}, res.scalar_type());
+    D.ld_s = matrix(s, "s", c.device, D.rows, D.d);
+    type_is(s, "s", res.scalar_type());
+    D.s_elem = elem(res.scalar_type());
+    at::Tensor y = y0 ? *y0 : c.empty({D.rows, D.d}, at::kBFloat16);
+    D.ld_y = matrix(y, "y", c.device, D.rows, D.d);
+    type_is(y, "y", at::kBFloat16);
+    check(mok_post_pre_rmsnorm_forward(&D, addr(x), addr(res), addr(post), addr(pre), addr(gate),
+                                       addr(s), addr(y), c.raw),
+          "mok_post_pre_rmsnorm_forward");
+    return tuple({s, y});
+  });
+}
+
+// (dy, x, s, post_weight, pre_weight, gate, ds, residual_scale, eps, dx_dtype, dx, dresidual,
+//  dpost, dpre, dgate, accumulate, workspace, stream) -> (dx, dresidual, dpost, dpre, dgate)
+PyObject* py_post_pre_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&] {
+    const at::Tensor& dy = tensor(a[0], "dy");
+    const at::Tensor& x = tensor(a[1], "x");
+    const at::Tensor& s = tensor(a[2], "s");
+    const at::Tensor& post = tensor(a[3], "post_weight");
+    const at::Tensor& pre = tensor(a[4], "pre_weight");
+    const at::Tensor* gate = tensor_or_null(a[5], "gate");
+    const at::Tensor* ds = tensor_or_null(a[6], "ds");
+    const at::Tensor *dx0 = tensor_or_null(a[10], "dx"), *dr0 = tensor_or_null(a[11], "dresidual"),
+                     *dp0 = tensor_or_null(a[12], "dpost"), *dq0 = tensor_or_null(a[13], "dpre"),
+                     *dg0 = tensor_or_null(a[14], "dgate");
+    const bool acc = flag(a[15], "accumulate");
+    const Call c(x, a[17]);
+    mok_post_pre_desc D = post_pre_desc(c, x, post, pre, gate, number(a[7]), number(a[8]));
+    D.ld_y = matrix(dy, "dy", c.device, D.rows, D.d);
+    type_real(dy, "dy");
+    D.ld_s = matrix(s, "s", c.device, D.rows, D.d);
+    type_real(s, "s");
+    if (ds) {
+      D.ld_res = matrix(*ds, "ds", c.device, D.rows, D.d);
+      type_is(*ds, "ds", s.scalar_type());
+    }
+    TORCH_CHECK_VALUE(gate || !dg0, "dgate needs a gate");
+    TORCH_CHECK_VALUE(!acc || (dp0 && dq0 && (dg0 || !gate)),
+                      "accumulate needs dpost, dpre and dgate to add into");
+    const at::ScalarType dt = dtype_or(a[9], (dx0 ? *dx0 : x).scalar_type(), "dx_dtype");
+    TORCH_CHECK_VALUE(real(dt), "dx must not be ", dt);
+    at::Tensor dx = dx0 ? *dx0 : c.empty({D.rows, D.d}, dt);
+    D.ld_dx = matrix(dx, "dx", c.device, D.rows, D.d);
+    type_is(dx, "dx", dt);
+    at::Tensor dr = dr0 ? *dr0 : c.empty({D.rows, D.d}, s.scalar_type());
+    D.ld_dr = matrix(dr, "dresidual", c.device, D.rows, D.d);
+    type_is(dr, "dresidual", s.scalar_type());
+    at::Tensor dp = dp0 ? *dp0 : c.empty({D.d}, at::kFloat);
+    at::Tensor dq = dq0 ? *dq0 : c.empty({D.d}, at::kFloat);
+    at::Tensor dg = dg0 ? *dg0 : (gate ? c.empty(gate->sizes(), at::kFloat) : at::Tensor());
+    dense(dp, "dpost", c.device, {D.d});
+    type_is(dp, "dpost", at::kFloat);
+    dense(dq, "dpre", c.device, {D.d});
+    type_is(dq, "dpre", at::kFloat);
+    if (gate) {
+      dense(dg, "dgate", c.device, gate->sizes());
+      type_is(dg, "dgate", at::kFloat);
+    }
+    D.s_elem = elem(s.scalar_type());
+    D.y_elem = elem(dy.scalar_type());
+    D.dx_elem = elem(dt);
+    D.accumulate = acc;
+    size_t n = 0;
+    check(mok_post_pre_rmsnorm_workspace_size(&D, &n), "mok_post_pre_rmsnorm_workspace_size");
+    const Scratch ws(c, tensor_or_null(a[16], "workspace"), n);
+    check(mok_post_pre_rmsnorm_backward(
+              &D, addr(dy), addr(x), addr(s), addr(post), addr(pre), addr(gate), addr(ds),
+              addr(dx), addr(dr), static_cast<float*>(addr(dp)), static_cast<float*>(addr(dq)),
+              static_cast<float*>(addr(dg)), ws.p, ws.n, c.status(), c.raw),
+          "mok_post_pre_rmsnorm_backward");
+    return tuple({dx, dr, dp, dq, dg});
+  });
+}
+
 // (raise, status): the two callables above
 PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 2) {
@@ -578,6 +763,10 @@ PyMethodDef methods[] = {
     MOK_METHOD(router_balance_backward, 11),
     MOK_METHOD(linear, 11),
     MOK_METHOD(linear_backward, 13),
+    MOK_METHOD(dropout, 8),
+    MOK_METHOD(dropout_backward, 7),
+    MOK_METHOD(post_pre_rmsnorm, 10),
+    MOK_METHOD(post_pre_rmsnorm_backward, 18),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -337,6 +338,25 @@ cudaError_t gemm_linear_dx(int64_t M, int64_t N, int64_t K, const BfParts& dz, c
 cudaError_t gemm_linear_dw(int64_t M, int64_t N, int64_t K, const BfParts& dz, const void* x,
                            int64_t ld_x, float* dw, bool accumulate, int splits, int* status,
                            cudaStream_t st);
+
+// Dropout (dropout.cu): elements whose word is below the threshold are dropped;
+// 2^32 drops them all.
+inline uint64_t dropout_threshold(double p) {
+  return static_cast<uint64_t>(nearbyint(p * 4294967296.0));
+}
+cudaError_t launch_dropout(const mok_dropout_desc& D, const void* x, const void* res,
+                           const int64_t* rng, void* y, cudaStream_t st);
+
+// The norms after and before a block (post_norm.cu); the descriptors' strides
+// filled in.
+cudaError_t launch_post_pre(const mok_post_pre_desc& D, const void* x, const void* res,
+                            const void* w1, const void* w2, const void* gate, void* s, void* y,
+                            cudaStream_t st);
+int64_t post_pre_bwd_blocks(const mok_post_pre_desc& D);  // partial weight gradients [2, .., d]
+cudaError_t launch_post_pre_bwd(const mok_post_pre_desc& D, const void* dy, const void* x,
+                                const void* s, const void* w1, const void* w2, const void* gate,
+                                const void* ds, void* dx, void* dr, float* dw1, float* dw2,
+                                float* dgate, float* part, int* status, cudaStream_t st);
 
 // MXFP8 fake quantisation (mx.cu): rows = blocks along each row, cols =
 // blocks of 32 rows; codes/scales may be null.
