@@ -618,6 +618,42 @@ mok_status mok_post_pre_rmsnorm_backward(const mok_post_pre_desc* desc, const vo
                                          size_t ws_bytes, int32_t* status, void* stream);
 mok_status mok_post_pre_rmsnorm_workspace_size(const mok_post_pre_desc* desc, size_t* bytes);
 
+typedef struct mok_grouped_desc {
+  int64_t rows;          /* R: 0 <= R <= 2^24 */
+  int64_t N, K;          /* widths of y and x: multiples of 8, 8 <= N, K <= 2^20 */
+  int32_t E;             /* groups: 1 <= E <= 512 */
+  int32_t y_elem;        /* forward: mok_elem of y; backward: MOK_ELEM_BF16 (dy) */
+  int32_t dx_elem;       /* backward: mok_elem of dx */
+  int32_t accumulate;    /* backward: 0, or MOK_ADD_DW to add into dw */
+  int64_t ld_x, ld_y;    /* row strides of x, and of y (forward) or dy (backward) */
+  int64_t ld_dx;         /* backward: of dx; each a multiple of 8, 0: contiguous */
+} mok_grouped_desc;
+
+/* Products grouped by expert over ragged rows: rows offsets[e] <= r <
+ * offsets[e+1] of x belong to group e,
+ *   y_r = w_e x_r
+ * x bf16 [R,K], w bf16 [E,N,K], y bf16 or fp32 [R,N], accumulated in fp32 on the
+ * tensor cores and rounded once.  offsets: int32 [E+1] on the device,
+ * nondecreasing from 0 to R (what mok_moe_dispatch_plan writes); groups may be
+ * of any size and empty, no row is padded.  offsets[0] may be above 0 and
+ * offsets[E] below R: rows outside of the groups are neither read nor written.
+ * An offset outside [0, R] is taken as the nearer end and one below an earlier
+ * offset as that one; either sets MOK_ERR_DEVICE_INDEX.  x, w, y 16-byte
+ * aligned.  status: as in mok_router_balance_forward; a bounded wait that gave up
+ * sets MOK_ERR_DEVICE_TIMEOUT. */
+mok_status mok_grouped_linear_forward(const mok_grouped_desc* desc, const void* x, const void* w,
+                                      const int32_t* offsets, void* y, int32_t* status,
+                                      void* stream);
+
+/* Backward from dy bf16 [R,N]:  dx_r = w_e^T dy_r [R,K] (dx_elem),  dw_e fp32
+ * [E,N,K] (+)= the sum over group e's rows of dy_r x_r^T, in a fixed order; each
+ * optional (NULL).  Rows of dx outside of the groups are left as they were; dw of
+ * a group without rows is 0 (or, accumulating, left as it was).  All 16-byte
+ * aligned. */
+mok_status mok_grouped_linear_backward(const mok_grouped_desc* desc, const void* dy,
+                                       const void* x, const void* w, const int32_t* offsets,
+                                       void* dx, float* dw, int32_t* status, void* stream);
+
 /* Waits for `stream`, then reads the device status word at the start of
  * `buf` (the `saved` buffer of forward/backward, or the workspace of the
  * other entry points) into *code (a mok_status; MOK_OK = no device error). */

@@ -64,6 +64,12 @@ class PostPreDesc(ctypes.Structure):
                 ("dx_elem", c_int32), ("accumulate", c_int32)]
 
 
+class GroupedDesc(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("N", c_int64), ("K", c_int64), ("E", c_int32),
+                ("y_elem", c_int32), ("dx_elem", c_int32), ("accumulate", c_int32),
+                ("ld_x", c_int64), ("ld_y", c_int64), ("ld_dx", c_int64)]
+
+
 # name -> (restype, argtypes)
 _SIGS = {
     "mok_moe_workspace_size": (c_int32, [ctypes.POINTER(MoeDesc), ctypes.POINTER(c_size_t),
@@ -119,6 +125,8 @@ _SIGS = {
                                       + [c_size_t, c_void_p, c_void_p]),
     "mok_post_pre_rmsnorm_workspace_size": (c_int32, [ctypes.POINTER(PostPreDesc),
                                                       ctypes.POINTER(c_size_t)]),
+    "mok_grouped_linear_forward": (c_int32, [ctypes.POINTER(GroupedDesc)] + [c_void_p] * 6),
+    "mok_grouped_linear_backward": (c_int32, [ctypes.POINTER(GroupedDesc)] + [c_void_p] * 8),
     "mok_selftest_bounded_wait": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_fill_zero": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_get_device_status": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(c_int32)]),

@@ -293,6 +293,25 @@ def linear_backward(dy, x, w, z=None, *, act="none", bias=False, dx_dtype=None, 
                                   workspace, stream)
 
 
+def grouped_linear(x, w, offsets, *, out_dtype=None, y=None, stream=None):
+    """y[r] = w[e] x[r] for the rows offsets[e] <= r < offsets[e+1] of every expert
+    e (see mok_grouped_linear_forward).  x [R, K] and w [E, N, K] bf16 (N, K and
+    the row strides multiples of 8), offsets int32 [E+1] on the GPU, as
+    `dispatch_plan` writes them; groups of any size.  y [R, N] of out_dtype, bf16
+    (the default) or fp32; its rows outside of the groups are left as they were (of
+    a y that the call makes they hold nothing)."""
+    return _ops().grouped_linear(x, w, offsets, out_dtype, y, stream)
+
+
+def grouped_linear_backward(dy, x, w, offsets, *, dx_dtype=None, dx=None, dw=None,
+                            accumulate=False, stream=None):
+    """Gradients of `grouped_linear` from dy bf16 [R, N] (see
+    mok_grouped_linear_backward): (dx, dw), dx of dx_dtype, bf16 (the default) or
+    fp32, its rows outside of the groups left as they were, dw fp32, added into
+    with `accumulate`."""
+    return _ops().grouped_linear_backward(dy, x, w, offsets, dx_dtype, dx, dw, accumulate, stream)
+
+
 def dropout(x, p, rng, site=0, *, residual=None, out_dtype=None, y=None, stream=None):
     """y = residual + dropout(x) with kept elements over 1 - p (see
     mok_dropout_forward).  rng: int64 [2] on the GPU, the seed and the step (its

@@ -1,6 +1,7 @@
 // C ABI of the operators around the layer (declared in include/mok.h): the
 // residual addition with RMS norm, the router's auxiliary losses, the dense
-// product, dropout and the norms after and before a block.  Argument checks and the order of kernels; nothing is enqueued
+// product, dropout, the norms after and before a block and the products grouped
+// by expert.  Argument checks and the order of kernels; nothing is enqueued
 // before every argument has been checked.
 #include <cuda_runtime.h>
 
@@ -103,6 +104,24 @@ mok_status post_pre_desc(const mok_post_pre_desc* desc, mok_post_pre_desc* D) {
   if (!stride(&D->ld_x, D->d) || !stride(&D->ld_res, D->d) || !stride(&D->ld_s, D->d) ||
       !stride(&D->ld_y, D->d) || !stride(&D->ld_dx, D->d) || !stride(&D->ld_dr, D->d))
     return MOK_ERR_INVALID_ARG;
+  return MOK_OK;
+}
+
+mok_status grouped_desc(const mok_grouped_desc* desc, mok_grouped_desc* D) {
+  if (!desc) return MOK_ERR_INVALID_ARG;
+  *D = *desc;
+  if (D->rows < 0 || D->N <= 0 || D->K <= 0 || D->E <= 0) return MOK_ERR_INVALID_ARG;
+  if (D->rows > (1 << 24) || D->N > (1 << 20) || D->K > (1 << 20) || D->N % 8 || D->K % 8 ||
+      D->E > kMaxExperts)
+    return MOK_ERR_UNSUPPORTED;
+  if (!elem_ok(D->y_elem) || !elem_ok(D->dx_elem)) return MOK_ERR_UNSUPPORTED;
+  if (D->accumulate & ~MOK_ADD_DW) return MOK_ERR_UNSUPPORTED;
+  if (!stride(&D->ld_x, D->K) || !stride(&D->ld_y, D->N) || !stride(&D->ld_dx, D->K))
+    return MOK_ERR_INVALID_ARG;
+  // (the TMA's strides end below 2^40 bytes)
+  if (D->ld_x % 8 || D->ld_y % 8 || D->ld_dx % 8 || D->ld_x >= (1LL << 37) ||
+      D->ld_y >= (1LL << 37) || D->ld_dx >= (1LL << 37))
+    return MOK_ERR_UNSUPPORTED;
   return MOK_OK;
 }
 
@@ -352,6 +371,41 @@ mok_status mok_post_pre_rmsnorm_backward(const mok_post_pre_desc* desc, const vo
                                          dresidual, dpost, dpre, dgate,
                                          static_cast<float*>(workspace), status,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+mok_status mok_grouped_linear_forward(const mok_grouped_desc* desc, const void* x, const void* w,
+                                      const int32_t* offsets, void* y, int32_t* status,
+                                      void* stream) {
+  mok_grouped_desc D;
+  mok_status st = grouped_desc(desc, &D);
+  if (st != MOK_OK) return st;
+  if (!w || !offsets || (D.rows > 0 && (!x || !y))) return MOK_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(offsets, 4) ||
+      !aligned(status, 4))
+    return MOK_ERR_INVALID_ARG;
+  st = mok_check_device();
+  if (st != MOK_OK) return st;
+  return cuda_status(
+      launch_grouped_fwd(D, x, w, offsets, y, status, static_cast<cudaStream_t>(stream)));
+}
+
+mok_status mok_grouped_linear_backward(const mok_grouped_desc* desc, const void* dy,
+                                       const void* x, const void* w, const int32_t* offsets,
+                                       void* dx, float* dw, int32_t* status, void* stream) {
+  mok_grouped_desc D;
+  mok_status st = grouped_desc(desc, &D);
+  if (st != MOK_OK) return st;
+  if (D.y_elem != MOK_ELEM_BF16) return MOK_ERR_UNSUPPORTED;
+  if (!offsets || (dx && !w) || (D.rows > 0 && (!dy || (dw && !x)))) return MOK_ERR_INVALID_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) ||
+      !aligned(dw, 16) || !aligned(offsets, 4) || !aligned(status, 4))
+    return MOK_ERR_INVALID_ARG;
+  st = mok_check_device();
+  if (st != MOK_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dx) st = cuda_status(launch_grouped_dx(D, dy, w, offsets, dx, status, s));
+  if (st == MOK_OK && dw) st = cuda_status(launch_grouped_dw(D, dy, x, offsets, dw, status, s));
+  return st;
 }
 
 }  // extern "C"

@@ -727,6 +727,95 @@ PyObject* py_post_pre_rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t
   });
 }
 
+// ---------------------------------------------------------- grouped_linear --
+
+// A bf16 matrix (or an output's) whose rows the TMA can take: its row stride.
+int64_t tma_rows(const at::Tensor& t, const char* name, const Call& c, int64_t rows,
+                 int64_t cols) {
+  const int64_t ld = matrix(t, name, c.device, rows, cols);
+  TORCH_CHECK_VALUE(ld % 8 == 0, name, " must have a row stride that is a multiple of 8, got ",
+                    ld);
+  return ld;
+}
+
+// x [R, K], w [E, N, K], offsets [E + 1]
+mok_grouped_desc grouped_desc(const Call& c, const at::Tensor& x, const at::Tensor& w,
+                              const at::Tensor& offsets) {
+  mok_grouped_desc D = {};
+  TORCH_CHECK_VALUE(w.dim() == 3, "w must be [experts, N, K]");
+  TORCH_CHECK_VALUE(w.size(0) < (1LL << 31), "the number of experts is 32-bit");
+  D.E = static_cast<int32_t>(w.size(0));
+  D.N = w.size(1);
+  D.K = w.size(2);
+  TORCH_CHECK_VALUE(D.N % 8 == 0 && D.K % 8 == 0, "N and K must be multiples of 8, got ", D.N,
+                    " and ", D.K);
+  dense(w, "w", c.device, {D.E, D.N, D.K});
+  type_is(w, "w", at::kBFloat16);
+  TORCH_CHECK_VALUE(x.dim() == 2, "x must be a matrix");
+  D.rows = x.size(0);
+  D.ld_x = tma_rows(x, "x", c, D.rows, D.K);
+  type_is(x, "x", at::kBFloat16);
+  dense(offsets, "offsets", c.device, {D.E + 1});
+  type_is(offsets, "offsets", at::kInt);
+  return D;
+}
+
+// (x, w, offsets, out_dtype, y, stream) -> y
+PyObject* py_grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&] {
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::Tensor& w = tensor(a[1], "w");
+    const at::Tensor& offsets = tensor(a[2], "offsets");
+    const at::Tensor* y0 = tensor_or_null(a[4], "y");
+    const Call c(x, a[5]);
+    mok_grouped_desc D = grouped_desc(c, x, w, offsets);
+    const at::ScalarType dt =
+        dtype_or(a[3], y0 ? y0->scalar_type() : at::kBFloat16, "out_dtype");
+    TORCH_CHECK_VALUE(real(dt), "y must not be ", dt);
+    at::Tensor y = y0 ? *y0 : c.empty({D.rows, D.N}, dt);
+    D.ld_y = tma_rows(y, "y", c, D.rows, D.N);
+    type_is(y, "y", dt);
+    D.y_elem = elem(dt);
+    check(mok_grouped_linear_forward(&D, addr(x), addr(w), static_cast<int32_t*>(addr(offsets)),
+                                     addr(y), c.status(), c.raw),
+          "mok_grouped_linear_forward");
+    return wrap(y);
+  });
+}
+
+// (dy, x, w, offsets, dx_dtype, dx, dw, accumulate, stream) -> (dx, dw)
+PyObject* py_grouped_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
+  return guarded([&] {
+    const at::Tensor& dy = tensor(a[0], "dy");
+    const at::Tensor& x = tensor(a[1], "x");
+    const at::Tensor& w = tensor(a[2], "w");
+    const at::Tensor& offsets = tensor(a[3], "offsets");
+    const at::Tensor *dx0 = tensor_or_null(a[5], "dx"), *dw0 = tensor_or_null(a[6], "dw");
+    const bool acc = flag(a[7], "accumulate");
+    const Call c(x, a[8]);
+    mok_grouped_desc D = grouped_desc(c, x, w, offsets);
+    D.ld_y = tma_rows(dy, "dy", c, D.rows, D.N);
+    type_is(dy, "dy", at::kBFloat16);
+    TORCH_CHECK_VALUE(dw0 || !acc, "accumulate needs dw to add into");
+    const at::ScalarType dt =
+        dtype_or(a[4], dx0 ? dx0->scalar_type() : at::kBFloat16, "dx_dtype");
+    TORCH_CHECK_VALUE(real(dt), "dx must not be ", dt);
+    at::Tensor dx = dx0 ? *dx0 : c.empty({D.rows, D.K}, dt);
+    D.ld_dx = tma_rows(dx, "dx", c, D.rows, D.K);
+    type_is(dx, "dx", dt);
+    at::Tensor dw = dw0 ? *dw0 : c.empty({D.E, D.N, D.K}, at::kFloat);
+    dense(dw, "dw", c.device, {D.E, D.N, D.K});
+    type_is(dw, "dw", at::kFloat);
+    D.dx_elem = elem(dt);
+    D.accumulate = acc ? MOK_ADD_DW : 0;
+    check(mok_grouped_linear_backward(&D, addr(dy), addr(x), addr(w),
+                                      static_cast<int32_t*>(addr(offsets)), addr(dx),
+                                      static_cast<float*>(addr(dw)), c.status(), c.raw),
+          "mok_grouped_linear_backward");
+    return tuple({dx, dw});
+  });
+}
+
 // (raise, status): the two callables above
 PyObject* py_setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 2) {
@@ -763,6 +852,8 @@ PyMethodDef methods[] = {
     MOK_METHOD(router_balance_backward, 11),
     MOK_METHOD(linear, 11),
     MOK_METHOD(linear_backward, 13),
+    MOK_METHOD(grouped_linear, 6),
+    MOK_METHOD(grouped_linear_backward, 9),
     MOK_METHOD(dropout, 8),
     MOK_METHOD(dropout_backward, 7),
     MOK_METHOD(post_pre_rmsnorm, 10),

@@ -2020,6 +2020,20 @@ bool make_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int esz, const v
   return make_map_t(m, dt, esz, base, inner, outer, row_elems, box_inner, box_rows, swz);
 }
 
+bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int nd,
+                     const uint64_t* dims, const uint64_t* stride_bytes, const uint32_t* box,
+                     CUtensorMapSwizzle swz) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  cuuint64_t d[5], s[4];
+  for (int i = 0; i < nd; ++i) d[i] = dims[i];
+  for (int i = 0; i + 1 < nd; ++i) s[i] = stride_bytes[i];
+  return fn(m, dt, static_cast<cuuint32_t>(nd), const_cast<void*>(base), d, s, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // bf16 operand map, box {64, box_rows}
 static bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                      uint64_t row_elems, uint32_t box_rows) {

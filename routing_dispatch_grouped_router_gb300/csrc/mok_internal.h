@@ -257,6 +257,11 @@ cudaError_t gemm_wgrad_gate_up(const Dims& D, const void* dGU_hi, const void* dG
 bool make_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int esz, const void* base,
                         uint64_t inner, uint64_t outer, uint64_t row_elems, uint32_t box_inner,
                         uint32_t box_rows, CUtensorMapSwizzle swz);
+// ... and one of nd <= 5 dimensions, the first of consecutive elements, the strides
+// of the others in bytes.
+bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int nd,
+                     const uint64_t* dims, const uint64_t* stride_bytes, const uint32_t* box,
+                     CUtensorMapSwizzle swz);
 // C[M,N] fp32 = dequant(A)[M,K] dequant(B)[N,K]^T, MXFP8 operands (E4M3 codes,
 // one E8M0 scale byte per 32 consecutive K values) on block-scaled tcgen05.
 cudaError_t gemm_dense_mxfp8(int64_t M, int64_t N, int64_t K, const uint8_t* A,
@@ -357,6 +362,15 @@ cudaError_t launch_post_pre_bwd(const mok_post_pre_desc& D, const void* dy, cons
                                 const void* s, const void* w1, const void* w2, const void* gate,
                                 const void* ds, void* dx, void* dr, float* dw1, float* dw2,
                                 float* dgate, float* part, int* status, cudaStream_t st);
+
+// Products grouped by expert over ragged rows (grouped.cu); the descriptors'
+// strides filled in.
+cudaError_t launch_grouped_fwd(const mok_grouped_desc& D, const void* x, const void* w,
+                               const int32_t* offsets, void* y, int* status, cudaStream_t st);
+cudaError_t launch_grouped_dx(const mok_grouped_desc& D, const void* dy, const void* w,
+                              const int32_t* offsets, void* dx, int* status, cudaStream_t st);
+cudaError_t launch_grouped_dw(const mok_grouped_desc& D, const void* dy, const void* x,
+                              const int32_t* offsets, float* dw, int* status, cudaStream_t st);
 
 // MXFP8 fake quantisation (mx.cu): rows = blocks along each row, cols =
 // blocks of 32 rows; codes/scales may be null.
