@@ -591,11 +591,13 @@ typedef struct mok_post_pre_desc {
  * [d], [rows] or NULL, as desc->gate says.  s may equal residual, or x of the
  * same type (same strides).  Any pointer aligned to its element and any row
  * stride >= d is taken; 16-byte aligned rows with d a multiple of 8 run at full
- * width. */
+ * width, and so do rows of other lengths in 16-byte aligned tensors whose strides
+ * agree modulo 8.  status: as in mok_router_balance_forward; a bounded wait that
+ * gave up sets MOK_ERR_DEVICE_TIMEOUT. */
 mok_status mok_post_pre_rmsnorm_forward(const mok_post_pre_desc* desc, const void* x,
                                         const void* residual, const void* post_weight,
                                         const void* pre_weight, const void* gate, void* s,
-                                        void* y, void* stream);
+                                        void* y, int32_t* status, void* stream);
 
 /* Backward, from dy [rows,d] of y and ds [rows,d] (s_elem; NULL: none) that
  * reaches s by other ways.  With n, m the normalised x and s:

@@ -120,7 +120,7 @@ _SIGS = {
                                             ctypes.POINTER(c_size_t)]),
     "mok_dropout_forward": (c_int32, [ctypes.POINTER(DropoutDesc)] + [c_void_p] * 5),
     "mok_dropout_backward": (c_int32, [ctypes.POINTER(DropoutDesc)] + [c_void_p] * 4),
-    "mok_post_pre_rmsnorm_forward": (c_int32, [ctypes.POINTER(PostPreDesc)] + [c_void_p] * 8),
+    "mok_post_pre_rmsnorm_forward": (c_int32, [ctypes.POINTER(PostPreDesc)] + [c_void_p] * 9),
     "mok_post_pre_rmsnorm_backward": (c_int32, [ctypes.POINTER(PostPreDesc)] + [c_void_p] * 13
                                       + [c_size_t, c_void_p, c_void_p]),
     "mok_post_pre_rmsnorm_workspace_size": (c_int32, [ctypes.POINTER(PostPreDesc),

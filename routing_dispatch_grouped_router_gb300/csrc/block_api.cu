@@ -312,7 +312,7 @@ mok_status mok_dropout_backward(const mok_dropout_desc* desc, const void* dy, co
 mok_status mok_post_pre_rmsnorm_forward(const mok_post_pre_desc* desc, const void* x,
                                         const void* residual, const void* post_weight,
                                         const void* pre_weight, const void* gate, void* s,
-                                        void* y, void* stream) {
+                                        void* y, int32_t* status, void* stream) {
   mok_post_pre_desc D;
   mok_status st = post_pre_desc(desc, &D);
   if (st != MOK_OK) return st;
@@ -322,12 +322,12 @@ mok_status mok_post_pre_rmsnorm_forward(const mok_post_pre_desc* desc, const voi
   const size_t se = elem_size(D.s_elem), we = elem_size(D.weight_elem);
   if (!aligned(x, elem_size(D.x_elem)) || !aligned(residual, se) || !aligned(s, se) ||
       !aligned(y, 2) || !aligned(post_weight, we) || !aligned(pre_weight, we) ||
-      !aligned(gate, elem_size(D.gate_elem)))
+      !aligned(gate, elem_size(D.gate_elem)) || !aligned(status, 4))
     return MOK_ERR_INVALID_ARG;
   st = mok_check_device();
   if (st != MOK_OK) return st;
   return cuda_status(launch_post_pre(D, x, residual, post_weight, pre_weight, gate, s, y,
-                                     static_cast<cudaStream_t>(stream)));
+                                     status, static_cast<cudaStream_t>(stream)));
 }
 
 mok_status mok_post_pre_rmsnorm_workspace_size(const mok_post_pre_desc* desc, size_t* bytes) {

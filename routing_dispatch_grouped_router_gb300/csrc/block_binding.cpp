@@ -658,7 +658,7 @@ PyObject* py_post_pre_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t) {
     D.ld_y = matrix(y, "y", c.device, D.rows, D.d);
     type_is(y, "y", at::kBFloat16);
     check(mok_post_pre_rmsnorm_forward(&D, addr(x), addr(res), addr(post), addr(pre), addr(gate),
-                                       addr(s), addr(y), c.raw),
+                                       addr(s), addr(y), c.status(), c.raw),
           "mok_post_pre_rmsnorm_forward");
     return tuple({s, y});
   });

@@ -356,7 +356,7 @@ cudaError_t launch_dropout(const mok_dropout_desc& D, const void* x, const void*
 // filled in.
 cudaError_t launch_post_pre(const mok_post_pre_desc& D, const void* x, const void* res,
                             const void* w1, const void* w2, const void* gate, void* s, void* y,
-                            cudaStream_t st);
+                            int* status, cudaStream_t st);
 int64_t post_pre_bwd_blocks(const mok_post_pre_desc& D);  // partial weight gradients [2, .., d]
 cudaError_t launch_post_pre_bwd(const mok_post_pre_desc& D, const void* dy, const void* x,
                                 const void* s, const void* w1, const void* w2, const void* gate,

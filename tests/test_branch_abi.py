@@ -78,20 +78,20 @@ def test_dropout_pointers_refused(lib):
 def test_norms_descriptors_refused(lib, kw, code):
     n = ctypes.c_size_t()
     assert lib.mok_post_pre_rmsnorm_workspace_size(norms(**kw), n) == code
-    assert lib.mok_post_pre_rmsnorm_forward(norms(**kw), A, A, A, A, None, A, A, None) == code
+    assert lib.mok_post_pre_rmsnorm_forward(norms(**kw), A, A, A, A, None, A, A, None, None) == code
 
 
 def test_norms_pointers_refused(lib):
     f = lib.mok_post_pre_rmsnorm_forward
-    for missing in range(7):
-        args = [A, A, A, A, None, A, A]
-        args[missing if missing < 4 else missing] = None
-        if missing != 4:
-            assert f(norms(), *args, None) == 1
-    assert f(norms(gate=1), A, A, A, A, None, A, A, None) == 1    # no gate
-    assert f(norms(), A, A, A, A, A, A, A, None) == 1             # one that is not asked for
-    assert f(norms(), P(4097), A, A, A, None, A, A, None) == 1
-    assert f(norms(), A, A, P(4098), A, None, A, A, None) == 1    # an fp32 weight at 2 bytes
+    for missing in (0, 1, 2, 3, 5, 6):
+        args = [A, A, A, A, None, A, A, None, None]
+        args[missing] = None
+        assert f(norms(), *args) == 1
+    assert f(norms(gate=1), A, A, A, A, None, A, A, None, None) == 1  # no gate
+    assert f(norms(), A, A, A, A, A, A, A, None, None) == 1           # one not asked for
+    assert f(norms(), P(4097), A, A, A, None, A, A, None, None) == 1
+    assert f(norms(), A, A, P(4098), A, None, A, A, None, None) == 1  # an fp32 weight at 2 bytes
+    assert f(norms(), A, A, A, A, None, A, A, P(4098), None) == 1
     b = lib.mok_post_pre_rmsnorm_backward
     n = ctypes.c_size_t()
     assert lib.mok_post_pre_rmsnorm_workspace_size(norms(), n) == 0 and n.value >= 2 * 4 * 64
