@@ -5,9 +5,6 @@
 // u of element n = row d + column is word n mod 4 of Philox4x32-10 at the counter
 // (n / 4, step, site) under the key seed, so that no mask is stored: the backward,
 // the same map of dy without a residual, draws it again.
-//
-// Bound by HBM bytes: 20 wide multiplications per four elements stay below the
-// time of their 16 to 48 bytes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,20 +22,13 @@ struct DropArgs {
   void* y;
   long long rows, ld_x, ld_r, ld_y;
   long long cols;    // elements of a row as it is walked (FLAT: all of them, one row)
-  long long groups;  // groups of a row: 8 elements (VEC), or the row's blocks of four
+  long long groups;  // groups of a row: 8 elements, or the row's blocks of four (kAny)
   uint32_t threshold, site;
   float scale;
   int all;  // every element is dropped
 };
 
 namespace {
-
-__device__ __forceinline__ uint4 words(const DropArgs& a, uint2 key, uint32_t step,
-                                       uint64_t block) {
-  return philox4x32_10(make_uint4(static_cast<uint32_t>(block), static_cast<uint32_t>(block >> 32),
-                                  step, a.site),
-                       key);
-}
 
 template <bool F32>
 __device__ __forceinline__ void get8(const void* base, long long i, float (&o)[8]) {
@@ -78,78 +68,113 @@ __device__ __forceinline__ void put1(void* base, long long i, float v) {
 
 }  // namespace
 
-// VEC: rows of whole, aligned groups of eight elements (contiguous tensors: one row
-// of them all, its last elements apart).  Otherwise a group is a block of the
-// generator, of whose four elements those of the row are taken one by one.
-template <bool XF32, bool YF32, bool VEC>
-__global__ void __launch_bounds__(256) dropout_kernel(DropArgs a) {
+// How the elements are walked: kFlat, contiguous tensors as one row of groups of
+// eight (its last elements apart); kRows, rows of whole groups at their strides; kAny,
+// rows of any length and alignment, a block of the generator at a time, of whose four
+// elements those of the row are taken one by one.
+enum class Walk { kFlat, kRows, kAny };
+constexpr int kBlocks = 5;  // of an SM
+
+// A group of eight per thread and step, its two blocks of the generator round by round
+// together.  SMALL: fewer than 2^34 elements, so that the counter's second word is 0:
+// the first two rounds' products of what is alike for all blocks then leave the loop,
+// 18 of 20 stay.
+//
+// Bound by HBM bytes where there are 8 or more of them per element (8192 x 7168, fp32
+// and a bf16 residual in: 69 us, floor 70), else by the products: a wide multiplication
+// holds its pipe for several cycles (bf16 alone 58 us, floor 35).  Blocks of 256
+// threads, five on an SM (two groups per thread 72 and 70 us; eight blocks of 32
+// registers 109 and 74).
+template <bool XF32, bool YF32, Walk W, bool SMALL>
+__global__ void __launch_bounds__(256, kBlocks) dropout_kernel(DropArgs a) {
+  using Index = std::conditional_t<SMALL, uint32_t, uint64_t>;
   grid_dep_launch();
   grid_dep_wait();
   const uint64_t seed = static_cast<uint64_t>(a.rng[0]);
   const uint2 key = make_uint2(static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32));
   const uint32_t step = static_cast<uint32_t>(a.rng[1]);
-  auto drop = [&](float x, uint32_t u, float r) {
-    return u >= a.threshold && !a.all ? fmaf(x, a.scale, r) : r;
+  auto counter = [&](uint64_t block) {
+    return make_uint4(static_cast<uint32_t>(block),
+                      SMALL ? 0u : static_cast<uint32_t>(block >> 32), step, a.site);
   };
-  // (one division; then row and group advance together)
-  const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  long long row = first / a.groups, g = first - row * a.groups;
-  const long long row_step = stride / a.groups, g_step = stride - row_step * a.groups;
-  while (row < a.rows) {
-    if (VEC) {
-      const uint64_t n = static_cast<uint64_t>(row) * a.cols + 8 * g;
-      const long long ix = row * a.ld_x + 8 * g, ir = row * a.ld_r + 8 * g,
-                      iy = row * a.ld_y + 8 * g;
-      if (8 * g + 8 <= a.cols) {
-        float x[8], r[8];
-        get8<XF32>(a.x, ix, x);
-        if (a.r) {
-          get8<YF32>(a.r, ir, r);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) r[j] = 0.f;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 u = words(a, key, step, n / 4 + h);
-          x[4 * h] = drop(x[4 * h], u.x, r[4 * h]);
-          x[4 * h + 1] = drop(x[4 * h + 1], u.y, r[4 * h + 1]);
-          x[4 * h + 2] = drop(x[4 * h + 2], u.z, r[4 * h + 2]);
-          x[4 * h + 3] = drop(x[4 * h + 3], u.w, r[4 * h + 3]);
-        }
-        put8<YF32>(a.y, iy, x);
-      } else {  // the last elements of a contiguous tensor
-        const int left = static_cast<int>(a.cols - 8 * g);
-        for (int j = 0; j < left; ++j) {
-          const uint4 u = words(a, key, step, (n + j) / 4);
-          const uint32_t w = (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
-          put1<YF32>(a.y, iy + j,
-                     drop(get1<XF32>(a.x, ix + j), w, a.r ? get1<YF32>(a.r, ir + j) : 0.f));
-        }
-      }
-    } else {
+  // (where all are dropped, x is not read but 0)
+  auto drop = [&](float x, uint32_t u, float r) {
+    return u >= a.threshold ? fmaf(x, a.scale, r) : r;
+  };
+  const Index stride = gridDim.x * static_cast<Index>(blockDim.x);
+  const Index total = static_cast<Index>(a.rows * a.groups);
+  const Index groups = static_cast<Index>(a.groups);
+  for (Index i = blockIdx.x * static_cast<Index>(blockDim.x) + threadIdx.x; i < total;
+       i += stride) {
+    if (W == Walk::kAny) {
+      const Index row = i / groups, g = i - row * groups;
       const uint64_t n0 = static_cast<uint64_t>(row) * a.cols;  // the row's first element
       const uint64_t block = n0 / 4 + g;
-      const uint4 u = words(a, key, step, block);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      uint4 u[1] = {counter(block)};
+      philox4x32_10(u, key);
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const long long c = static_cast<long long>(block * 4 + j - n0);
         if (c < 0 || c >= a.cols) continue;
         put1<YF32>(a.y, row * a.ld_y + c,
-                   drop(get1<XF32>(a.x, row * a.ld_x + c), w[j],
+                   drop(a.all ? 0.f : get1<XF32>(a.x, row * a.ld_x + c), w[j],
                         a.r ? get1<YF32>(a.r, row * a.ld_r + c) : 0.f));
       }
+      continue;
     }
-    row += row_step;
-    g += g_step;
-    if (g >= a.groups) {
-      g -= a.groups;
-      ++row;
+    uint64_t n;  // the group's first element
+    long long ix, ir, iy;
+    if (W == Walk::kFlat) {
+      n = 8 * static_cast<uint64_t>(i);
+      if (static_cast<long long>(n) + 8 > a.cols) break;
+      ix = ir = iy = static_cast<long long>(n);
+    } else {
+      const Index row = i / groups;
+      const long long c = 8 * static_cast<long long>(i - row * groups);
+      n = static_cast<uint64_t>(row) * a.cols + c;
+      ix = row * a.ld_x + c;
+      ir = row * a.ld_r + c;
+      iy = row * a.ld_y + c;
     }
+    float x[8], r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = r[e] = 0.f;
+    if (!a.all) get8<XF32>(a.x, ix, x);
+    if (a.r) get8<YF32>(a.r, ir, r);
+    uint4 u[2] = {counter(n / 4), counter(n / 4 + 1)};
+    philox4x32_10(u, key);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x[4 * h] = drop(x[4 * h], u[h].x, r[4 * h]);
+      x[4 * h + 1] = drop(x[4 * h + 1], u[h].y, r[4 * h + 1]);
+      x[4 * h + 2] = drop(x[4 * h + 2], u[h].z, r[4 * h + 2]);
+      x[4 * h + 3] = drop(x[4 * h + 3], u[h].w, r[4 * h + 3]);
+    }
+    put8<YF32>(a.y, iy, x);
+  }
+  if (W == Walk::kFlat && blockIdx.x == 0 && threadIdx.x < a.cols % 8) {  // the last elements
+    const long long n = a.cols / 8 * 8 + threadIdx.x;
+    uint4 u[1] = {counter(static_cast<uint64_t>(n) / 4)};
+    philox4x32_10(u, key);
+    const int j = threadIdx.x & 3;
+    const uint32_t w = j == 0 ? u[0].x : j == 1 ? u[0].y : j == 2 ? u[0].z : u[0].w;
+    put1<YF32>(a.y, n, drop(a.all ? 0.f : get1<XF32>(a.x, n), w,
+                            a.r ? get1<YF32>(a.r, n) : 0.f));
   }
 }
+
+namespace {
+
+template <bool XF32, bool YF32, Walk W>
+cudaError_t launch(const DropArgs& a, bool small, cudaStream_t st) {
+  const long long blocks = (a.rows * a.groups + 255) / 256, most = kGb300Sms * kBlocks;
+  return launch_dependent(
+      small ? dropout_kernel<XF32, YF32, W, true> : dropout_kernel<XF32, YF32, W, false>,
+      dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st, a);
+}
+
+}  // namespace
 
 cudaError_t launch_dropout(const mok_dropout_desc& D, const void* x, const void* res,
                            const int64_t* rng, void* y, cudaStream_t st) {
@@ -175,14 +200,17 @@ cudaError_t launch_dropout(const mok_dropout_desc& D, const void* x, const void*
   if (a.rows > 1)
     vec = vec && a.cols % 8 == 0 && a.ld_x * xe % 16 == 0 && a.ld_y * ye % 16 == 0 &&
           (!res || a.ld_r * ye % 16 == 0);
-  a.groups = vec ? (a.cols + 7) / 8 : (a.cols + 3) / 4 + (a.rows > 1 ? 1 : 0);
-  const long long blocks = (a.rows * a.groups + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(blocks < kGb300Sms * 8 ? blocks : kGb300Sms * 8);
+  const Walk walk = !vec ? Walk::kAny : a.rows > 1 ? Walk::kRows : Walk::kFlat;
+  a.groups = walk == Walk::kRows   ? a.cols / 8
+             : walk == Walk::kFlat ? (a.cols + 7) / 8
+                                   : (a.cols + 3) / 4 + (a.rows > 1 ? 1 : 0);
+  const bool small = D.rows * D.d < (1LL << 34) && a.rows * a.groups < (1LL << 31);
   ProfScope prof("dropout", st);
   auto run = [&](auto X, auto Y) {
     constexpr bool f = decltype(X)::value, g = decltype(Y)::value;
-    return launch_dependent(vec ? dropout_kernel<f, g, true> : dropout_kernel<f, g, false>,
-                            dim3(grid), dim3(256), 0, st, a);
+    return walk == Walk::kFlat   ? launch<f, g, Walk::kFlat>(a, small, st)
+           : walk == Walk::kRows ? launch<f, g, Walk::kRows>(a, small, st)
+                                 : launch<f, g, Walk::kAny>(a, small, st);
   };
   cudaError_t e;
   if (xf) e = yf ? run(std::true_type(), std::true_type()) : run(std::true_type(), std::false_type());

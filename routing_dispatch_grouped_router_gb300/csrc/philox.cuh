@@ -7,17 +7,22 @@
 
 namespace mok {
 
-__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint2 k) {
+// Of N counters under one key, round by round: a round waits for its products, and
+// the counters share its key.
+template <int N>
+__device__ __forceinline__ void philox4x32_10(uint4 (&c)[N], uint2 k) {
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u;
-    const uint64_t b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k.x, static_cast<uint32_t>(b),
-                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k.y, static_cast<uint32_t>(a));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint64_t a = static_cast<uint64_t>(c[i].x) * 0xD2511F53u;
+      const uint64_t b = static_cast<uint64_t>(c[i].z) * 0xCD9E8D57u;
+      c[i] = make_uint4(static_cast<uint32_t>(b >> 32) ^ c[i].y ^ k.x, static_cast<uint32_t>(b),
+                        static_cast<uint32_t>(a >> 32) ^ c[i].w ^ k.y, static_cast<uint32_t>(a));
+    }
     k.x += 0x9E3779B9u;
     k.y += 0xBB67AE85u;
   }
-  return c;
 }
 
 }  // namespace mok
