@@ -333,11 +333,14 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       const uint32_t full_leader = PAIR ? mapa_shared(smem_addr(full), 0) : 0u;
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t armed = 0, armed_par = 0;  // stages whose barrier this CTA armed, and its phase
+      uint32_t steps = 0;  // stages filled
       bool ok = true;
       for (int i = 0; unit(i) < total && ok; ++i) {
         const Tile tl = tile_at(unit(i));
-        for (int kb = 0; kb < tl.num_kb; ++kb) {
+        const int n0 = tl.n_tile * BN + rank * C::B_ROWS;
+        uint32_t bytes = (MODE == GRP_DW ? C::A_BYTES : a_bytes(tl.rows)) + C::B_BYTES;
+        if (PAIR) bytes += (MODE == GRP_DW ? C::A_BYTES : a_bytes(tl.other)) + C::B_BYTES;
+        for (int kb = 0; kb < tl.num_kb; ++kb, ++steps) {
           if (!wait(&empty[stage], phase ^ 1u)) {
             ok = false;
             break;
@@ -345,16 +348,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           uint8_t* sA = smem + stage * C::STAGE_BYTES;
           uint8_t* sB = sA + C::A_BYTES;
           const uint32_t bar_c = full_leader + 8u * stage;
-          const uint32_t mine = (MODE == GRP_DW ? C::A_BYTES : a_bytes(tl.rows)) + C::B_BYTES;
-          if (leader) {
-            const uint32_t bit = 1u << stage;
-            uint32_t bytes = mine;
-            if (PAIR) bytes += (MODE == GRP_DW ? C::A_BYTES : a_bytes(tl.other)) + C::B_BYTES;
-            mbar_arrive_expect_tx(&full[stage], bytes);
-            armed |= bit;
-            armed_par = phase ? armed_par | bit : armed_par & ~bit;
-          }
-          const int n0 = tl.n_tile * BN + rank * C::B_ROWS;
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           if (MODE != GRP_DW) {
             auto rows = [&](const CUtensorMap* tm, int r) {
               uint8_t* dst = sA + r * 128;
@@ -398,9 +392,12 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
         // let the copies already issued land before the CTA can exit
         const int zero = 0;
-        for (int s = 0; s < C::STAGES; ++s)
-          if (armed >> s & 1u) mbar_wait(&full[s], armed_par >> s & 1u, &zero);
-        if (PAIR && !leader) spin_ns(1000000ull);
+        if (leader) {
+          for (uint32_t s = 0; s < C::STAGES && s < steps; ++s)
+            mbar_wait(&full[s], (steps - 1 - s) / C::STAGES & 1u, &zero);
+        } else {
+          spin_ns(1000000ull);
+        }
       }
     }
   } else if (warp == 1) {
@@ -408,7 +405,17 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     if (lane == 0 && leader) {
       constexpr uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, BN, A_MN, B_MN);
       constexpr uint32_t lbo_a = A_MN ? 8192u : 16u, lbo_b = B_MN ? 8192u : 16u;
-      constexpr uint32_t kstep_a = A_MN ? 2048u : 32u, kstep_b = B_MN ? 2048u : 32u;
+      // One thread issues the MMAs, and what it does per K block counts (a select of
+      // two descriptors made 64 groups of 512 rows, N = K = 2048, 182 -> 193 us):
+      // descriptors are their first stage's, whose low words take the stage's and the
+      // step's offsets in sixteens.
+      constexpr uint32_t kstep_a = A_MN ? 128u : 2u, kstep_b = B_MN ? 128u : 2u;
+      const uint32_t base = smem_addr(smem);
+      const uint64_t ad0 = smem_desc_sw128(base, lbo_a, 1024);
+      const uint64_t bd0 = smem_desc_sw128(base + C::A_BYTES, lbo_b, 1024);
+      auto word = [](uint64_t d, uint32_t lo) {
+        return (d & 0xffffffff00000000ull) | lo;
+      };
       auto commit = [&](uint64_t* bar) {
         if (PAIR) mma_commit_pair(bar);
         else mma_commit(bar);
@@ -446,14 +453,13 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           int mmas = 4;
           if (MODE == GRP_DW && kb == tl.num_kb - 1 && (tl.kn & 63)) mmas = (tl.kn & 63) >> 4;
           tc_fence_after_sync();
-          const uint32_t a_base = smem_addr(smem + stage * C::STAGE_BYTES);
-          const uint32_t b_base = a_base + C::A_BYTES;
+          const uint32_t x = static_cast<uint32_t>(ad0) + stage * (C::STAGE_BYTES / 16);
+          const uint32_t y = static_cast<uint32_t>(bd0) + stage * (C::STAGE_BYTES / 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (MODE == GRP_DW && j >= mmas) break;
-            const uint64_t ad = smem_desc_sw128(a_base + j * kstep_a, lbo_a, 1024);
-            const uint64_t bd = smem_desc_sw128(b_base + j * kstep_b, lbo_b, 1024);
-            const uint32_t acc = ((kb - kb0) | j) != 0 ? 1u : 0u;
+            const uint64_t ad = word(ad0, x + j * kstep_a), bd = word(bd0, y + j * kstep_b);
+            const uint32_t acc = j > 0 ? 1u : (kb != kb0 ? 1u : 0u);
             if (PAIR) mma_bf16_pair(d_tmem, ad, bd, idesc, acc);
             else mma_bf16(d_tmem, ad, bd, idesc, acc);
           }
@@ -792,11 +798,12 @@ cudaError_t rows_product(const char* name, const mok_grouped_desc& D, const void
   // N = K = 1024: 14.5 us, wide 16.8; 16384 in 64, N = K = 2048: 176 and 146).
   if (most_tiles(D, 128) * ((cols + 255) / 256) < kGb300Sms)
     return run(std::integral_constant<int, 128>(), No());
-  // Pairs halve what an SM reads per product, and round a group up to 256 rows:
-  // 32768 rows of N = K = 2048 in 8, 32, 64 groups 159, 176, 217 us (one CTA a tile:
-  // 173, 200, 222), in even groups of 256 and 384 rows alike, zipf groups of 128 on
-  // average 324 us (311).
-  if (D.rows >= 512LL * D.E) return run(std::integral_constant<int, 256>(), Yes());
+  // Pairs halve what an SM reads per product, and round a group up to 256 rows (N = K
+  // = 2048, even groups of 192 rows: 121 us, one CTA a tile 128; 256: alike; 512: 211
+  // and 222; 4096: 160 and 173; zipf groups of 128 rows on average, 4096 x 1536: 335
+  // and 314).  (Short tiles with the weights as the MMA's M, or all of them so, won 2%
+  // where groups end in them and lost 4% elsewhere.)
+  if (D.rows >= 160LL * D.E) return run(std::integral_constant<int, 256>(), Yes());
   return run(std::integral_constant<int, 256>(), No());
 }
 
