@@ -651,10 +651,12 @@ mok_status mok_grouped_linear_forward(const mok_grouped_desc* desc, const void* 
  * [E,N,K] (+)= the sum over group e's rows of dy_r x_r^T, in a fixed order; each
  * optional (NULL).  Rows of dx outside of the groups are left as they were; dw of
  * a group without rows is 0 (or, accumulating, left as it was).  All 16-byte
- * aligned. */
+ * aligned.  workspace: see the size query (for dw; NULL where it says 0). */
 mok_status mok_grouped_linear_backward(const mok_grouped_desc* desc, const void* dy,
                                        const void* x, const void* w, const int32_t* offsets,
-                                       void* dx, float* dw, int32_t* status, void* stream);
+                                       void* dx, float* dw, void* workspace, size_t ws_bytes,
+                                       int32_t* status, void* stream);
+mok_status mok_grouped_linear_workspace_size(const mok_grouped_desc* desc, size_t* bytes);
 
 /* Waits for `stream`, then reads the device status word at the start of
  * `buf` (the `saved` buffer of forward/backward, or the workspace of the

@@ -126,7 +126,10 @@ _SIGS = {
     "mok_post_pre_rmsnorm_workspace_size": (c_int32, [ctypes.POINTER(PostPreDesc),
                                                       ctypes.POINTER(c_size_t)]),
     "mok_grouped_linear_forward": (c_int32, [ctypes.POINTER(GroupedDesc)] + [c_void_p] * 6),
-    "mok_grouped_linear_backward": (c_int32, [ctypes.POINTER(GroupedDesc)] + [c_void_p] * 8),
+    "mok_grouped_linear_backward": (c_int32, [ctypes.POINTER(GroupedDesc)] + [c_void_p] * 7
+                                    + [c_size_t, c_void_p, c_void_p]),
+    "mok_grouped_linear_workspace_size": (c_int32, [ctypes.POINTER(GroupedDesc),
+                                                    ctypes.POINTER(c_size_t)]),
     "mok_selftest_bounded_wait": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_fill_zero": (c_int32, [c_void_p, c_size_t, c_void_p]),
     "mok_get_device_status": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(c_int32)]),

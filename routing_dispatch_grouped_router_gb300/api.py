@@ -304,12 +304,13 @@ def grouped_linear(x, w, offsets, *, out_dtype=None, y=None, stream=None):
 
 
 def grouped_linear_backward(dy, x, w, offsets, *, dx_dtype=None, dx=None, dw=None,
-                            accumulate=False, stream=None):
+                            accumulate=False, workspace=None, stream=None):
     """Gradients of `grouped_linear` from dy bf16 [R, N] (see
     mok_grouped_linear_backward): (dx, dw), dx of dx_dtype, bf16 (the default) or
     fp32, its rows outside of the groups left as they were, dw fp32, added into
     with `accumulate`."""
-    return _ops().grouped_linear_backward(dy, x, w, offsets, dx_dtype, dx, dw, accumulate, stream)
+    return _ops().grouped_linear_backward(dy, x, w, offsets, dx_dtype, dx, dw, accumulate,
+                                          workspace, stream)
 
 
 def dropout(x, p, rng, site=0, *, residual=None, out_dtype=None, y=None, stream=None):

@@ -389,22 +389,37 @@ mok_status mok_grouped_linear_forward(const mok_grouped_desc* desc, const void* 
       launch_grouped_fwd(D, x, w, offsets, y, status, static_cast<cudaStream_t>(stream)));
 }
 
+mok_status mok_grouped_linear_workspace_size(const mok_grouped_desc* desc, size_t* bytes) {
+  mok_grouped_desc D;
+  const mok_status st = grouped_desc(desc, &D);
+  if (st != MOK_OK) return st;
+  if (!bytes) return MOK_ERR_INVALID_ARG;
+  *bytes = grouped_ws_bytes(D);
+  return MOK_OK;
+}
+
 mok_status mok_grouped_linear_backward(const mok_grouped_desc* desc, const void* dy,
                                        const void* x, const void* w, const int32_t* offsets,
-                                       void* dx, float* dw, int32_t* status, void* stream) {
+                                       void* dx, float* dw, void* workspace, size_t ws_bytes,
+                                       int32_t* status, void* stream) {
   mok_grouped_desc D;
   mok_status st = grouped_desc(desc, &D);
   if (st != MOK_OK) return st;
   if (D.y_elem != MOK_ELEM_BF16) return MOK_ERR_UNSUPPORTED;
   if (!offsets || (dx && !w) || (D.rows > 0 && (!dy || (dw && !x)))) return MOK_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dx, 16) ||
-      !aligned(dw, 16) || !aligned(offsets, 4) || !aligned(status, 4))
+      !aligned(dw, 16) || !aligned(offsets, 4) || !aligned(workspace, 16) || !aligned(status, 4))
     return MOK_ERR_INVALID_ARG;
+  if (dw) {
+    const size_t need = grouped_ws_bytes(D);
+    if (need > 0 && !workspace) return MOK_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOK_ERR_WORKSPACE;
+  }
   st = mok_check_device();
   if (st != MOK_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dx) st = cuda_status(launch_grouped_dx(D, dy, w, offsets, dx, status, s));
-  if (st == MOK_OK && dw) st = cuda_status(launch_grouped_dw(D, dy, x, offsets, dw, status, s));
+  if (st == MOK_OK && dw) st = cuda_status(launch_grouped_dw(D, dy, x, offsets, dw, workspace, status, s));
   return st;
 }
 

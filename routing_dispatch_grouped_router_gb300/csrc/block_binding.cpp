@@ -783,7 +783,7 @@ PyObject* py_grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t) {
   });
 }
 
-// (dy, x, w, offsets, dx_dtype, dx, dw, accumulate, stream) -> (dx, dw)
+// (dy, x, w, offsets, dx_dtype, dx, dw, accumulate, workspace, stream) -> (dx, dw)
 PyObject* py_grouped_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) {
   return guarded([&] {
     const at::Tensor& dy = tensor(a[0], "dy");
@@ -792,7 +792,7 @@ PyObject* py_grouped_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) 
     const at::Tensor& offsets = tensor(a[3], "offsets");
     const at::Tensor *dx0 = tensor_or_null(a[5], "dx"), *dw0 = tensor_or_null(a[6], "dw");
     const bool acc = flag(a[7], "accumulate");
-    const Call c(x, a[8]);
+    const Call c(x, a[9]);
     mok_grouped_desc D = grouped_desc(c, x, w, offsets);
     D.ld_y = tma_rows(dy, "dy", c, D.rows, D.N);
     type_is(dy, "dy", at::kBFloat16);
@@ -808,9 +808,13 @@ PyObject* py_grouped_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t) 
     type_is(dw, "dw", at::kFloat);
     D.dx_elem = elem(dt);
     D.accumulate = acc ? MOK_ADD_DW : 0;
+    size_t n = 0;
+    check(mok_grouped_linear_workspace_size(&D, &n), "mok_grouped_linear_workspace_size");
+    const Scratch ws(c, tensor_or_null(a[8], "workspace"), n);
     check(mok_grouped_linear_backward(&D, addr(dy), addr(x), addr(w),
                                       static_cast<int32_t*>(addr(offsets)), addr(dx),
-                                      static_cast<float*>(addr(dw)), c.status(), c.raw),
+                                      static_cast<float*>(addr(dw)), ws.p, ws.n, c.status(),
+                                      c.raw),
           "mok_grouped_linear_backward");
     return tuple({dx, dw});
   });
@@ -853,7 +857,7 @@ PyMethodDef methods[] = {
     MOK_METHOD(linear, 11),
     MOK_METHOD(linear_backward, 13),
     MOK_METHOD(grouped_linear, 6),
-    MOK_METHOD(grouped_linear_backward, 9),
+    MOK_METHOD(grouped_linear_backward, 10),
     MOK_METHOD(dropout, 8),
     MOK_METHOD(dropout_backward, 7),
     MOK_METHOD(post_pre_rmsnorm, 10),

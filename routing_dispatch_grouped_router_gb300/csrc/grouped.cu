@@ -36,6 +36,7 @@ struct GroupedArgs {
   int cols;       // columns of C
   int num_kb;     // FWD, DX: 64-value blocks of the sum
   int m_tiles;    // DW: row tiles of C (PAIR: of 256 rows)
+  int splits;     // DW: parts of a group's rows, each with a C of its own
   int n_tiles;
   long long ld_out;  // row stride of C
   void* out;
@@ -179,19 +180,30 @@ __device__ __forceinline__ Tile tile_of(const GroupedArgs& a, const int* off, co
   Tile tl;
   if (MODE == GRP_DW) {
     const int per = a.m_tiles * a.n_tiles;
-    const int nth = static_cast<int>(t / per);
-    tl.e = pre[nth];
-    const int local = static_cast<int>(t - static_cast<long long>(nth) * per);
+    const int part = static_cast<int>(t / per);
+    const int nth = part / a.splits, split = part - nth * a.splits;
+    const int local = static_cast<int>(t - static_cast<long long>(part) * per);
     int m;
     place(local, a.m_tiles, a.n_tiles, &m, &tl.n_tile);
+    const int e = pre[nth];
+    tl.e = split * a.E + e;
     tl.row0 = m * TM + rank * 128;
     tl.rows = min(max(a.rows_w - tl.row0, 0), 128);
     tl.other = 0;
-    tl.k0 = off[tl.e];
-    tl.kn = off[tl.e + 1] - tl.k0;
+    tl.k0 = off[e];
+    tl.kn = off[e + 1] - tl.k0;
     tl.tail = tl.kn & 15;
     tl.kn -= tl.tail;
     tl.num_kb = (tl.kn + 63) / 64;
+    if (a.splits > 1) {  // its share of the K blocks; the last one also has the tail
+      const int lo = static_cast<int>(static_cast<long long>(tl.num_kb) * split / a.splits);
+      const int hi = static_cast<int>(static_cast<long long>(tl.num_kb) * (split + 1) / a.splits);
+      const bool last = split == a.splits - 1;
+      tl.kn = (last ? tl.kn : hi * 64) - lo * 64;
+      tl.k0 += lo * 64;
+      tl.num_kb = hi - lo;
+      if (!last) tl.tail = 0;
+    }
     return tl;
   }
   int lo = 0, hi = a.E;  // pre[lo] n_tiles <= t < pre[hi] n_tiles
@@ -300,7 +312,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   const uint32_t tmem_base = *tmem_slot;
   volatile int* vabort = abort_flag;
   const long long total = MODE == GRP_DW
-                              ? static_cast<long long>(args.E) * args.m_tiles * args.n_tiles
+                              ? static_cast<long long>(args.E) * args.splits * args.m_tiles *
+                                    args.n_tiles
                               : static_cast<long long>(pre[args.E]) * args.n_tiles;
   auto tile_at = [&](long long t) { return tile_of<MODE, PAIR>(args, off, pre, t, rank); };
   // this CTA's (pair's) units: one of every `step`, from alternate ends for the
@@ -514,7 +527,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       const uint32_t par = static_cast<uint32_t>(tails >> 1) & 1u;
       ++tails;
       uint8_t* p = smem + C::TAIL_OFF + slot * C::TAIL_BYTES;
-      bool ok = wait(&tail_empty[slot], par ^ 1u);
+      // (a tile of 2^24 rows takes a good part of a wait's limit: up to 64 of them)
+      bool ok = false;
+      for (int tries = 0; tries < 64 && !ok && !*vabort; ++tries)
+        ok = wait(&tail_empty[slot], par ^ 1u);
       if (ok) {
         if (lane == 0) {
           mbar_arrive_expect_tx(&tail_full[slot], C::TAIL_BYTES);
@@ -821,8 +837,54 @@ cudaError_t launch_grouped_dx(const mok_grouped_desc& D, const void* dy, const v
                               D.dx_elem == MOK_ELEM_F32, offsets, status, st);
 }
 
+// out (+)= the sum of `n` parts, in a fixed order.  Each warp sums every eighth part of
+// 32 words (W = 8, for few words) or each thread all parts of one (W = 1).
+template <int W>
+__global__ void __launch_bounds__(256)
+    grouped_sum_kernel(const float4* part, int n, long long words, float4* out, int accumulate) {
+  __shared__ float4 s_sum[8][32];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = W == 8 ? warp : 0;
+  const long long i = W == 8 ? blockIdx.x * 32ll + lane : blockIdx.x * 256ll + threadIdx.x;
+  const auto add = [](float4& v, const float4& u) {
+    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+  };
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < words) {
+#pragma unroll 10
+    for (int s = first; s < n; s += W) add(v, part[s * words + i]);
+  }
+  if (W == 8) {
+    s_sum[warp][lane] = v;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) add(v, s_sum[w][lane]);
+  }
+  if (i >= words) return;
+  if (accumulate) add(v, out[i]);
+  out[i] = v;
+}
+
+// Parts of the groups' rows that dw is summed in: as many as give every SM a tile
+// where there are fewer tiles of 128 x 128, none of less than 512 rows on average.  (A
+// group of 131072 rows, N = K = 64: one CTA's 2048 K blocks in a row otherwise.)
+static int dw_splits(const mok_grouped_desc& D) {
+  const long long tiles = D.E * ((D.N + 127) / 128) * ((D.K + 127) / 128);
+  long long s = kGb300Sms / tiles;
+  if (s > D.rows / (512LL * D.E)) s = D.rows / (512LL * D.E);
+  return static_cast<int>(s < 1 ? 1 : s);
+}
+
+size_t grouped_ws_bytes(const mok_grouped_desc& D) {
+  const int s = dw_splits(D);
+  return s > 1 ? static_cast<size_t>(s) * D.E * D.N * D.K * 4 : 0;
+}
+
 cudaError_t launch_grouped_dw(const mok_grouped_desc& D, const void* dy, const void* x,
-                              const int32_t* offsets, float* dw, int* status, cudaStream_t st) {
+                              const int32_t* offsets, float* dw, void* ws, int* status,
+                              cudaStream_t st) {
   const bool add = (D.accumulate & MOK_ADD_DW) != 0;
   if (D.rows == 0)
     return add ? cudaSuccess : cudaMemsetAsync(dw, 0, static_cast<size_t>(D.E) * D.N * D.K * 4, st);
@@ -832,7 +894,8 @@ cudaError_t launch_grouped_dw(const mok_grouped_desc& D, const void* dy, const v
   a.R = static_cast<int>(D.rows);
   a.rows_w = static_cast<int>(D.N);
   a.cols = static_cast<int>(D.K);
-  a.accumulate = add;
+  a.splits = dw_splits(D);
+  a.accumulate = add && a.splits == 1;
   a.status = status;
   CUtensorMap ta, tb, ta2, tb2, tc;
   const uint64_t K = D.K, N = D.N, E = D.E;
@@ -846,11 +909,12 @@ cudaError_t launch_grouped_dw(const mok_grouped_desc& D, const void* dy, const v
     const uint32_t box[3] = {64, rows, static_cast<uint32_t>(n)};
     return make_tensor_map(m, kBf, p, whole ? 3 : 2, dims, strides, box, kSw128);
   };
-  const uint64_t dims[3] = {K, N, E}, strides[2] = {K * 4, N * K * 4};
+  const uint64_t dims[3] = {K, N, E * a.splits}, strides[2] = {K * 4, N * K * 4};
   const uint32_t box[3] = {32, 32, 1};
   if (!col_map(&ta, dy, N, D.ld_y, a.blocks_n, 2, 64) ||
       !col_map(&ta2, dy, N, D.ld_y, a.blocks_n, 2, 16) ||
-      !make_tensor_map(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dw, 3, dims, strides, box, kSw128))
+      !make_tensor_map(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.splits > 1 ? ws : dw, 3, dims,
+                       strides, box, kSw128))
     return cudaErrorInvalidValue;
   auto run = [&](auto BNC, auto P) {
     constexpr int BN = decltype(BNC)::value;
@@ -862,10 +926,25 @@ cudaError_t launch_grouped_dw(const mok_grouped_desc& D, const void* dy, const v
     a.m_tiles = static_cast<int>((D.N + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128));
     a.n_tiles = static_cast<int>((D.K + BN - 1) / BN);
     return launch<GRP_DW, BN, true, PAIR>("grouped_linear_dw", ta, tb, ta2, tb2, tc, a,
-                                          static_cast<long long>(D.E) * a.m_tiles * a.n_tiles, st);
+                                          static_cast<long long>(D.E) * a.splits * a.m_tiles *
+                                              a.n_tiles,
+                                          st);
   };
   using Yes = std::true_type;
   using No = std::false_type;
+  if (a.splits > 1) {
+    cudaError_t e = run(std::integral_constant<int, 128>(), No());
+    if (e != cudaSuccess) return e;
+    const long long words = D.E * D.N * D.K / 4;  // (at most 152 tiles of 128 x 128)
+    ProfScope prof("grouped_linear_dw_sum", st);
+    const bool few = words < 64LL * kGb300Sms;
+    e = launch_dependent(few ? grouped_sum_kernel<8> : grouped_sum_kernel<1>,
+                         dim3(static_cast<unsigned>(few ? (words + 31) / 32 : (words + 255) / 256)),
+                         dim3(256), 0, st, static_cast<const float4*>(ws), a.splits, words,
+                         reinterpret_cast<float4*>(dw), add ? 1 : 0);
+    count_launch();
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
   if (static_cast<long long>(D.E) * ((D.N + 127) / 128) * ((D.K + 255) / 256) < kGb300Sms)
     return run(std::integral_constant<int, 128>(), No());
   // Short groups are bound by the stores of dw, which single CTAs do better (64

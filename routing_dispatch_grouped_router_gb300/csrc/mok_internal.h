@@ -369,8 +369,10 @@ cudaError_t launch_grouped_fwd(const mok_grouped_desc& D, const void* x, const v
                                const int32_t* offsets, void* y, int* status, cudaStream_t st);
 cudaError_t launch_grouped_dx(const mok_grouped_desc& D, const void* dy, const void* w,
                               const int32_t* offsets, void* dx, int* status, cudaStream_t st);
+size_t grouped_ws_bytes(const mok_grouped_desc& D);  // scratch of launch_grouped_dw
 cudaError_t launch_grouped_dw(const mok_grouped_desc& D, const void* dy, const void* x,
-                              const int32_t* offsets, float* dw, int* status, cudaStream_t st);
+                              const int32_t* offsets, float* dw, void* ws, int* status,
+                              cudaStream_t st);
 
 // MXFP8 fake quantisation (mx.cu): rows = blocks along each row, cols =
 // blocks of 32 rows; codes/scales may be null.

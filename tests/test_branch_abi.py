@@ -121,7 +121,10 @@ def test_norms_workspace_covers_any_alignment(lib):
     (dict(ld_x=76), 2), (dict(ld_y=68), 2), (dict(ld_dx=73), 2), (dict(ld_x=1 << 37), 2)])
 def test_grouped_descriptors_refused(lib, kw, code):
     assert lib.mok_grouped_linear_forward(grouped(**kw), A, A, A, A, None, None) == code
-    assert lib.mok_grouped_linear_backward(grouped(**kw), A, A, A, A, A, A, None, None) == code
+    n = ctypes.c_size_t()
+    assert lib.mok_grouped_linear_backward(grouped(**kw), A, A, A, A, A, A, None, 0, None,
+                                           None) == code
+    assert lib.mok_grouped_linear_workspace_size(grouped(**kw), n) == code
 
 
 def test_grouped_pointers_refused(lib):
@@ -137,10 +140,16 @@ def test_grouped_pointers_refused(lib):
     for i in range(4):
         args = [A] * 6
         args[i] = None
-        assert b(grouped(), *args, None, None) == 1
-    assert b(grouped(y_elem=1), *[A] * 6, None, None) == 2  # fp32 dy
-    assert b(grouped(), A, A, A, A, P(4104), A, None, None) == 1
-    assert b(grouped(), A, A, A, A, A, P(4104), None, None) == 1
+        assert b(grouped(), *args, None, 0, None, None) == 1
+    assert b(grouped(y_elem=1), *[A] * 6, None, 0, None, None) == 2  # fp32 dy
+    assert b(grouped(), A, A, A, A, P(4104), A, None, 0, None, None) == 1
+    assert b(grouped(), A, A, A, A, A, P(4104), None, 0, None, None) == 1
+    n = ctypes.c_size_t()
+    assert lib.mok_grouped_linear_workspace_size(grouped(), n) == 0 and n.value == 0
+    long = grouped(rows=100000, E=1)
+    assert lib.mok_grouped_linear_workspace_size(long, n) == 0 and n.value > 0
+    assert b(long, *[A] * 6, None, n.value, None, None) == 1
+    assert b(long, *[A] * 6, A, n.value - 1, None, None) == 3
 
 
 def test_python_refusals_without_a_gpu(lib):

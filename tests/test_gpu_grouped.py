@@ -123,6 +123,27 @@ def test_grouped_large(sizes, N, K, dtype):
             assert rms(y[r], a @ we.T) < 1e-6 and rms(dx[r], g @ we) < 1e-6
 
 
+@pytest.mark.parametrize("sizes,N,K", [([20000], 64, 72), ([9000, 0, 13], 136, 64),
+                                       ([4097, 1, 2222], 8, 200), ([1030], 256, 128)])
+def test_grouped_weight_gradient_in_parts(sizes, N, K):
+    """Few tiles and many rows: dw summed in parts of the rows, to 1e-6 rms, added into
+    dw after their sum; one group's values in no other's."""
+    x, dy, w, off, y, dx, dw = check(sizes, N, K, BF16)
+    o = off.tolist()
+    for e, n in enumerate(sizes):
+        if n:
+            r = slice(o[e], o[e + 1])
+            want = dy[r].to(F64).T @ x[r].to(F64)
+            assert ((dw[e].to(F64) - want).pow(2).mean() / want.pow(2).mean()).sqrt() < 1e-6
+    acc = dw.clone()
+    api.grouped_linear_backward(dy, x, w, off, dw=acc, accumulate=True)
+    assert torch.equal(acc, 2 * dw)
+    if len(sizes) > 1:
+        x2 = x.clone()
+        x2[o[-2]:] = math.nan
+        assert torch.equal(api.grouped_linear_backward(dy, x2, w, off)[1][:-1], dw[:-1])
+
+
 def test_grouped_values_stay_in_their_group():
     """NaN and Inf in one group's rows or weights reach no other group's results."""
     sizes = [33, 7, 129, 64, 1, 250]
