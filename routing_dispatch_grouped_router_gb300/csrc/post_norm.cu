@@ -135,13 +135,14 @@ __global__ void __launch_bounds__(kRingThreads) post_pre_ring_kernel(PostPreFwd 
     for (uint32_t i = 0; i < g.depth && blockIdx.x + i * step < a.rows; ++i)
       fill(i, blockIdx.x + i * step);
   F2 w1[2][4], w2[2][4];
+  // (by elements: vectors, 16 loads instead of 48 a thread, made 8192 x 7168 111 us)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    ring_weight(a.w1, a.w_f32, t + i * tpr, h, own[i], w1[i]);
-    ring_weight(a.w2, a.w_f32, t + i * tpr, h, own[i], w2[i]);
+    ring_weight<false>(a.w1, a.w_f32, t + i * tpr, h, own[i], w1[i]);
+    ring_weight<false>(a.w2, a.w_f32, t + i * tpr, h, own[i], w2[i]);
     if (a.gate_kind == MOK_GATE_CHANNEL) {
       F2 z[4];
-      ring_weight(a.gate, a.gate_f32, t + i * tpr, h, own[i], z);
+      ring_weight<false>(a.gate, a.gate_f32, t + i * tpr, h, own[i], z);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w1[i][j] = mul2(w1[i][j], z[j]);
     }

@@ -208,11 +208,22 @@ __device__ __forceinline__ uint32_t ring_own(int v, int h, int d) {
   if (e + 8 > d) own &= e < d ? 0xffu >> (e + 8 - d) : 0u;
   return own;
 }
+// (WIDE, rows without a shift: by aligned vectors.)
+template <bool WIDE>
 __device__ __forceinline__ void ring_weight(const void* w, int f32, int v, int h, uint32_t own,
                                             F2 (&o)[4]) {
-  auto at = [&](int j) { return (own >> j & 1u) ? elem_at(w, 8 * v - h + j, f32) : 0.f; };
+  float x[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = f2(at(2 * j), at(2 * j + 1));
+  for (int j = 0; j < 8; ++j) x[j] = 0.f;
+  if (WIDE) {
+    if (own) load_weight<true>(w, f32, v, 0, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (own >> j & 1u) x[j] = elem_at(w, 8 * v - h + j, f32);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = f2(x[2 * j], x[2 * j + 1]);
 }
 
 // The warp's sums of N <= 8 values (a power of two): of value lane / (32 / N).  Each

@@ -37,11 +37,11 @@ __global__ void __launch_bounds__(THREADS)
   F2 w1[2][4], w2[2][4], dw1[2][4], dw2[2][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    ring_weight(a.w1, a.w_f32, t + i * tpr, h, own[i], w1[i]);
-    ring_weight(a.w2, a.w_f32, t + i * tpr, h, own[i], w2[i]);
+    ring_weight<!SHIFT>(a.w1, a.w_f32, t + i * tpr, h, own[i], w1[i]);
+    ring_weight<!SHIFT>(a.w2, a.w_f32, t + i * tpr, h, own[i], w2[i]);
     if (a.gate_kind == MOK_GATE_CHANNEL) {
       F2 z[4];
-      ring_weight(a.gate, a.gate_f32, t + i * tpr, h, own[i], z);
+      ring_weight<!SHIFT>(a.gate, a.gate_f32, t + i * tpr, h, own[i], z);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w1[i][j] = mul2(w1[i][j], z[j]);
     }
