@@ -638,7 +638,7 @@ typedef struct mok_grouped_desc {
  * tensor cores and rounded once.  offsets: int32 [E+1] on the device,
  * nondecreasing from 0 to R (what mok_moe_dispatch_plan writes); groups may be
  * of any size and empty, no row is padded.  offsets[0] may be above 0 and
- * offsets[E] below R: rows outside of the groups are neither read nor written.
+ * offsets[E] below R: rows outside of the groups take no part and are not written.
  * An offset outside [0, R] is taken as the nearer end and one below an earlier
  * offset as that one; either sets MOK_ERR_DEVICE_INDEX.  x, w, y 16-byte
  * aligned.  status: as in mok_router_balance_forward; a bounded wait that gave up

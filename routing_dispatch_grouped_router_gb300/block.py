@@ -105,6 +105,7 @@ class GroupedExperts:
     def __init__(self):
         self.kept = None
 
+    @torch.no_grad()  # the products have no part in autograd's graph: nor has the rest
     def forward(self, x, topk_w, offsets, token_of_row, pos, w_up, w_down):
         """y fp32 [T, d] = the sum over a token's slots of topk_w times its
         expert's output.  x bf16 [T, d]."""
@@ -115,6 +116,7 @@ class GroupedExperts:
         self.kept = (rows, z, h, o, topk_w, offsets, token_of_row, pos)
         return torch.einsum("tk,tkd->td", topk_w, o[pos.long()])
 
+    @torch.no_grad()
     def backward(self, dy, w_up, w_down):
         """(dx fp32 [T, d], dtopk_w fp32 [T, k], dw_up, dw_down fp32) of the last
         forward from dy fp32 [T, d]."""
