@@ -46,6 +46,8 @@ struct GroupedArgs {
   long long ld_out;  // row stride of C
   void* out;
   int wide;          // C's rows begin on 32 bytes, and so do their ends
+  int round16;       // F32: C is bf16 all the same (a long sum, see kOneSumKb)
+  int chunk_kb;      // F32: K blocks of one accumulation
   // DX, DW: w's, x's (K) and dy's (N) 64-column blocks are a dimension of their maps:
   // one copy brings a stage's blocks.  (One thread issues the copies; one per 64
   // columns or 32 rows made it the slowest part: 64 groups of 512 rows, N = K = 2048,
@@ -67,6 +69,12 @@ constexpr int kTailWarp = 10;
 // registers with correct rounding (one accumulation over 2048 values is 2e-6 off,
 // these 6e-7).
 constexpr int kChunkKb = 9;
+// A bf16 result is one accumulation while that is short: values of one sign lose 1e-7
+// of their sum per MMA, 1e-4 over 256 K blocks (a bf16 half step is 2e-3 to 4e-3).
+// Longer sums are taken in chunks of 64 K blocks and rounded at the end (2^20 values of
+// one sign were 6.7e-3 off in one accumulation).  8192 rows of 8 groups, N = 2048, K =
+// 16448: 356 us, in chunks of nine 378, in one accumulation 362.
+constexpr int kOneSumKb = 256, kLongChunkKb = 64;
 
 template <int MODE, int BN, bool PAIR>
 struct Cfg {
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         // (a group of less than 16 rows has its tail alone)
         const int last = tl.num_kb > 0 || tl.tail == 0 ? tl.num_kb : 1;
         for (int kb = 0; kb < last; ++kb) {
-          if (kb == 0 || (F32 && kb == kb0 + kChunkKb)) {
+          if (kb == 0 || (F32 && kb == kb0 + args.chunk_kb)) {
             if (kb > 0) {  // the next chunk's sum goes to the other accumulator
               commit(&tfull[it & 1]);
               ++it;
@@ -593,8 +601,9 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     // 32 columns of this lane's row (words of 16 bytes) to C's columns x ..
     auto put = [&](const Tile& tl, int x, const uint4* w, int words) {
       const long long row = tl.row0 + q * 32 + lane;
-      uint8_t* p = out + (row * args.ld_out + x) * ES;
-      const int left = min((args.cols - x) * ES / 16, words);  // words within the row
+      const int es = ES == 4 && args.round16 ? 2 : ES;
+      uint8_t* p = out + (row * args.ld_out + x) * es;
+      const int left = min((args.cols - x) * es / 16, words);  // words within the row
       if (wide) {
 #pragma unroll
         for (int j = 0; j < words; j += 2)
@@ -612,7 +621,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       const bool in = lane < valid;
       const int x0 = tl.n_tile * BN + half * HC;
       const int chunks =
-          !F32 || (tl.num_kb == 0 && tl.tail) ? 1 : (tl.num_kb + kChunkKb - 1) / kChunkKb;
+          !F32 || (tl.num_kb == 0 && tl.tail) ? 1 : (tl.num_kb + args.chunk_kb - 1) / args.chunk_kb;
       float sum[F32 ? HC : 1];
       if constexpr (F32) {
 #pragma unroll
@@ -679,6 +688,19 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
             for (int c = 0; c < HC; c += 32)
               if (x0 + c < args.cols) put_dw(tl, x0 + c, sum + c);
+          }
+        } else if (in && args.round16) {
+#pragma unroll
+          for (int c = 0; c < HC; c += 32) {
+            if (x0 + c >= args.cols) continue;
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float* v = sum + c + 8 * j;
+              w[j] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            }
+            put(tl, x0 + c, w, 4);
           }
         } else if (in) {
 #pragma unroll
@@ -789,6 +811,8 @@ cudaError_t rows_product(const char* name, const mok_grouped_desc& D, const void
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && ld_out * es % 32 == 0 &&
            cols * es % 32 == 0;
   a.blocks_k = MODE == GRP_DX && D.K % 64 == 0;
+  a.round16 = !f32 && a.num_kb > kOneSumKb;
+  a.chunk_kb = a.round16 ? kLongChunkKb : kChunkKb;
   if (!make_tensor_map_2d(&ta, kBf, 2, A, sum, D.rows, ld_a, 64, 128, kSw128) ||
       !make_tensor_map_2d(&ta2, kBf, 2, A, sum, D.rows, ld_a, 64, 32, kSw128))
     return cudaErrorInvalidValue;
@@ -810,7 +834,8 @@ cudaError_t rows_product(const char* name, const mok_grouped_desc& D, const void
     if (!ok) return cudaErrorInvalidValue;
     a.n_tiles = static_cast<int>((cols + BN - 1) / BN);
     const long long units = most_tiles(D, PAIR ? 256 : 128) * a.n_tiles;
-    return f32 ? launch<MODE, BN, true, PAIR>(name, ta, tb, ta2, tb, ta, a, units, st)
+    return f32 || a.round16
+               ? launch<MODE, BN, true, PAIR>(name, ta, tb, ta2, tb, ta, a, units, st)
                : launch<MODE, BN, false, PAIR>(name, ta, tb, ta2, tb, ta, a, units, st);
   };
   using Yes = std::true_type;
@@ -901,6 +926,7 @@ cudaError_t launch_grouped_dw(const mok_grouped_desc& D, const void* dy, const v
   a.cols = static_cast<int>(D.K);
   a.splits = dw_splits(D);
   a.accumulate = add && a.splits == 1;
+  a.chunk_kb = kChunkKb;
   a.status = status;
   CUtensorMap ta, tb, ta2, tb2, tc;
   const uint64_t K = D.K, N = D.N, E = D.E;

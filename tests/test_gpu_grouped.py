@@ -287,3 +287,47 @@ def test_grouped_on_a_dispatch_plan():
     want = torch.einsum("td,tknd->tkn", x.to(F64), w.to(F64)[idx.long()])
     mag = torch.einsum("td,tknd->tkn", x.to(F64).abs(), w.to(F64).abs()[idx.long()])
     assert bool(((got.to(F64) - want).abs() <= mag * 2 * d * U32 + want.abs() * U32).all())
+
+
+def test_grouped_long_sums():
+    """2^20 values of one sign into bf16: half a step, and what sums of 4096 values on
+    the tensor cores (truncated: twice u32 a value), added in fp32, may lose.  (One
+    accumulation loses 6.7e-3 here, over two of the half steps.)"""
+    R, n, m = 32, 1 << 20, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = torch.rand(R, n, generator=g, device="cuda").bfloat16()
+    b = (torch.rand(1, m, n, generator=g, device="cuda") * n ** -0.5).bfloat16()
+    off = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    want = a.to(F64) @ b[0].to(F64).T  # (every term is positive: its own magnitude)
+    bound = want * (1.01 * rounding(BF16) + (2 * 4096 + n / 4096) * U32)
+    y = api.grouped_linear(a, b, off)
+    dx, _ = api.grouped_linear_backward(a, a[:, :m].contiguous(), b.transpose(1, 2).contiguous(),
+                                        off)
+    for got in (y, dx):
+        d = (got.to(F64) - want).abs()
+        assert bool((d <= bound).all()), (d / want).max().item()
+
+
+@pytest.mark.parametrize("sizes,cols", [([20, 0, 13], 264), ([100] * 160, 256),
+                                        ([5000, 130], 264)])
+def test_grouped_long_sums_of_every_tile(sizes, cols):
+    """Just past 2^14 values, by narrow tiles, wide ones and pairs: rows of bf16 and fp32
+    results in 64 bits, bf16 ones within half a step and the loss of 4096 values in one
+    accumulation."""
+    n = 16456
+    _, off = table(sizes)
+    R, E = sum(sizes), len(sizes)
+    a, b = randn(1, R, n), randn(2, E, cols, n, scale=n ** -0.5)
+    out = torch.full((R, cols + 8), 7.0, dtype=BF16, device="cuda")
+    y = api.grouped_linear(a, b, off, y=out[:, :cols])
+    y32 = api.grouped_linear(a, b, off, out_dtype=F32)
+    x, w = torch.zeros(R, cols, dtype=BF16, device="cuda"), b.transpose(1, 2).contiguous()
+    dx, _ = api.grouped_linear_backward(a, x, w, off)
+    dx32, _ = api.grouped_linear_backward(a, x, w, off, dx_dtype=F32)
+    assert bool((out[:, cols:] == 7).all())
+    for r in (0, R // 2, R - 1):
+        e = (off[1:] <= r).sum().item()
+        want = b[e].to(F64) @ a[r].to(F64)
+        mag = b[e].to(F64).abs() @ a[r].to(F64).abs()
+        for got, m in ((y, 4096), (y32, 576), (dx, 4096), (dx32, 576)):
+            close(got[r], want, mag, m + n / m, got.dtype)
