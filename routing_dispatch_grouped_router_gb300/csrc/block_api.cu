@@ -107,6 +107,13 @@ mok_status post_pre_desc(const mok_post_pre_desc* desc, mok_post_pre_desc* D) {
   return MOK_OK;
 }
 
+// Whether there is a gate where the descriptor has one.  Without rows a token's gate is
+// empty and may be NULL; a channel's is [d], and the sums read it.
+bool gate_fits(const mok_post_pre_desc& D, const void* gate) {
+  if (D.rows == 0) return gate || D.gate != MOK_GATE_CHANNEL;
+  return (gate != nullptr) == (D.gate != MOK_GATE_NONE);
+}
+
 mok_status grouped_desc(const mok_grouped_desc* desc, mok_grouped_desc* D) {
   if (!desc) return MOK_ERR_INVALID_ARG;
   *D = *desc;
@@ -318,7 +325,7 @@ mok_status mok_post_pre_rmsnorm_forward(const mok_post_pre_desc* desc, const voi
   if (st != MOK_OK) return st;
   if (!post_weight || !pre_weight || (D.rows > 0 && (!x || !residual || !s || !y)))
     return MOK_ERR_INVALID_ARG;
-  if ((gate != nullptr) != (D.gate != MOK_GATE_NONE) && D.rows > 0) return MOK_ERR_INVALID_ARG;
+  if (!gate_fits(D, gate)) return MOK_ERR_INVALID_ARG;
   const size_t se = elem_size(D.s_elem), we = elem_size(D.weight_elem);
   if (!aligned(x, elem_size(D.x_elem)) || !aligned(residual, se) || !aligned(s, se) ||
       !aligned(y, 2) || !aligned(post_weight, we) || !aligned(pre_weight, we) ||
@@ -350,7 +357,7 @@ mok_status mok_post_pre_rmsnorm_backward(const mok_post_pre_desc* desc, const vo
   if (st != MOK_OK) return st;
   if (!post_weight || !pre_weight || (D.rows > 0 && (!dy || !x || !s || !dx || !dresidual)))
     return MOK_ERR_INVALID_ARG;
-  if ((gate != nullptr) != (D.gate != MOK_GATE_NONE) && D.rows > 0) return MOK_ERR_INVALID_ARG;
+  if (!gate_fits(D, gate)) return MOK_ERR_INVALID_ARG;
   if (dgate && D.gate == MOK_GATE_NONE) return MOK_ERR_INVALID_ARG;
   const size_t se = elem_size(D.s_elem), we = elem_size(D.weight_elem);
   if (!aligned(dy, elem_size(D.y_elem)) || !aligned(x, elem_size(D.x_elem)) || !aligned(s, se) ||

@@ -168,3 +168,20 @@ def test_python_refusals_without_a_gpu(lib):
                  lambda: api.grouped_linear_backward(x, x, torch.zeros(1, 8, 8), off)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_norms_without_rows_need_a_channels_gate(lib):
+    """A channel's gate is [d] whatever the rows (the sums of the weights' gradients
+    read it); only a token's, [0], may be missing."""
+    f, b = lib.mok_post_pre_rmsnorm_forward, lib.mok_post_pre_rmsnorm_backward
+    d = norms(rows=0, gate=1)
+    assert f(d, None, None, A, A, None, None, None, None, None) == 1
+    for grads in ((A, A, A), (A, None, None), (None, A, None), (None, None, A), (None,) * 3):
+        assert b(d, None, None, None, A, A, None, None, None, None, *grads, None, 0, None,
+                 None) == 1
+    # those that are right end at the missing GPU, if at all
+    if not torch.cuda.is_available():
+        ok = f(norms(rows=0), None, None, A, A, None, None, None, None, None)
+        assert ok != 1
+        assert f(norms(rows=0, gate=2), None, None, A, A, None, None, None, None, None) == ok
+        assert f(d, None, None, A, A, A, None, None, None, None) == ok
