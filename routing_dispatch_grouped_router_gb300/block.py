@@ -100,7 +100,11 @@ class GroupedExperts:
     """Experts act(x w_up^T) w_down^T with relu^2 between the products, over the
     rows that a dispatch plan sorts by expert: w_up bf16 [E, F, d], w_down bf16 [E,
     d, F].  The plan (`api.dispatch_plan`): offsets int32 [E+1], token_of_row int32
-    [T k], pos int32 [T, k]; topk_w fp32 [T, k] the slots' weights."""
+    [T k], pos int32 [T, k]; topk_w fp32 [T, k] the slots' weights.
+
+    A slot that the plan skipped for a bad index (pos -1; the plan's status tells) adds
+    nothing and gets no gradient.  Such a plan has rows of no group, the last one among
+    them: it stands for all skipped slots, as a row of zeros."""
 
     def __init__(self):
         self.kept = None
@@ -109,23 +113,28 @@ class GroupedExperts:
     def forward(self, x, topk_w, offsets, token_of_row, pos, w_up, w_down):
         """y fp32 [T, d] = the sum over a token's slots of topk_w times its
         expert's output.  x bf16 [T, d]."""
-        rows = x[token_of_row.long()]
+        # (words of rows of no group are unwritten)
+        rows = x[token_of_row.long().clamp(0, x.shape[0] - 1)]
+        skipped = pos < 0
+        slots = torch.where(skipped, rows.shape[0] - 1, pos).long()
+        topk_w = topk_w.masked_fill(skipped, 0.0)
         z = api.grouped_linear(rows, w_up, offsets)
         h = torch.square(torch.relu(z.float())).to(torch.bfloat16)
         o = api.grouped_linear(h, w_down, offsets, out_dtype=torch.float32)
-        self.kept = (rows, z, h, o, topk_w, offsets, token_of_row, pos)
-        return torch.einsum("tk,tkd->td", topk_w, o[pos.long()])
+        o[-1:].masked_fill_(skipped.any(), 0.0)
+        self.kept = (rows, z, h, o, topk_w, offsets, slots, skipped)
+        return torch.einsum("tk,tkd->td", topk_w, o[slots])
 
     @torch.no_grad()
     def backward(self, dy, w_up, w_down):
         """(dx fp32 [T, d], dtopk_w fp32 [T, k], dw_up, dw_down fp32) of the last
         forward from dy fp32 [T, d]."""
-        rows, z, h, o, topk_w, offsets, token_of_row, pos = self.kept
-        slots = pos.long()
-        dtopk_w = torch.einsum("td,tkd->tk", dy, o[slots])
+        rows, z, h, o, topk_w, offsets, slots, skipped = self.kept
+        dtopk_w = torch.einsum("td,tkd->tk", dy, o[slots]).masked_fill_(skipped, 0.0)
         do = torch.empty(o.shape, dtype=torch.bfloat16, device=o.device)
         do[slots] = (topk_w.unsqueeze(2) * dy.unsqueeze(1)).to(torch.bfloat16)
         dh, dw_down = api.grouped_linear_backward(do, h, w_down, offsets, dx_dtype=torch.float32)
         dz = (dh * 2 * torch.relu(z.float())).to(torch.bfloat16)
         dr, dw_up = api.grouped_linear_backward(dz, rows, w_up, offsets, dx_dtype=torch.float32)
+        dr[-1:].masked_fill_(skipped.any(), 0.0)
         return dr[slots].sum(1), dtopk_w, dw_up, dw_down

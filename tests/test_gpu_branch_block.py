@@ -160,3 +160,46 @@ def test_grouped_experts_between_norms(T, d, F, E, k):
         graph.replay()
     for name, a, b in zip(names, again, got):
         assert torch.equal(a, b), name
+
+
+def test_grouped_experts_of_a_plan_with_bad_indices():
+    """The plan reports them and skips their slots: as a plan of weight 0 there, with any
+    value in the words that the plan leaves unwritten."""
+    T, d, F, E, k = 61, 136, 80, 5, 3
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def rnd(*shape, scale=1.0, dtype=torch.bfloat16):
+        return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
+
+    x, dy = rnd(T, d), rnd(T, d, dtype=F32)
+    wu, wd = rnd(E, F, d, scale=d ** -0.5), rnd(E, d, F, scale=F ** -0.5)
+    idx = torch.stack([torch.randperm(E, generator=gen, device="cuda")[:k] for _ in range(T)]).int()
+    bad = torch.rand(T, k, generator=gen, device="cuda") < 0.3
+    bad[7] = True
+    tw = torch.softmax(rnd(T, k, dtype=F32), 1)
+    desc = api.make_desc(T, 128, E, 128, k)
+    outs = []
+    for skip in (False, True):
+        counts, off = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (E, E + 1))
+        pos = torch.empty(T, k, dtype=torch.int32, device="cuda")
+        rows = torch.full((T * k,), (1 << 31) - 1, dtype=torch.int32, device="cuda")
+        ws = torch.empty(api.stage_workspace_size(desc), dtype=torch.uint8, device="cuda")
+        at = torch.where(bad, torch.where(idx > 2, -1, E), idx).int() if skip else idx
+        api.dispatch_plan(desc, at, counts, off, pos, rows, ws)
+        assert api.device_status(ws) == (17 if skip else 0)
+        assert (pos < 0).sum().item() == (bad.sum().item() if skip else 0)
+        experts = block.GroupedExperts()
+        y = experts.forward(x, tw if skip else tw.masked_fill(bad, 0.0), off, rows, pos, wu, wd)
+        outs.append((y,) + experts.backward(dy, wu, wd))
+    assert api.device_status(api.operator_status()) == 0
+    for a, b in zip(*outs):
+        assert bool(torch.isfinite(b).all())
+    # y, dx, the weights' gradients are sums of the same terms and zeros, in groups whose
+    # rows lie elsewhere: fp32 sums of at most F, d or T k terms in another order, and
+    # bf16 roundings (h, dz of equal fp32 values) that may fall to the other side
+    (y0, dx0, dt0, du0, dd0), (y1, dx1, dt1, du1, dd1) = outs
+    assert not dt1[bad].any()
+    for a, b in ((y0, y1), (dx0, dx1), (dt0[~bad], dt1[~bad]), (du0, du1), (dd0, dd1)):
+        err = ((a - b).pow(2).mean() / a.pow(2).mean()).sqrt().item()
+        assert err <= U16, err
+    assert not y1[7].any() and not dx1[7].any()
