@@ -203,3 +203,35 @@ def test_grouped_experts_of_a_plan_with_bad_indices():
         err = ((a - b).pow(2).mean() / a.pow(2).mean()).sqrt().item()
         assert err <= U16, err
     assert not y1[7].any() and not dx1[7].any()
+
+
+@pytest.mark.parametrize("T,k", [(1, 2), (40, 4), (4096, 8)])
+def test_grouped_experts_do_not_follow_torchs_tf32(T, k):
+    """Torch's switch for its own products changes nothing in fp32 here: the same bits."""
+    d, F, E = 1024, 128, 16
+    gen = torch.Generator(device="cuda").manual_seed(T)
+
+    def rnd(*shape, scale=1.0, dtype=torch.bfloat16):
+        return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
+
+    x, dy = rnd(T, d), rnd(T, d, dtype=F32)
+    wu, wd = rnd(E, F, d, scale=d ** -0.5), rnd(E, d, F, scale=F ** -0.5)
+    idx = torch.stack([torch.randperm(E, generator=gen, device="cuda")[:k] for _ in range(T)])
+    tw = torch.softmax(rnd(T, k, dtype=F32), 1)
+    flat = idx.reshape(-1)
+    order = torch.argsort(flat, stable=True)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1:] = torch.bincount(flat, minlength=E).cumsum(0)
+    pos = torch.empty(T * k, dtype=torch.int32, device="cuda")
+    pos[order] = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    before, outs = torch.backends.cuda.matmul.allow_tf32, []
+    try:
+        for tf32 in (False, True):
+            torch.backends.cuda.matmul.allow_tf32 = tf32
+            experts = block.GroupedExperts()
+            y = experts.forward(x, tw, off, (order // k).int(), pos.view(T, k), wu, wd)
+            outs.append((y,) + experts.backward(dy, wu, wd))
+    finally:
+        torch.backends.cuda.matmul.allow_tf32 = before
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
