@@ -29,10 +29,15 @@ class MoEBlock:
     gate fp32 [d].  Gradients come as a dict of the same names, fp32.
 
     dropout: the share of the output's elements that are dropped, by the
-    generator state that `forward` is given and `site`, the block's number."""
+    generator state that `forward` is given and `site`, the block's number.
+    residual_scale is the post_norm form's."""
 
     def __init__(self, T, d, E, I, k, *, act="silu", eps=1e-6, balance_coef=1e-2, z_coef=1e-3,
                  dtype=api.BF16, post_norm=False, residual_scale=1.0, dropout=0.0, site=0):
+        if not post_norm and residual_scale != 1.0:
+            raise ValueError("residual_scale needs post_norm")
+        if not 0.0 <= dropout <= 1.0:
+            raise ValueError(f"dropout must be from 0 to 1, got {dropout}")
         self.layer = api.MoELayer(T, d, E, I, k, dtype=dtype)
         self.T, self.k, self.act, self.eps = T, k, act, eps
         self.post_norm, self.residual_scale = post_norm, residual_scale
