@@ -65,7 +65,8 @@ constexpr int kEpiWarps = 8;
 constexpr int threads_of(int mode) { return 320 + (mode == GRP_DW ? 32 : 0); }
 constexpr int kTailWarp = 10;
 // An fp32 result is summed on the tensor cores, whose accumulation truncates, over
-// at most 36 MMAs (9 K blocks) at a time, and the chunks' sums are added in
+// at most 36 MMAs (9 K blocks; 37 where dw's last chunk also takes the group's last rows)
+// at a time, and the chunks' sums are added in
 // registers with correct rounding (one accumulation over 2048 values is 2e-6 off,
 // these 6e-7).
 constexpr int kChunkKb = 9;
@@ -541,9 +542,12 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       ++tails;
       uint8_t* p = smem + C::TAIL_OFF + slot * C::TAIL_BYTES;
       // (a tile of 2^24 rows takes a good part of a wait's limit: up to 64 of them)
+      // (the warp's lanes give up together: one may see a phase or the flag later)
       bool ok = false;
-      for (int tries = 0; tries < 64 && !ok && !*vabort; ++tries)
-        ok = wait(&tail_empty[slot], par ^ 1u);
+      for (int tries = 0; tries < 64 && !ok; ++tries) {
+        ok = __all_sync(0xffffffffu, wait(&tail_empty[slot], par ^ 1u));
+        if (!ok && __any_sync(0xffffffffu, *vabort)) break;
+      }
       if (ok) {
         if (lane == 0) {
           mbar_arrive_expect_tx(&tail_full[slot], C::TAIL_BYTES);
@@ -553,9 +557,9 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     C::B_ROWS / 64, 2048, args.blocks_k);
         }
         __syncwarp();
-        ok = wait(&tail_full[slot], par);
+        ok = __all_sync(0xffffffffu, wait(&tail_full[slot], par));
       }
-      if (!__all_sync(0xffffffffu, ok)) {
+      if (!ok) {
         *vabort = 1;
         if (lane == 0) set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
         spin_ns(1000000ull);  // copies in flight land before the CTA can exit
@@ -629,10 +633,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
       }
       bool ok = true;
       for (int ch = 0; ch < chunks; ++ch, ++it) {
-        if (!wait(&tfull[it & 1], static_cast<uint32_t>(it >> 1) & 1u)) {
+        ok = __all_sync(0xffffffffu,
+                        wait(&tfull[it & 1], static_cast<uint32_t>(it >> 1) & 1u));
+        if (!ok) {
           *vabort = 1;
           set_status(args.status, MOK_ERR_DEVICE_TIMEOUT);
-          ok = false;
           break;
         }
         tc_fence_after_sync();
@@ -681,7 +686,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           else mbar_arrive(&tempty[it & 1]);
         }
       }
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!ok) break;
       if constexpr (F32) {
         if (MODE == GRP_DW) {
           if (valid > 0 && !(args.accumulate && chunks == 0)) {
