@@ -116,3 +116,36 @@ def test_dropout_rows_of_the_largest_sizes():
     assert torch.equal(y[0, first:] != 0, keep)
     y2 = api.dropout(x.view(n, 1), 0.5, rng, 2, y=y.view(n, 1))
     assert torch.equal(y2[first:, 0] != 0, keep)
+
+
+def test_dropout_of_rows_of_one_element():
+    """2^31 - 1 rows of one element at a stride of two: more than 2^31 groups, so that
+    places are counted in 64 bits, and what lies between the rows stays."""
+    n = (1 << 31) - 1
+    x = torch.ones(n, 1, dtype=BF16, device="cuda")
+    rng = torch.tensor([9, 1], device="cuda")
+    out = torch.full((n, 2), 7.0, dtype=BF16, device="cuda")
+    api.dropout(x, 0.5, rng, 2, y=out[:, :1])
+    for first in (0, 1 << 30, n // 4 * 4 - 4096):
+        count = min(4096, n - first)
+        keep = ref.dropout_words(9, 1, 2, first, count, "cuda") >= 1 << 31
+        assert torch.equal(out[first:first + count, 0],
+                           torch.where(keep, 2.0, 0.0).to(BF16))
+    for part in out[:, 1].split(1 << 28):
+        assert bool((part == 7).all())
+
+
+@pytest.mark.parametrize("rows,d,pad", [((1 << 21) + 1, 8200, 0), ((1 << 21) + 1, 8200, 8),
+                                        ((1 << 21) + 1, 8201, 1)])
+def test_dropout_past_2_to_the_34_elements(rows, d, pad):
+    """More than 2^34 elements, where the counter's second word is not 0, in place:
+    contiguous, in rows of whole words, in rows at an odd stride."""
+    x = torch.ones(rows, d + pad, dtype=BF16, device="cuda")
+    rng = torch.tensor([9, 1], device="cuda")
+    v = x[:, :d]
+    assert api.dropout(v, 0.25, rng, 2, y=v) is v
+    for r0 in (0, rows // 2, rows - 4):
+        a = r0 * d // 4 * 4
+        w = ref.dropout_words(9, 1, 2, a, 4 * d + 8, "cuda")[r0 * d - a:][:4 * d].reshape(4, d)
+        assert torch.equal(v[r0:r0 + 4] != 0, w >= 1 << 30)
+    assert bool((x[::97, d:] == 1).all())

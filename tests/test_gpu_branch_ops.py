@@ -375,3 +375,60 @@ def test_post_pre_empty_and_refused():
                  lambda: api.post_pre_rmsnorm_backward(x, x, x, w, w, dx_dtype=torch.float16)):
         with pytest.raises(ValueError):
             call()
+
+
+# -------------------------------------- more rows than the norms' rings hold --
+
+# (rows, d): 5 to 20 rows a block, more than a ring's slots (at most four), so that these
+# are filled again; the second at a shift, rows of odd length
+RINGS = [(4000, 4096), (6001, 2051), (7003, 1032)]
+
+
+@pytest.mark.parametrize("rows,d", RINGS)
+@pytest.mark.parametrize("xt,st", [(BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("kind", ["none", "channel", "token"])
+def test_post_pre_many_rows(rows, d, xt, st, kind):
+    x, r = randn(1, rows, d, dtype=xt, scale=0.5), randn(2, rows, d, dtype=st, scale=3.0)
+    w1, w2, gate = randn(3, d, dtype=F32), randn(4, d, dtype=F32), gate_of(kind, rows, d, F32)
+    s, y = api.post_pre_rmsnorm(x, r, w1, w2, gate, residual_scale=0.75, eps=1e-5)
+    s0, bound, norm = ref.post_pre(x, r, w1, w2, gate, 0.75, 1e-5, st)
+    close(s, s0, bound)
+    close(y, *norm(s))
+    dy, ds = randn(5, rows, d), randn(6, rows, d, dtype=st)
+    got = api.post_pre_rmsnorm_backward(dy, x, s, w1, w2, gate, ds, residual_scale=0.75, eps=1e-5)
+    want, bounds = ref.post_pre_backward(dy, x, s, w1, w2, gate, ds, 0.75, 1e-5)
+    for o, w, b in zip(got, want, bounds):
+        close(o, w, b + w.abs() * 1.01 * rounding(o.dtype) + 1e-30)
+    # in the places that mok.h allows, on another stream, and from a graph: the same bits
+    for target in (0, 1):
+        x2, r2 = x.clone(), r.clone()
+        if target == 0 and xt != st:
+            continue
+        s2, y2 = api.post_pre_rmsnorm(x2, r2, w1, w2, gate, residual_scale=0.75, eps=1e-5,
+                                      s=(x2, r2)[target])
+        assert s2 is (x2, r2)[target] and torch.equal(s2, s) and torch.equal(y2, y)
+    for target in (0, 1):
+        x2, dy2, ds2 = x.clone(), dy.clone(), ds.clone()
+        place = (x2, dy2)[target]
+        if place.dtype != got[0].dtype:
+            continue
+        again = api.post_pre_rmsnorm_backward(dy2, x2, s, w1, w2, gate, ds2, residual_scale=0.75,
+                                              eps=1e-5, dx=place, dresidual=ds2)
+        assert again[0] is place and again[1] is ds2
+        for a, b in zip(again, got):
+            assert a is b or torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = api.post_pre_rmsnorm(x, r, w1, w2, gate, residual_scale=0.75, eps=1e-5, stream=side)
+    other += api.post_pre_rmsnorm_backward(dy, x, other[0], w1, w2, gate, ds, residual_scale=0.75,
+                                           eps=1e-5, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = api.post_pre_rmsnorm(x, r, w1, w2, gate, residual_scale=0.75, eps=1e-5)
+        kept += api.post_pre_rmsnorm_backward(dy, x, kept[0], w1, w2, gate, ds,
+                                              residual_scale=0.75, eps=1e-5)
+    graph.replay()
+    graph.replay()
+    for a, b, c in zip(other, kept, (s, y) + tuple(got)):
+        assert (a is None and b is None) or (torch.equal(a, c) and torch.equal(b, c))

@@ -331,3 +331,21 @@ def test_grouped_long_sums_of_every_tile(sizes, cols):
         mag = b[e].to(F64).abs() @ a[r].to(F64).abs()
         for got, m in ((y, 4096), (y32, 576), (dx, 4096), (dx32, 576)):
             close(got[r], want, mag, m + n / m, got.dtype)
+
+
+RAGGED = [517, 1, 0, 700, 63, 480, 530, 16, 1033, 500, 0, 799, 401, 512, 31, 900, 640, 333, 777, 2,
+          15, 1200, 600, 257]
+
+
+@pytest.mark.parametrize("sizes", [RAGGED, [n // 2 + 3 for n in RAGGED]])
+@pytest.mark.parametrize("N,K", [(1024, 1536), (1088, 1600), (1096, 1600), (1088, 1608)])
+def test_grouped_ragged_at_training_sizes(sizes, N, K):
+    """Pairs of CTAs and wide single ones with groups' last rows below sixteen, widths
+    of whole 64-column blocks (an odd number of them: the last box passes the map's end)
+    and others."""
+    check(sizes, N, K, BF16)
+
+
+def test_grouped_lengths_of_every_remainder():
+    """Every number of last rows, between neighbours of NaN, by pairs (fp32 dx too)."""
+    check([400 + i for i in range(16)] + [800 + 3 * i for i in range(16)], 512, 256, F32)
