@@ -11,8 +11,10 @@
 // Bound by HBM bytes: a row is read once, kept on the chip across both norms'
 // reductions and written once.  Forward, 8192 x 7168, fp32 into a bf16 stream: 100 us
 // (5.9 TB/s, floor 88); backward, 16384 x 4096, fp32 x and stream: 240 us (6.1 TB/s,
-// floor 221).  Short bf16 rows in the backward are bound by issue instead: 4099 x 2880
-// 44 us (3.2 TB/s, floor 21).
+// floor 221).  Short bf16 rows in the backward wait on latency instead: 4099 x 2880 44
+// us (3.2 TB/s, floor 21), with three warps a scheduler, of which one issues in 47% of
+// the cycles (its instructions alone are 16 us), and the sums' kernel after it (10 us
+// by itself, in part under the first one's end).
 #include "post_norm.cuh"
 
 namespace mok {

@@ -270,10 +270,6 @@ cudaError_t with_types(const F& f, bool a, B... rest) {
                     rest...);
 }
 
-// How a row's elements are taken: words at any alignment by register loads, aligned
-// vectors, or aligned vectors of rows at a common shift.
-enum class Rows { kAny, kVec, kShift };
-
 // Threads of a row, blocks and ring of the ring kernels, by the descriptor and the
 // rows' kind alone (the backward's sums do not depend on the device); blocks = 0
 // where they do not serve: rows too short or too long, fewer than the ring is good
